@@ -6,12 +6,13 @@ kernels: an FP32 FFMA SGEMM and an fp16 -> fp32-accumulate tcgen05 GEMM).
 missing -- there is no fallback.  The `inputs` module (seeded synthetic data)
 does not load the library, so it can be imported on a machine without a GPU.
 """
-__all__ = ["gemm", "gemm_raw", "gemm_host", "check_device_status", "status_string", "binding",
-           "inputs"]
+_BINDING = ("gemm", "gemm_raw", "gemm_host", "check_device_status", "status_string", "Mx",
+            "mx_empty", "mx_quantize", "mx_dequantize", "mx_act_backward", "gemm_mx")
+__all__ = [*_BINDING, "binding", "inputs"]
 
 
 def __getattr__(name):
-    if name in ("gemm", "gemm_raw", "gemm_host", "check_device_status", "status_string"):
+    if name in _BINDING:
         from . import binding
         return getattr(binding, name)
     if name in ("binding", "inputs"):

@@ -30,6 +30,24 @@ _lib.gemm_host.restype = _int
 _lib.gemm_strided_batched.argtypes = [_int, _int, _i64, _i64, _i64, _int, _flt, _flt, _vp, _i64,
                                       _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp]
 _lib.gemm_strided_batched.restype = _int
+_lib.gemm_mx_row_bytes.argtypes = [_int, _i64]
+_lib.gemm_mx_row_bytes.restype = _i64
+_lib.gemm_mx_scale_bytes.argtypes = [_int, _i64, _i64]
+_lib.gemm_mx_scale_bytes.restype = _i64
+_lib.gemm_mx_quantize.argtypes = [_int, _int, _i64, _i64, _int, _flt, _vp, _i64, _int, _vp, _i64,
+                                  _vp, _i64, _vp, _vp]
+_lib.gemm_mx_quantize.restype = _int
+_lib.gemm_mx_dequantize.argtypes = [_int, _i64, _i64, _vp, _i64, _vp, _int, _vp, _i64, _vp]
+_lib.gemm_mx_dequantize.restype = _int
+_lib.gemm_mx_act_backward.argtypes = [_i64, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _vp,
+                                      _i64, _vp, _vp]
+_lib.gemm_mx_act_backward.restype = _int
+_lib.gemm_mx4.argtypes = [_int, _i64, _i64, _i64, _int, _flt, _flt, _vp, _i64, _vp, _vp, _i64,
+                          _vp, _vp, _i64, _vp, _int, _vp]
+_lib.gemm_mx4.restype = _int
+_lib.gemm_mx.argtypes = [_int, _int, _int, _i64, _i64, _i64, _int, _flt, _flt, _vp, _i64, _vp,
+                         _i64, _vp, _vp, _i64, _vp, _int, _vp]
+_lib.gemm_mx.restype = _int
 _lib.gemm_check_device_status.argtypes = [_vp]
 _lib.gemm_check_device_status.restype = _int
 _lib.gemm_status_string.argtypes = [_int]
@@ -55,7 +73,7 @@ F32_TF32 = 3
 F32_3XTF32 = 4
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_TIMEOUT = range(7)
 PATHS = {0: "none", 1: "scale", 2: "ffma", 3: "ffma_splitk", 4: "tc", 5: "tc_splitk",
-         6: "ffma_batched", 7: "tc_batched", 8: "per_entry"}
+         6: "ffma_batched", 7: "tc_batched", 8: "per_entry", 9: "mx", 10: "mx_tc"}
 
 
 class GemmError(RuntimeError):
@@ -309,6 +327,187 @@ def gemm(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=None, 
 
 
 _gemm_fn = _lib.gemm
+
+# ---------------------------------------------------------------------------
+# Microscaled operands (include/gemm.h, gemm_mx_format_t)
+# ---------------------------------------------------------------------------
+MX_FORMATS = {"fp4": 0, "fp4_e4m3": 1, "int8": 2}
+
+
+def mx_row_bytes(fmt, cols) -> int:
+    """Bytes of a row of codes (whole 16-byte units)."""
+    return _lib.gemm_mx_row_bytes(MX_FORMATS[fmt], int(cols))
+
+
+def mx_scale_bytes(fmt, rows, cols) -> int:
+    """Bytes of the scale tiles."""
+    return _lib.gemm_mx_scale_bytes(MX_FORMATS[fmt], int(rows), int(cols))
+
+
+class Mx:
+    """A matrix [rows, cols] in microscaled storage: `codes`, a 2-D uint8 CUDA
+    tensor of `rows` rows (row pitch a multiple of 16 bytes, at least
+    mx_row_bytes), and `scales`, a contiguous uint8 CUDA tensor of at least
+    mx_scale_bytes elements.  fmt: 'fp4', 'fp4_e4m3' or 'int8'."""
+    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "pitch")
+
+    def __init__(self, codes, scales, fmt, rows, cols):
+        code = MX_FORMATS.get(fmt)
+        if code is None:
+            raise ValueError(f"unknown format {fmt!r}")
+        shape, stride = codes.shape, codes.stride()
+        if not (codes.is_cuda and scales.is_cuda):
+            raise ValueError("stored operands are CUDA tensors")
+        if codes.element_size() != 1 or scales.element_size() != 1:
+            raise TypeError("codes and scales are bytes")
+        need = _lib.gemm_mx_row_bytes(code, cols)
+        if len(shape) != 2 or shape[0] != rows or shape[1] < need or \
+                (shape[1] > 1 and stride[1] != 1):
+            raise ValueError(f"codes: {rows} rows of at least {need} bytes, contiguous within a row")
+        if scales.numel() < _lib.gemm_mx_scale_bytes(code, rows, cols) or \
+                not scales.is_contiguous():
+            raise ValueError("scales: a contiguous tensor of mx_scale_bytes(fmt, rows, cols) bytes")
+        self.codes, self.scales, self.fmt, self.format = codes, scales, fmt, code
+        self.rows, self.cols = int(rows), int(cols)
+        # (a single row's pitch is not used: any valid one)
+        self.pitch = stride[0] if rows > 1 else max(need, 16)
+
+
+def mx_empty(rows, cols, fmt, device="cuda") -> Mx:
+    """Room for a stored matrix."""
+    import torch
+    if fmt not in MX_FORMATS:
+        raise ValueError(f"unknown format {fmt!r}")
+    return Mx(torch.empty((rows, mx_row_bytes(fmt, cols)), dtype=torch.uint8, device=device),
+              torch.empty(mx_scale_bytes(fmt, rows, cols), dtype=torch.uint8, device=device),
+              fmt, rows, cols)
+
+
+def _plain_code(t, what):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError("matrices are 2-D")
+    if not t.is_cuda:
+        raise ValueError(f"{what} takes CUDA tensors")
+    return code
+
+
+def _handle(stream, t):
+    return (stream.cuda_stream if stream is not None else _current_stream(t.get_device())) or None
+
+
+def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
+    """Stores mult * op(X) in Q (an Mx) and, with Y, writes Y = act(op(X)) in the
+    same pass: the forward pass of an activation whose input is checkpointed.
+    X is [rows, cols] (or [cols, rows] with transX) float32, float16 or bfloat16;
+    Y has X's dtype and shape and may be X.  Returns Q."""
+    dtype = _plain_code(X, "mx_quantize()")
+    want = (Q.cols, Q.rows) if transX else (Q.rows, Q.cols)
+    if tuple(X.shape) != want:
+        raise ValueError(f"X is {tuple(X.shape)}, expected {want}")
+    if Y is not None:
+        if Y.dtype != X.dtype or Y.shape != X.shape or not Y.is_cuda:
+            raise ValueError("Y has X's dtype and shape, on a CUDA device")
+    elif act != "none":
+        raise ValueError("act needs Y")
+    rc = _lib.gemm_mx_quantize(
+        Q.format, int(transX), Q.rows, Q.cols, dtype, float(mult), X.data_ptr() or None, _ld(X),
+        ACTS[act], (Y.data_ptr() or None) if Y is not None else None,
+        _ld(Y) if Y is not None else 0, Q.codes.data_ptr() or None, Q.pitch,
+        Q.scales.data_ptr() or None, _handle(stream, X))
+    if rc != OK:
+        raise GemmError(rc)
+    return Q
+
+
+def mx_dequantize(Q, Y, stream=None):
+    """Y = the values of Q, in Y's dtype.  Returns Y."""
+    dtype = _plain_code(Y, "mx_dequantize()")
+    if tuple(Y.shape) != (Q.rows, Q.cols):
+        raise ValueError(f"Y is {tuple(Y.shape)}, expected {(Q.rows, Q.cols)}")
+    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, Q.codes.data_ptr() or None, Q.pitch,
+                                 Q.scales.data_ptr() or None, dtype, Y.data_ptr() or None, _ld(Y),
+                                 _handle(stream, Y))
+    if rc != OK:
+        raise GemmError(rc)
+    return Y
+
+
+def mx_act_backward(dY, Q, dX, act="gelu", dbias=None, stream=None):
+    """dX = dY * act'(x) with x read from its 8-bit checkpoint Q ('int8'), and
+    dbias[j] = sum_i dX[i, j] (a contiguous float32 tensor of cols elements, or
+    None).  dX may be dY.  Returns dX."""
+    dtype = _plain_code(dY, "mx_act_backward()")
+    if Q.fmt != "int8":
+        raise TypeError("the checkpoint is an 'int8' Mx")
+    if dX.dtype != dY.dtype or not dX.is_cuda or tuple(dX.shape) != (Q.rows, Q.cols) or \
+            tuple(dY.shape) != (Q.rows, Q.cols):
+        raise ValueError(f"dY and dX: {(Q.rows, Q.cols)} CUDA tensors of one dtype")
+    if dbias is not None and (not dbias.is_cuda or dbias.numel() != Q.cols or
+                              dbias.element_size() != 4 or not dbias.is_floating_point() or
+                              not dbias.is_contiguous()):
+        raise ValueError("dbias: a contiguous float32 CUDA tensor of cols elements")
+    rc = _lib.gemm_mx_act_backward(
+        Q.rows, Q.cols, dtype, ACTS[act], dY.data_ptr() or None, _ld(dY),
+        Q.codes.data_ptr() or None, Q.pitch, Q.scales.data_ptr() or None, dX.data_ptr() or None,
+        _ld(dX), (dbias.data_ptr() or None) if dbias is not None else None, _handle(stream, dY))
+    if rc != OK:
+        raise GemmError(rc)
+    return dX
+
+
+def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=None, bias=None,
+            act="none"):
+    """The product with stored operands, in place on C; alpha, beta, bias and
+    act as gemm().
+
+    A a tensor, B an Mx: C = act(alpha * op(A) @ op(B) + beta * C + bias), B
+    stored [K, N], or [N, K] with transB; A and C share a dtype.
+    A and B Mx of the same 4-bit format, both stored along K (A [M, K], B
+    [N, K]): C = act(alpha * A @ B.T + beta * C + bias); transA and transB stay
+    False.  Returns C."""
+    dtype = _plain_code(C, "gemm_mx()")
+    M, N = C.shape
+    stored_a = isinstance(A, Mx)
+    if stored_a:
+        if transA or transB:
+            raise ValueError("two stored operands are both stored along K")
+        if A.fmt != B.fmt:
+            raise TypeError("both operands have the same format")
+        K, Kb, Ma, Nb = A.cols, B.cols, A.rows, B.rows
+    else:
+        if A.dtype != C.dtype:
+            raise TypeError("A and C must share a dtype")
+        if A.dim() != 2:
+            raise ValueError("matrices are 2-D")
+        if not A.is_cuda:
+            raise ValueError("gemm_mx() takes CUDA tensors")
+        Ma, K = (A.shape[1], A.shape[0]) if transA else (A.shape[0], A.shape[1])
+        Kb, Nb = (B.cols, B.rows) if transB else (B.rows, B.cols)
+    if K != Kb:
+        raise ValueError(f"inner dimensions differ: {K} vs {Kb}")
+    if Ma != M or Nb != N:
+        raise ValueError(f"C is {(M, N)}, expected {(Ma, Nb)}")
+    if bias is not None and (not bias.is_cuda or bias.dtype != C.dtype or bias.numel() != N or
+                             not bias.is_contiguous()):
+        raise ValueError("bias: a contiguous CUDA tensor of N elements of C's dtype")
+    bp = (bias.data_ptr() or None) if bias is not None else None
+    s = _handle(stream, C)
+    if stored_a:
+        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, float(alpha), float(beta),
+                           A.codes.data_ptr() or None, A.pitch, A.scales.data_ptr() or None,
+                           B.codes.data_ptr() or None, B.pitch, B.scales.data_ptr() or None,
+                           C.data_ptr() or None, _ld(C), bp, ACTS[act], s)
+    else:
+        rc = _lib.gemm_mx(B.format, int(transA), int(transB), M, N, K, dtype, float(alpha),
+                          float(beta), A.data_ptr() or None, _ld(A), B.codes.data_ptr() or None,
+                          B.pitch, B.scales.data_ptr() or None, C.data_ptr() or None, _ld(C), bp,
+                          ACTS[act], s)
+    if rc != OK:
+        raise GemmError(rc)
+    return C
 
 
 def gemm_host(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=None):

@@ -963,6 +963,42 @@ int run_batched(int transA, int transB, int64_t M64, int64_t N64, int64_t K64, i
 
 }  // namespace
 
+namespace gb300 {
+int api_state(ApiState* out) {
+  const int rc = device_state(&out->dev, &out->status, &out->sms);
+  out->timeout_ns = (uint64_t)g_timeout_ns.load();
+  out->fault_injection = g_fault_injection.load();
+  return rc;
+}
+cudaError_t api_scratch(void** p, size_t bytes, cudaStream_t s) {
+  cudaMemPool_t pool;
+  const cudaError_t e = scratch_pool(&pool);
+  if (e != cudaSuccess) return e;
+  return cudaMallocFromPoolAsync(p, bytes, pool, s);
+}
+void api_scratch_free(void* p, cudaStream_t s) {
+  if (p) cudaFreeAsync(p, s);
+}
+int api_done(int path, const LaunchCtx& ctx, cudaError_t e) {
+  g_total_launches += ctx.launches;
+  tl_last_grid = ctx.grid;
+  tl_last_launches = ctx.launches;
+  tl_last_path = e == cudaSuccess ? path : GEMM_PATH_NONE;
+  return e == cudaSuccess ? GEMM_OK : cuda_fail(e);
+}
+void api_add_launches(int n) { tl_last_launches += n; }
+void api_reset() {
+  tl_last_path = GEMM_PATH_NONE;
+  tl_last_launches = 0;
+}
+int api_gemm(int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype, float alpha,
+             float beta, const void* A, int64_t lda, const void* B, int64_t ldb, void* C,
+             int64_t ldc, cudaStream_t stream, Epilogue ep) {
+  return run_gemm(transA, transB, M, N, K, dtype, alpha, beta, A, lda, B, ldb, C, ldc, stream,
+                  transA ? K : M, transA ? M : K, transB ? N : K, transB ? K : N, ep);
+}
+}  // namespace gb300
+
 extern "C" {
 
 int gemm_strided_batched(int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype,

@@ -230,4 +230,81 @@ int hgemm_pair_slots(int bn, int transA, int transB, int num_sms);
 HPlan hgemm_plan(int M, int N, int K, int bn, int transA, int transB, int kstep, int batch,
                  int pair_allowed, int num_sms, int sk_mode);
 
+// ---------------------------------------------------------------- microscaled storage
+// (formats and layout: include/gemm.h; `out` is the element type of the other
+// operand or result: 0 fp32, 1 fp16, 2 bf16)
+struct MxQuantArgs {
+  int format, out, transX, rows, cols;
+  float mult;
+  const void* X;
+  int64_t ldx;
+  void* Y;  // act(X), or null (not with transX)
+  int64_t ldy;
+  int act;
+  void* q;
+  int64_t ldq;
+  void* s;
+};
+struct MxDequantArgs {
+  int format, out, rows, cols;
+  const void* q;
+  int64_t ldq;
+  const void* s;
+  void* Y;
+  int64_t ldy;
+};
+struct MxActBwdArgs {
+  int out, rows, cols, act;
+  const void* dY;
+  int64_t lddy;
+  const void* q;
+  int64_t ldq;
+  const void* s;
+  void* dX;
+  int64_t lddx;
+  float* dbias;  // column sums of dX, or null
+  float* part;   // mx_act_backward_scratch bytes when dbias is given
+};
+// C[M,N] = act(alpha * A B^T + beta * C + bias), A [M,K] and B [N,K] 4-bit
+struct Mx4Args {
+  int format, out, M, N, K;
+  const void* A;
+  int64_t lda;  // bytes
+  const void* As;
+  const void* B;
+  int64_t ldb;
+  const void* Bs;
+  void* C;
+  int64_t ldc;
+  float alpha, beta;
+  Epilogue ep;
+  int num_sms;
+  int fault_injection;
+};
+cudaError_t launch_mx_quantize(const MxQuantArgs& a, LaunchCtx& ctx);
+cudaError_t launch_mx_dequantize(const MxDequantArgs& a, LaunchCtx& ctx);
+size_t mx_act_backward_scratch(int rows, int cols);
+cudaError_t launch_mx_act_backward(const MxActBwdArgs& a, LaunchCtx& ctx);
+cudaError_t launch_mx4(const Mx4Args& a, LaunchCtx& ctx);
+
+// What the entry points of every translation unit share (gemm_api.cu).
+struct ApiState {
+  int dev, sms;
+  unsigned int* status;
+  uint64_t timeout_ns;
+  int fault_injection;
+};
+int api_state(ApiState* out);  // a gemm_status_t
+cudaError_t api_scratch(void** p, size_t bytes, cudaStream_t s);
+void api_scratch_free(void* p, cudaStream_t s);
+// records a call's path, launches and grid; returns its gemm_status_t
+int api_done(int path, const LaunchCtx& ctx, cudaError_t e);
+// adds a pre-pass's launches to the last call's count
+void api_add_launches(int n);
+void api_reset();  // no path, no launches: the state of a refused call
+// the 16- or 32-bit product behind gemm_ex() (arguments already checked)
+int api_gemm(int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype, float alpha,
+             float beta, const void* A, int64_t lda, const void* B, int64_t ldb, void* C,
+             int64_t ldc, cudaStream_t stream, Epilogue ep);
+
 }  // namespace gb300

@@ -1,0 +1,473 @@
+// Microscaled storage, the elementwise side: quantisation of a matrix (with
+// the activation of the forward pass in the same read), its inverse, and the
+// activation's backward pass from an 8-bit checkpoint.
+//
+//   scale  s_rb = scale of max over the block |mult * x|        (mx_format.cuh)
+//   code   q_rc = nearest code to mult * x_rc / s_rb, ties to even
+//   Y      y_rc = act(x_rc)
+//   dX     dx_rc = dy_rc * act'(q_rc s_rb),   dbias_c = sum_r dx_rc
+//
+// All are bound by HBM: each element is read once and written once.  A thread
+// takes 16 consecutive elements of a row (two or four 16-byte loads), four such
+// units in flight; 8 threads a row cover 128 columns, so a warp reads whole
+// 256-byte row segments, and a block of 8 warps a tile of 128 rows x 128
+// columns, whose scales are one tile of the storage (two for 16-column blocks).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx_format.cuh"
+
+namespace gb300 {
+namespace {
+
+constexpr int TILE = 128;     // rows and columns of a block's tile
+constexpr int THREADS = 256;
+
+struct QuantParams {
+  const void* X;
+  int64_t ldx;
+  int rows, cols;
+  float mult;
+  void* Y;  // act(X), or null
+  int64_t ldy;
+  int act;
+  uint8_t* q;
+  int64_t ldq;
+  uint8_t* s;
+  int64_t s_tiles;   // scale tiles of a 128-row range
+  int64_t tiles_n, tiles;
+  int vec_x, vec_y;  // 16-byte accesses allowed
+};
+
+// largest magnitude as bits: a NaN counts above infinity, infinity above all
+// numbers
+__device__ __forceinline__ uint32_t max_abs_bits(const float (&x)[16]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+template <typename T, int FMT, bool WITH_Y>
+__global__ void __launch_bounds__(THREADS) mx_quantize_kernel(const QuantParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u = lane & 7;
+  for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+    const int64_t tm = t / p.tiles_n;
+    const int64_t c0 = (t - tm * p.tiles_n) * TILE + u * 16;
+    const int n = (int)min((int64_t)16, max((int64_t)0, (int64_t)p.cols - c0));
+    const int64_t r0 = tm * TILE + warp * 16 + (lane >> 3);
+    MxRow16<T> in[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = r0 + 4 * j;
+      in[j] = mx_load16<T>(static_cast<const T*>(p.X) + r * p.ldx + c0, r < p.rows ? n : 0,
+                           p.vec_x != 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = r0 + 4 * j;
+      float x[16];
+      mx_unpack16<T>(in[j], x);
+      if (WITH_Y && r < p.rows) {
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = apply_act(x[i], p.act);
+        mx_store16<T>(static_cast<T*>(p.Y) + r * p.ldy + c0, n, p.vec_y != 0, y);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= p.mult;
+      uint32_t m = max_abs_bits(x);
+      if (mx_block(FMT) == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      const bool real = r < p.rows && n > 0;
+      uint32_t byte = mx_scale_byte<FMT>(__uint_as_float(m));
+      MxCodes<FMT> c;
+      mx_encode16<FMT>(x, byte, c);
+      // (codes of absent columns up to the row's 16-byte unit are written as 0)
+      if (r < p.rows && c0 / 16 * mx_bytes16<FMT>() < mx_row_bytes(FMT, p.cols))
+        mx_store_codes<FMT>(p.q + r * p.ldq + c0 / 16 * mx_bytes16<FMT>(), c);
+      // four blocks' scale bytes as a word; absent rows and blocks 0
+      byte = real ? byte : 0u;
+      if (mx_block(FMT) == 32) {
+        // the block's second unit may be absent while its first is not
+        byte = __shfl_sync(0xffffffffu, byte, lane & ~1);
+        uint32_t w = byte << (8 * (u >> 1));
+        w |= __shfl_xor_sync(0xffffffffu, w, 2);
+        w |= __shfl_xor_sync(0xffffffffu, w, 4);
+        const int64_t st = c0 / 128;
+        if (u == 0 && st < p.s_tiles)
+          *reinterpret_cast<uint32_t*>(p.s + mx_scale_word(r, st, p.s_tiles)) = w;
+      } else {
+        uint32_t w = byte << (8 * (u & 3));
+        w |= __shfl_xor_sync(0xffffffffu, w, 1);
+        w |= __shfl_xor_sync(0xffffffffu, w, 2);
+        const int64_t st = c0 / 64;
+        if ((u & 3) == 0 && st < p.s_tiles)
+          *reinterpret_cast<uint32_t*>(p.s + mx_scale_word(r, st, p.s_tiles)) = w;
+      }
+    }
+  }
+}
+
+// The transposed form: X is stored [cols, rows], so a block of a stored-to row
+// runs down a column of X.  A thread takes two adjacent op(X) rows (one 4- or
+// 8-byte load from each stored row, 32 of them in flight) and 32 columns;
+// codes and scale bytes go through shared memory, so that they leave in whole
+// row segments.
+constexpr int TT_ROWS = 64, TT_COLS = 128, TT_THREADS = 128;
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(TT_THREADS) mx_quantize_t_kernel(const QuantParams p) {
+  constexpr int ROW_BYTES = TT_COLS / 16 * mx_bytes16<FMT>();
+  constexpr int PITCH = ROW_BYTES + 16;  // (rows two apart in different banks)
+  constexpr int NB = TT_COLS / mx_block(FMT);
+  __shared__ __align__(16) uint8_t codes[TT_ROWS * PITCH];
+  __shared__ __align__(16) uint8_t scales[TT_ROWS * NB];
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+    const int64_t tm = t / p.tiles_n;
+    const int64_t r0 = tm * TT_ROWS, cc0 = (t - tm * p.tiles_n) * TT_COLS;
+    const int64_t r = r0 + 2 * lane;
+    const int64_t c0 = cc0 + 32 * warp;
+    const int nr = (int)min((int64_t)2, max((int64_t)0, (int64_t)p.rows - r));
+    const int nc = (int)min((int64_t)32, max((int64_t)0, (int64_t)p.cols - c0));
+    const T* src = static_cast<const T*>(p.X) + c0 * p.ldx + r;
+    struct alignas(2 * sizeof(T)) Two { T a, b; };
+    Two in[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      in[i].a = in[i].b = MxIo<T>::from(0.f);
+      if (i < nc) {
+        if (p.vec_x && nr == 2) in[i] = *reinterpret_cast<const Two*>(src + i * p.ldx);
+        else {
+          if (nr > 0) in[i].a = src[i * p.ldx];
+          if (nr > 1) in[i].b = src[i * p.ldx + 1];
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float lo[16], hi[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        lo[i] = MxIo<T>::to(h ? in[i].b : in[i].a) * p.mult;
+        hi[i] = MxIo<T>::to(h ? in[16 + i].b : in[16 + i].a) * p.mult;
+      }
+      uint32_t ml = max_abs_bits(lo), mh = max_abs_bits(hi);
+      if (mx_block(FMT) == 32) ml = mh = max(ml, mh);
+      const uint32_t bl = mx_scale_byte<FMT>(__uint_as_float(ml));
+      const uint32_t bh = mx_scale_byte<FMT>(__uint_as_float(mh));
+      MxCodes<FMT> c;
+      uint8_t* dst = codes + (2 * lane + h) * PITCH + 2 * warp * mx_bytes16<FMT>();
+      mx_encode16<FMT>(lo, bl, c);
+      mx_store_codes<FMT>(dst, c);
+      mx_encode16<FMT>(hi, bh, c);
+      mx_store_codes<FMT>(dst + mx_bytes16<FMT>(), c);
+      uint8_t* sb = scales + (2 * lane + h) * NB;
+      if (mx_block(FMT) == 32) {
+        sb[warp] = (uint8_t)(nr > h && nc > 0 ? bl : 0u);
+      } else {
+        sb[2 * warp] = (uint8_t)(nr > h && nc > 0 ? bl : 0u);
+        sb[2 * warp + 1] = (uint8_t)(nr > h && nc > 16 ? bh : 0u);
+      }
+    }
+    __syncthreads();
+    constexpr int CH = ROW_BYTES / 16;  // 16-byte chunks of a tile row
+    for (int i = threadIdx.x; i < TT_ROWS * CH; i += TT_THREADS) {
+      const int rr = i / CH, ch = i % CH;
+      const int64_t at = cc0 / 16 * mx_bytes16<FMT>() + ch * 16;
+      if (r0 + rr < p.rows && at < mx_row_bytes(FMT, p.cols))
+        *reinterpret_cast<uint4*>(p.q + (r0 + rr) * p.ldq + at) =
+            *reinterpret_cast<const uint4*>(codes + rr * PITCH + ch * 16);
+    }
+    for (int i = threadIdx.x; i < TT_ROWS * NB / 4; i += TT_THREADS) {
+      const int rr = i / (NB / 4), w = i % (NB / 4);
+      const int64_t st = cc0 / TT_COLS * (NB / 4) + w;
+      if (st < p.s_tiles)
+        *reinterpret_cast<uint32_t*>(p.s + mx_scale_word(r0 + rr, st, p.s_tiles)) =
+            *reinterpret_cast<const uint32_t*>(scales + rr * NB + 4 * w);
+    }
+    __syncthreads();
+  }
+}
+
+struct DequantParams {
+  const uint8_t* q;
+  int64_t ldq;
+  const uint8_t* s;
+  int64_t s_tiles;
+  int rows, cols;
+  void* Y;
+  int64_t ldy;
+  int64_t tiles_n, tiles;
+  int vec_y;
+};
+
+// the scale of 16-column unit starting at c0 of row r
+template <int FMT>
+__device__ __forceinline__ float unit_scale(const uint8_t* s, int64_t s_tiles, int64_t r,
+                                            int64_t c0) {
+  const int64_t b = c0 / mx_block(FMT);
+  return mx_scale_value<FMT>(s[mx_scale_word(r, b >> 2, s_tiles) + (b & 3)]);
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(THREADS) mx_dequantize_kernel(const DequantParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+    const int64_t tm = t / p.tiles_n;
+    const int64_t c0 = (t - tm * p.tiles_n) * TILE + (lane & 7) * 16;
+    const int n = (int)min((int64_t)16, (int64_t)p.cols - c0);
+    if (n <= 0) continue;
+    const int64_t r0 = tm * TILE + warp * 16 + (lane >> 3);
+    MxCodes<FMT> c[4];
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = r0 + 4 * j;
+      if (r < p.rows) {
+        c[j] = mx_load_codes<FMT>(p.q + r * p.ldq + c0 / 16 * mx_bytes16<FMT>());
+        s[j] = unit_scale<FMT>(p.s, p.s_tiles, r, c0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = r0 + 4 * j;
+      if (r >= p.rows) continue;
+      float x[16];
+      mx_decode16<FMT>(c[j], s[j], x);
+      mx_store16<T>(static_cast<T*>(p.Y) + r * p.ldy + c0, n, p.vec_y != 0, x);
+    }
+  }
+}
+
+struct ActBwdParams {
+  const void* dY;
+  int64_t lddy;
+  const uint8_t* q;
+  int64_t ldq;
+  const uint8_t* s;
+  int64_t s_tiles;
+  int rows, cols, act;
+  void* dX;
+  int64_t lddx;
+  float* part;  // [tiles_m][cols] column sums of a tile, or null
+  int64_t tiles_n, tiles;
+  int vec_in, vec_out;
+};
+
+// act'(x): relu 1 where x > 0; gelu Phi(x) + x phi(x), the derivative of
+// x Phi(x)
+__device__ __forceinline__ float act_slope(float x, int act) {
+  if (act == 1) return x > 0.f ? 1.f : 0.f;
+  if (act == 2)
+    return 0.5f * (1.f + erff(x * 0.70710678118654752f)) +
+           x * 0.39894228040143268f * expf(-0.5f * x * x);
+  return 1.f;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS) mx_act_backward_kernel(const ActBwdParams p) {
+  __shared__ float colsum[8][TILE];
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u = lane & 7;
+  for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+    const int64_t tm = t / p.tiles_n;
+    const int64_t cc0 = (t - tm * p.tiles_n) * TILE, c0 = cc0 + u * 16;
+    const int n = (int)min((int64_t)16, max((int64_t)0, (int64_t)p.cols - c0));
+    const int64_t r0 = tm * TILE + warp * 16 + (lane >> 3);
+    float sum[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+    MxRow16<T> in[4];
+    MxCodes<MX_INT8> c[4];
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = r0 + 4 * j;
+      if (r < p.rows && n > 0) {
+        in[j] = mx_load16<T>(static_cast<const T*>(p.dY) + r * p.lddy + c0, n, p.vec_in != 0);
+        c[j] = mx_load_codes<MX_INT8>(p.q + r * p.ldq + c0);
+        s[j] = unit_scale<MX_INT8>(p.s, p.s_tiles, r, c0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = r0 + 4 * j;
+      if (r >= p.rows || n <= 0) continue;
+      float dy[16], x[16];
+      mx_unpack16<T>(in[j], dy);
+      mx_decode16<MX_INT8>(c[j], s[j], x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        dy[i] *= act_slope(x[i], p.act);
+        sum[i] += i < n ? dy[i] : 0.f;
+      }
+      mx_store16<T>(static_cast<T*>(p.dX) + r * p.lddx + c0, n, p.vec_out != 0, dy);
+    }
+    if (p.part) {
+      // the warp's 16 rows, then the block's 128, in a fixed order
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
+        if (lane < 8) colsum[warp][u * 16 + i] = sum[i];
+      }
+      __syncthreads();
+      if (threadIdx.x < TILE && cc0 + threadIdx.x < p.cols) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += colsum[w][threadIdx.x];
+        p.part[tm * p.cols + cc0 + threadIdx.x] = v;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// out[c] = sum over tile rows of part[.][c], in order
+__global__ void mx_column_sum_kernel(const float* part, int64_t tiles_m, int cols, float* out) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= cols) return;
+  float v = 0.f;
+  for (int64_t t = 0; t < tiles_m; ++t) v += part[t * cols + c];
+  out[c] = v;
+}
+
+inline bool vec_ok(const void* p, int64_t ld, int64_t es) {
+  return ((uintptr_t)p % 16) == 0 && (ld * es) % 16 == 0;
+}
+inline unsigned grid_of(int64_t tiles) {
+  return (unsigned)(tiles < (1ll << 30) ? tiles : (1ll << 30));
+}
+
+template <typename T, int FMT>
+cudaError_t quantize_t(const MxQuantArgs& a, LaunchCtx& ctx) {
+  QuantParams p;
+  p.X = a.X; p.ldx = a.ldx;
+  p.rows = a.rows; p.cols = a.cols;
+  p.mult = a.mult;
+  p.Y = a.Y; p.ldy = a.ldy; p.act = a.act;
+  p.q = static_cast<uint8_t*>(a.q); p.ldq = a.ldq;
+  p.s = static_cast<uint8_t*>(a.s);
+  p.s_tiles = mx_scale_tiles(FMT, a.cols);
+  p.vec_y = a.Y && vec_ok(a.Y, a.ldy, sizeof(T));
+  const int64_t rows128 = ((int64_t)a.rows + 127) / 128;
+  cudaError_t e;
+  if (a.transX) {
+    p.vec_x = ((uintptr_t)a.X % (2 * sizeof(T))) == 0 && a.ldx % 2 == 0;
+    p.tiles_n = ((int64_t)a.cols + TT_COLS - 1) / TT_COLS;
+    p.tiles = rows128 * (128 / TT_ROWS) * p.tiles_n;
+    ctx.grid = (int)grid_of(p.tiles);
+    e = launch_kernel(mx_quantize_t_kernel<T, FMT>, dim3(ctx.grid), dim3(TT_THREADS), 0,
+                      ctx.stream, 1, p);
+  } else {
+    p.vec_x = vec_ok(a.X, a.ldx, sizeof(T));
+    p.tiles_n = ((int64_t)a.cols + TILE - 1) / TILE;
+    p.tiles = rows128 * p.tiles_n;
+    ctx.grid = (int)grid_of(p.tiles);
+    e = a.Y ? launch_kernel(mx_quantize_kernel<T, FMT, true>, dim3(ctx.grid), dim3(THREADS), 0,
+                            ctx.stream, 1, p)
+            : launch_kernel(mx_quantize_kernel<T, FMT, false>, dim3(ctx.grid), dim3(THREADS), 0,
+                            ctx.stream, 1, p);
+  }
+  if (e == cudaSuccess) ctx.launches++;
+  return e;
+}
+
+template <typename T, int FMT>
+cudaError_t dequantize_t(const MxDequantArgs& a, LaunchCtx& ctx) {
+  DequantParams p;
+  p.q = static_cast<const uint8_t*>(a.q); p.ldq = a.ldq;
+  p.s = static_cast<const uint8_t*>(a.s);
+  p.s_tiles = mx_scale_tiles(FMT, a.cols);
+  p.rows = a.rows; p.cols = a.cols;
+  p.Y = a.Y; p.ldy = a.ldy;
+  p.vec_y = vec_ok(a.Y, a.ldy, sizeof(T));
+  p.tiles_n = ((int64_t)a.cols + TILE - 1) / TILE;
+  p.tiles = ((int64_t)a.rows + TILE - 1) / TILE * p.tiles_n;
+  ctx.grid = (int)grid_of(p.tiles);
+  const cudaError_t e = launch_kernel(mx_dequantize_kernel<T, FMT>, dim3(ctx.grid),
+                                      dim3(THREADS), 0, ctx.stream, 1, p);
+  if (e == cudaSuccess) ctx.launches++;
+  return e;
+}
+
+template <typename T>
+cudaError_t act_backward_t(const MxActBwdArgs& a, LaunchCtx& ctx) {
+  ActBwdParams p;
+  p.dY = a.dY; p.lddy = a.lddy;
+  p.q = static_cast<const uint8_t*>(a.q); p.ldq = a.ldq;
+  p.s = static_cast<const uint8_t*>(a.s);
+  p.s_tiles = mx_scale_tiles(MX_INT8, a.cols);
+  p.rows = a.rows; p.cols = a.cols; p.act = a.act;
+  p.dX = a.dX; p.lddx = a.lddx;
+  p.part = a.dbias ? a.part : nullptr;
+  p.vec_in = vec_ok(a.dY, a.lddy, sizeof(T));
+  p.vec_out = vec_ok(a.dX, a.lddx, sizeof(T));
+  p.tiles_n = ((int64_t)a.cols + TILE - 1) / TILE;
+  const int64_t tiles_m = ((int64_t)a.rows + TILE - 1) / TILE;
+  p.tiles = tiles_m * p.tiles_n;
+  ctx.grid = (int)grid_of(p.tiles);
+  cudaError_t e = launch_kernel(mx_act_backward_kernel<T>, dim3(ctx.grid), dim3(THREADS), 0,
+                                ctx.stream, 1, p);
+  if (e == cudaSuccess) ctx.launches++;
+  if (e == cudaSuccess && a.dbias) {
+    e = launch_kernel(mx_column_sum_kernel, dim3((unsigned)((a.cols + 127) / 128)), dim3(128), 0,
+                      ctx.stream, 1, (const float*)a.part, tiles_m, a.cols, a.dbias);
+    if (e == cudaSuccess) ctx.launches++;
+  }
+  return e;
+}
+
+}  // namespace
+
+#define GB300_MX_TYPES(FN, FMT, ...)                                \
+  switch (a.out) {                                                  \
+    case 0: return FN<float, FMT>(__VA_ARGS__);                     \
+    case 1: return FN<__half, FMT>(__VA_ARGS__);                    \
+    case 2: return FN<__nv_bfloat16, FMT>(__VA_ARGS__);             \
+    default: return cudaErrorInvalidValue;                          \
+  }
+#define GB300_MX_FORMATS(FN, ...)                                       \
+  switch (a.format) {                                                   \
+    case MX_FP4: GB300_MX_TYPES(FN, MX_FP4, __VA_ARGS__)                \
+    case MX_FP4_E4M3: GB300_MX_TYPES(FN, MX_FP4_E4M3, __VA_ARGS__)      \
+    case MX_INT8: GB300_MX_TYPES(FN, MX_INT8, __VA_ARGS__)              \
+    default: return cudaErrorInvalidValue;                              \
+  }
+
+cudaError_t launch_mx_quantize(const MxQuantArgs& a, LaunchCtx& ctx) {
+  GB300_MX_FORMATS(quantize_t, a, ctx)
+}
+cudaError_t launch_mx_dequantize(const MxDequantArgs& a, LaunchCtx& ctx) {
+  GB300_MX_FORMATS(dequantize_t, a, ctx)
+}
+size_t mx_act_backward_scratch(int rows, int cols) {
+  return (size_t)(((int64_t)rows + TILE - 1) / TILE) * cols * sizeof(float);
+}
+cudaError_t launch_mx_act_backward(const MxActBwdArgs& a, LaunchCtx& ctx) {
+  switch (a.out) {
+    case 0: return act_backward_t<float>(a, ctx);
+    case 1: return act_backward_t<__half>(a, ctx);
+    case 2: return act_backward_t<__nv_bfloat16>(a, ctx);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace gb300

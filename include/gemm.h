@@ -238,6 +238,105 @@ int gemm_strided_batched(int transA, int transB, int64_t M, int64_t N, int64_t K
                          int64_t strideC, int64_t batch, gemm_stream_t stream);
 
 /*
+ * Microscaled operands: matrices stored in 4 or 8 bits an element with one
+ * scale for each block of consecutive columns of a row.  They are what a LoRA
+ * step keeps beside its 16-bit tensors: frozen weights in 4 bits, and the
+ * activations that its backward pass reads again in 8.
+ *
+ * A stored matrix [rows, cols] is two device buffers:
+ *   - codes: rows at a pitch of ldq BYTES, a multiple of 16 and at least
+ *     gemm_mx_row_bytes(format, cols); the base is 16-byte aligned.  Two 4-bit
+ *     codes a byte, the even column in the low half, or one signed byte a
+ *     column; bytes past the last column within that row length are zero.
+ *   - scales: gemm_mx_scale_bytes(format, rows, cols) bytes, 16-byte aligned,
+ *     one byte a block, in tiles of 128 rows x 4 blocks (512 bytes): the byte of
+ *     row r and block b lies in tile (r / 128) * ceil(blocks / 4) + b / 4, at
+ *     (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4; absent rows and blocks are
+ *     zero.
+ * A block is cut at the row's end: it may be short there.
+ *
+ * The value of a code is code * scale.  Quantising takes, for each block, the
+ * largest magnitude amax of mult * x (fp32 product), from it the scale, and the
+ * nearest code to mult * x / scale (ties to even, saturating).  A block that
+ * holds a NaN or an infinity gets a NaN scale: all of it reads as NaN.
+ */
+typedef enum {
+    GEMM_MX_FP4 = 0,      /* e2m1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and negatives), 32
+                             columns a block, scale a power of two 2^(byte - 127)
+                             (255: NaN): 2^(floor(log2 amax) - 2) */
+    GEMM_MX_FP4_E4M3 = 1, /* e2m1 codes, 16 columns a block, scale an e4m3 number
+                             (0x7F: NaN): amax / 6 rounded to nearest even, at most
+                             448.  Values far below e4m3's 2^-9 vanish: scale them up
+                             with mult and give 1 / mult to the product as alpha */
+    GEMM_MX_INT8 = 2      /* whole numbers -127 .. 127, 32 columns a block, scale
+                             2^(floor(log2 amax) - 6) */
+} gemm_mx_format_t;
+
+/* Sizes of the two buffers; -1 for an unknown format or size. */
+int64_t gemm_mx_row_bytes(int format, int64_t cols);
+int64_t gemm_mx_scale_bytes(int format, int64_t rows, int64_t cols);
+
+/*
+ * gemm_mx_quantize -- stores op(X), [rows, cols], in `format`.
+ *
+ * X: device matrix of dtype (GEMM_F32, GEMM_F16_F32ACC or GEMM_BF16_F32ACC),
+ *   [rows, cols] or, with transX, [cols, rows]; any ldx and element alignment.
+ * mult: finite; the values stored are mult * X.
+ * Y: NULL, or act(X) (without mult) is written to it in the same pass, dtype,
+ *   [rows, cols]: the forward pass of an activation whose input is kept in 8
+ *   bits.  Not with transX (GEMM_ERR_UNSUPPORTED); act without Y is an error.
+ *   Y may be X itself with the same pitch.
+ */
+int gemm_mx_quantize(int format, int transX, int64_t rows, int64_t cols, int dtype, float mult,
+                     const void* X, int64_t ldx, int act, void* Y, int64_t ldy, void* q,
+                     int64_t ldq, void* scales, gemm_stream_t stream);
+
+/* gemm_mx_dequantize -- Y = the values of a stored matrix, rounded to dtype
+ * (exact but where fp16's range ends). */
+int gemm_mx_dequantize(int format, int64_t rows, int64_t cols, const void* q, int64_t ldq,
+                       const void* scales, int dtype, void* Y, int64_t ldy, gemm_stream_t stream);
+
+/*
+ * gemm_mx_act_backward -- the backward pass of Y = act(X) from X's checkpoint
+ * in GEMM_MX_INT8:
+ *     dX = dY * act'(x8),   dbias[j] = sum_i dX[i, j]
+ * act'(x): GEMM_ACT_NONE 1; GEMM_ACT_RELU 1 where x > 0, else 0;
+ * GEMM_ACT_GELU Phi(x) + x phi(x).  dY, dX: dtype, [rows, cols]; dX may be dY
+ * itself with the same pitch.  dbias: NULL or cols fp32 sums (of the values
+ * before their rounding to dtype, in an order that does not change from call to
+ * call).  rows == 0 sets dbias to zero.
+ */
+int gemm_mx_act_backward(int64_t rows, int64_t cols, int dtype, int act, const void* dY,
+                         int64_t lddy, const void* q, int64_t ldq, const void* scales, void* dX,
+                         int64_t lddx, float* dbias, gemm_stream_t stream);
+
+/*
+ * gemm_mx4 -- product of two 4-bit operands,
+ *     C = act(alpha * A * B^T + beta * C + bias[j]),
+ * A [M, K] and B [N, K] stored in the same 4-bit format (blocks along K), C of
+ * dtype; products of codes and scales exact, fp32 accumulation.  lda, ldb in
+ * BYTES (see above), ldc in elements; bias and act as gemm_ex().
+ * GEMM_ERR_UNSUPPORTED for GEMM_MX_INT8.
+ */
+int gemm_mx4(int format, int64_t M, int64_t N, int64_t K, int dtype, float alpha, float beta,
+             const void* A, int64_t lda, const void* As, const void* B, int64_t ldb,
+             const void* Bs, void* C, int64_t ldc, const void* bias, int act,
+             gemm_stream_t stream);
+
+/*
+ * gemm_mx -- gemm_ex() with a stored right operand:
+ *     C = act(alpha * op(A) * op(B) + beta * C + bias[j]),
+ * A and C of dtype as in gemm(); B stored in `format` as [K, N] (blocks along
+ * N) or, with transB, as [N, K] (blocks along K); ldb in BYTES.  The values of
+ * B are rounded to dtype before the product (exact but where fp16's range
+ * ends).
+ */
+int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype,
+            float alpha, float beta, const void* A, int64_t lda, const void* B, int64_t ldb,
+            const void* Bs, void* C, int64_t ldc, const void* bias, int act,
+            gemm_stream_t stream);
+
+/*
  * gemm_check_device_status -- synchronises `stream`, then reads and clears
  * the current device's status word.  Returns GEMM_ERR_TIMEOUT if a kernel
  * gave up on a wait since the last check, GEMM_ERR_CUDA if the stream
@@ -268,7 +367,9 @@ typedef enum {
                                   the kernel */
     GEMM_PATH_FFMA_BATCHED = 6, /* strided batch: fp32 FFMA kernel, batch on the grid */
     GEMM_PATH_TC_BATCHED = 7,  /* strided batch: one persistent tcgen05 launch */
-    GEMM_PATH_PER_ENTRY = 8    /* strided batch run entry by entry (unaligned operands) */
+    GEMM_PATH_PER_ENTRY = 8,   /* strided batch run entry by entry (unaligned operands) */
+    GEMM_PATH_MX = 9,          /* microscaled storage: quantise, dequantise, act backward */
+    GEMM_PATH_MX_TC = 10       /* product of 4-bit operands: block-scaled tcgen05 kernel */
 } gemm_path_t;
 
 int gemm_last_path(void);
