@@ -281,6 +281,30 @@ struct Mx4Args {
   int num_sms;
   int fault_injection;
 };
+// the same for few rows M, B streamed once; A of type `out` (fp16 or bf16, 16-
+// byte aligned rows; As null) or stored in B's format (lda in bytes, As its
+// scales; then `out` is C's type alone)
+struct MxStreamArgs {
+  int format, out, M, N, K;
+  const void* A;
+  int64_t lda;
+  const void* As;
+  const void* B;
+  int64_t ldb;
+  const void* Bs;
+  void* C;
+  int64_t ldc;
+  float alpha, beta;
+  Epilogue ep;
+  int num_sms;
+  int fault_injection;
+};
+// cudaErrorNotSupported (nothing launched) where the grid or a tensor map does
+// not take the problem
+cudaError_t launch_mx_stream(const MxStreamArgs& a, LaunchCtx& ctx);
+// C[M,N] = A^T B, A [K,M] of type `out` (fp16 or bf16, 16-byte aligned rows), M
+// up to 64, B [K,N] stored in 8 bits (As unused)
+cudaError_t launch_mx_wgrad(const MxStreamArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, LaunchCtx& ctx);
 size_t mx_act_backward_scratch(int rows, int cols);

@@ -18,6 +18,10 @@ namespace {
 
 constexpr int64_t LIM = (int64_t)1 << 31;
 
+// Rows up to which a product streams its 4-bit right operand.
+constexpr int64_t WGRAD_ROWS = 64;  // (columns of A, in the tn product)
+constexpr int64_t STREAM_ROWS = 128, STREAM_ROWS_4 = 32;
+
 inline bool known_format(int f) { return f >= GEMM_MX_FP4 && f <= GEMM_MX_INT8; }
 inline bool known_type(int d) {
   return d == GEMM_F32 || d == GEMM_F16_F32ACC || d == GEMM_BF16_F32ACC;
@@ -227,6 +231,12 @@ int gemm_mx4(int format, int64_t M, int64_t N, int64_t K, int dtype, float alpha
   if (K == 0)
     return api_done(GEMM_PATH_SCALE, ctx,
                     launch_scale(dtype, (int)M, (int)N, C, ldc, beta, ctx, ep));
+  if (M <= STREAM_ROWS_4) {
+    MxStreamArgs a{format, dtype, (int)M, (int)N, (int)K, A, lda, As, B, ldb, Bs, C, ldc, alpha,
+                   beta, ep, st.sms, st.fault_injection};
+    const cudaError_t ce = launch_mx_stream(a, ctx);
+    if (ce != cudaErrorNotSupported) return api_done(GEMM_PATH_MX_STREAM, ctx, ce);
+  }
   Mx4Args a{format, dtype, (int)M, (int)N, (int)K, A, lda, As, B, ldb, Bs, C, ldc, alpha, beta,
             ep, st.sms, st.fault_injection};
   return api_done(GEMM_PATH_MX_TC, ctx, launch_mx4(a, ctx));
@@ -264,6 +274,50 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
   if (K == 0)
     return api_done(GEMM_PATH_SCALE, ctx,
                     launch_scale(dtype, (int)M, (int)N, C, ldc, beta, ctx, ep));
+  if (M <= STREAM_ROWS && transB && dtype != GEMM_F32 && format != GEMM_MX_INT8 &&
+      (!transA || M == 1)) {
+    // Few rows: B streamed once.  A's rows go through the tensor-memory-access
+    // unit: rows off 16-byte alignment (and a single row stored as a column) are
+    // copied into scratch first.
+    Scratch ws;
+    const void* Ad = A;
+    int64_t ldad = lda;
+    cudaError_t ce = cudaSuccess;
+    const bool column = transA && lda != 1;
+    if (column || ((uintptr_t)A % 16) != 0 || (lda % 8 != 0 && M > 1)) {
+      ldad = (K + 7) / 8 * 8;
+      ce = ws.get((size_t)(M * ldad * 2), stream);
+      if (ce == cudaSuccess)
+        ce = column ? launch_copy_rows(2, (int)K, 1, A, lda, ws.ptr, 1, ctx)
+                    : launch_repack_16((int)M, (int)K, A, transA ? K : lda, ws.ptr, ldad, ctx);
+      Ad = ws.ptr;
+      if (ce != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, ce);
+    }
+    if (M == 1) ldad = (K + 7) / 8 * 8;
+    MxStreamArgs a{format, dtype, (int)M, (int)N, (int)K, Ad, ldad, nullptr, B, ldb, Bs, C, ldc,
+                   alpha, beta, ep, st.sms, st.fault_injection};
+    ce = launch_mx_stream(a, ctx);
+    if (ce != cudaErrorNotSupported) return api_done(GEMM_PATH_MX_STREAM, ctx, ce);
+  }
+  if (M <= WGRAD_ROWS && transA && !transB && dtype != GEMM_F32 && format == GEMM_MX_INT8) {
+    // a low-rank adapter's gradient: the checkpoint streamed once
+    Scratch ws;
+    const void* Ad = A;
+    int64_t ldad = lda;
+    cudaError_t ce = cudaSuccess;
+    if (((uintptr_t)A % 16) != 0 || lda % 8 != 0) {
+      ldad = (M + 7) / 8 * 8;
+      ce = ws.get((size_t)(K * ldad * 2), stream);
+      if (ce == cudaSuccess)
+        ce = launch_repack_16((int)K, (int)M, A, lda, ws.ptr, ldad, ctx);
+      Ad = ws.ptr;
+      if (ce != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, ce);
+    }
+    MxStreamArgs a{format, dtype, (int)M, (int)N, (int)K, Ad, ldad, nullptr, B, ldb, Bs, C, ldc,
+                   alpha, beta, ep, st.sms, st.fault_injection};
+    ce = launch_mx_wgrad(a, ctx);
+    if (ce != cudaErrorNotSupported) return api_done(GEMM_PATH_MX_STREAM, ctx, ce);
+  }
   // B expanded to the other operand's type in scratch, then that type's product
   const int64_t ldw = (bc + 7) / 8 * 8;
   Scratch ws;

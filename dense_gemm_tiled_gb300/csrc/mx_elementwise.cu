@@ -35,7 +35,6 @@ struct QuantParams {
   float mult;
   void* Y;  // act(X), or null
   int64_t ldy;
-  int act;
   uint8_t* q;
   int64_t ldq;
   uint8_t* s;
@@ -44,8 +43,10 @@ struct QuantParams {
   int vec_x, vec_y;  // 16-byte accesses allowed
 };
 
-// largest magnitude as bits: a NaN counts above infinity, infinity above all
-// numbers
+// bits of |mult| * (a magnitude given by its bits), with a NaN's kept a NaN's
+__device__ __forceinline__ uint32_t scale_bits(uint32_t m, float mult) {
+  return __float_as_uint(__uint_as_float(m) * mult) & 0x7FFFFFFFu;
+}
 __device__ __forceinline__ uint32_t max_abs_bits(const float (&x)[16]) {
   uint32_t m = 0;
 #pragma unroll
@@ -53,7 +54,35 @@ __device__ __forceinline__ uint32_t max_abs_bits(const float (&x)[16]) {
   return m;
 }
 
-template <typename T, int FMT, bool WITH_Y>
+// Phi(x) = (1 + erf(x / sqrt 2)) / 2 and e = exp(-x^2 / 2), which the gelu and
+// its derivative share:  erfc(z) = t (a1 + t (a2 + ... )) exp(-z^2), t = 1 / (1 +
+// p z), z >= 0, within 1.5e-7 (M. Abramowitz and I. Stegun, "Handbook of
+// Mathematical Functions", 7.1.26).  One exponential, one reciprocal and about
+// ten other instructions; with erff and expf these kernels were bound by
+// arithmetic (16384 x 5632 bf16, forward and backward: 465 us).
+__device__ __forceinline__ float normal_cdf(float x, float& e) {
+  const float z = fabsf(x) * 0.70710678118654752f;
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, z, 1.f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-0.72134752044448170f * x * x));
+  float c = fmaf(t, 1.061405429f, -1.453152027f);
+  c = fmaf(t, c, 1.421413741f);
+  c = fmaf(t, c, -0.284496736f);
+  c = fmaf(t, c, 0.254829592f);
+  c = 0.5f * t * c * e;
+  return x < 0.f ? c : 1.f - c;
+}
+__device__ __forceinline__ float act_value(float x, int act) {
+  if (act == 1) return x > 0.f ? x : 0.f;
+  if (act == 2) {
+    float e;
+    return x * normal_cdf(x, e);
+  }
+  return x;
+}
+
+// ACT: the activation of Y, or -1 without Y
+template <typename T, int FMT, int ACT>
 __global__ void __launch_bounds__(THREADS) mx_quantize_kernel(const QuantParams p) {
   pdl_wait();
   pdl_trigger();
@@ -76,20 +105,24 @@ __global__ void __launch_bounds__(THREADS) mx_quantize_kernel(const QuantParams 
       const int64_t r = r0 + 4 * j;
       float x[16];
       mx_unpack16<T>(in[j], x);
-      if (WITH_Y && r < p.rows) {
+      if (ACT >= 0 && r < p.rows) {
         float y[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = apply_act(x[i], p.act);
+        for (int i = 0; i < 16; ++i) y[i] = act_value(x[i], ACT);
         mx_store16<T>(static_cast<T*>(p.Y) + r * p.ldy + c0, n, p.vec_y != 0, y);
       }
+      // (the largest of |mult x| is |mult| times the largest |x|: rounding keeps order)
+      uint32_t m = mx_max_abs16<T>(in[j]);
+      if (p.mult != 1.f) {
+        m = scale_bits(m, p.mult);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] *= p.mult;
-      uint32_t m = max_abs_bits(x);
+        for (int i = 0; i < 16; ++i) x[i] *= p.mult;
+      }
       if (mx_block(FMT) == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       const bool real = r < p.rows && n > 0;
       uint32_t byte = mx_scale_byte<FMT>(__uint_as_float(m));
       MxCodes<FMT> c;
-      mx_encode16<FMT>(x, byte, c);
+      mx_encode16<FMT>(x, byte, __uint_as_float(m), c);
       // (codes of absent columns up to the row's 16-byte unit are written as 0)
       if (r < p.rows && c0 / 16 * mx_bytes16<FMT>() < mx_row_bytes(FMT, p.cols))
         mx_store_codes<FMT>(p.q + r * p.ldq + c0 / 16 * mx_bytes16<FMT>(), c);
@@ -168,9 +201,9 @@ __global__ void __launch_bounds__(TT_THREADS) mx_quantize_t_kernel(const QuantPa
       const uint32_t bh = mx_scale_byte<FMT>(__uint_as_float(mh));
       MxCodes<FMT> c;
       uint8_t* dst = codes + (2 * lane + h) * PITCH + 2 * warp * mx_bytes16<FMT>();
-      mx_encode16<FMT>(lo, bl, c);
+      mx_encode16<FMT>(lo, bl, __uint_as_float(ml), c);
       mx_store_codes<FMT>(dst, c);
-      mx_encode16<FMT>(hi, bh, c);
+      mx_encode16<FMT>(hi, bh, __uint_as_float(mh), c);
       mx_store_codes<FMT>(dst + mx_bytes16<FMT>(), c);
       uint8_t* sb = scales + (2 * lane + h) * NB;
       if (mx_block(FMT) == 32) {
@@ -259,7 +292,7 @@ struct ActBwdParams {
   int64_t ldq;
   const uint8_t* s;
   int64_t s_tiles;
-  int rows, cols, act;
+  int rows, cols;
   void* dX;
   int64_t lddx;
   float* part;  // [tiles_m][cols] column sums of a tile, or null
@@ -269,15 +302,18 @@ struct ActBwdParams {
 
 // act'(x): relu 1 where x > 0; gelu Phi(x) + x phi(x), the derivative of
 // x Phi(x)
-__device__ __forceinline__ float act_slope(float x, int act) {
-  if (act == 1) return x > 0.f ? 1.f : 0.f;
-  if (act == 2)
-    return 0.5f * (1.f + erff(x * 0.70710678118654752f)) +
-           x * 0.39894228040143268f * expf(-0.5f * x * x);
+template <int ACT>
+__device__ __forceinline__ float act_slope(float x) {
+  if (ACT == 1) return x > 0.f ? 1.f : 0.f;
+  if (ACT == 2) {
+    float e;
+    const float c = normal_cdf(x, e);
+    return fmaf(0.39894228040143268f * x, e, c);
+  }
   return 1.f;
 }
 
-template <typename T>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(THREADS) mx_act_backward_kernel(const ActBwdParams p) {
   __shared__ float colsum[8][TILE];
   pdl_wait();
@@ -313,7 +349,7 @@ __global__ void __launch_bounds__(THREADS) mx_act_backward_kernel(const ActBwdPa
       mx_decode16<MX_INT8>(c[j], s[j], x);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        dy[i] *= act_slope(x[i], p.act);
+        dy[i] *= act_slope<ACT>(x[i]);
         sum[i] += i < n ? dy[i] : 0.f;
       }
       mx_store16<T>(static_cast<T*>(p.dX) + r * p.lddx + c0, n, p.vec_out != 0, dy);
@@ -362,7 +398,7 @@ cudaError_t quantize_t(const MxQuantArgs& a, LaunchCtx& ctx) {
   p.X = a.X; p.ldx = a.ldx;
   p.rows = a.rows; p.cols = a.cols;
   p.mult = a.mult;
-  p.Y = a.Y; p.ldy = a.ldy; p.act = a.act;
+  p.Y = a.Y; p.ldy = a.ldy;
   p.q = static_cast<uint8_t*>(a.q); p.ldq = a.ldq;
   p.s = static_cast<uint8_t*>(a.s);
   p.s_tiles = mx_scale_tiles(FMT, a.cols);
@@ -381,10 +417,11 @@ cudaError_t quantize_t(const MxQuantArgs& a, LaunchCtx& ctx) {
     p.tiles_n = ((int64_t)a.cols + TILE - 1) / TILE;
     p.tiles = rows128 * p.tiles_n;
     ctx.grid = (int)grid_of(p.tiles);
-    e = a.Y ? launch_kernel(mx_quantize_kernel<T, FMT, true>, dim3(ctx.grid), dim3(THREADS), 0,
-                            ctx.stream, 1, p)
-            : launch_kernel(mx_quantize_kernel<T, FMT, false>, dim3(ctx.grid), dim3(THREADS), 0,
-                            ctx.stream, 1, p);
+    auto kern = !a.Y         ? mx_quantize_kernel<T, FMT, -1>
+                : a.act == 2 ? mx_quantize_kernel<T, FMT, 2>
+                : a.act == 1 ? mx_quantize_kernel<T, FMT, 1>
+                             : mx_quantize_kernel<T, FMT, 0>;
+    e = launch_kernel(kern, dim3(ctx.grid), dim3(THREADS), 0, ctx.stream, 1, p);
   }
   if (e == cudaSuccess) ctx.launches++;
   return e;
@@ -415,7 +452,7 @@ cudaError_t act_backward_t(const MxActBwdArgs& a, LaunchCtx& ctx) {
   p.q = static_cast<const uint8_t*>(a.q); p.ldq = a.ldq;
   p.s = static_cast<const uint8_t*>(a.s);
   p.s_tiles = mx_scale_tiles(MX_INT8, a.cols);
-  p.rows = a.rows; p.cols = a.cols; p.act = a.act;
+  p.rows = a.rows; p.cols = a.cols;
   p.dX = a.dX; p.lddx = a.lddx;
   p.part = a.dbias ? a.part : nullptr;
   p.vec_in = vec_ok(a.dY, a.lddy, sizeof(T));
@@ -424,8 +461,11 @@ cudaError_t act_backward_t(const MxActBwdArgs& a, LaunchCtx& ctx) {
   const int64_t tiles_m = ((int64_t)a.rows + TILE - 1) / TILE;
   p.tiles = tiles_m * p.tiles_n;
   ctx.grid = (int)grid_of(p.tiles);
-  cudaError_t e = launch_kernel(mx_act_backward_kernel<T>, dim3(ctx.grid), dim3(THREADS), 0,
-                                ctx.stream, 1, p);
+  auto kern = a.act == 2   ? mx_act_backward_kernel<T, 2>
+              : a.act == 1 ? mx_act_backward_kernel<T, 1>
+                           : mx_act_backward_kernel<T, 0>;
+  cudaError_t e =
+      launch_kernel(kern, dim3(ctx.grid), dim3(THREADS), 0, ctx.stream, 1, p);
   if (e == cudaSuccess) ctx.launches++;
   if (e == cudaSuccess && a.dbias) {
     e = launch_kernel(mx_column_sum_kernel, dim3((unsigned)((a.cols + 127) / 128)), dim3(128), 0,

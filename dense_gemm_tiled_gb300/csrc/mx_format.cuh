@@ -75,26 +75,30 @@ __device__ __forceinline__ uint32_t mx_scale_byte(float amax) {
 }
 
 // ---------------------------------------------------------------- elements
-// two fp32 values -> two e2m1 codes, lo in the low half (nearest, ties to
-// even, at most 6)
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+// eight fp32 values -> eight e2m1 codes, the first in the lowest half byte
+// (nearest, ties to even, at most 6)
+__device__ __forceinline__ uint32_t e2m1_word(const float* y) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-      "cvt.u32.u8 %0, t;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return r;
 }
-// the low byte's two e2m1 codes -> two fp16 values (exact)
-__device__ __forceinline__ uint32_t e2m1_half2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.u8.u32 t, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-      : "=r"(r)
-      : "r"(byte));
-  return r;
+// a word's eight e2m1 codes -> eight fp16 values, in pairs (exact)
+__device__ __forceinline__ void e2m1_halves(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 
 // 16 elements' codes: 8 bytes of e2m1 pairs or 16 signed bytes.
@@ -104,46 +108,65 @@ struct MxCodes {
   uint32_t w[WORDS];
 };
 
-// y = x / scale, with the scale's byte already chosen from the block
+// Codes of x / scale, the scale's byte already chosen from the block; `amax`
+// the block's largest magnitude.
 template <int FMT>
-__device__ __forceinline__ void mx_encode16(const float (&x)[16], uint32_t byte,
+__device__ __forceinline__ void mx_encode16(const float (&x)[16], uint32_t byte, float amax,
                                             MxCodes<FMT>& c) {
-  float y[16];
   if constexpr (FMT == MX_FP4_E4M3) {
-    // a correctly rounded quotient: it is a tie between two codes only where
-    // x / scale is one
+    // The correctly rounded quotient (a tie between two codes only where x /
+    // scale is one) from the correctly rounded reciprocal r of the block's
+    // scale: y0 = rn(x r), y = rn(y0 + r (x - y0 s)) with the residual exact in
+    // an FMA (P. Markstein, "Computation of elementary functions on the IBM RISC
+    // System/6000 processor", 1990).  |x| is at most a few times 6 s, or 448 is
+    // s, so nothing overflows; where the residual is inexact (x below 2^-100) y
+    // is far below every code.
+    float y[16];
     const float s = e4m3_value(byte);
-    // (a scale of 0: every code 0, with its element's sign)
-    const bool some = byte != 0u && byte != 0x7Fu;
+    if (byte == 0u) {  // every code 0, with its element's sign
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      y[i] = some ? __fdiv_rn(x[i], s) : byte == 0u ? copysignf(0.f, x[i]) : 0.f;
-  } else {
-    // times 2^(127 - byte), a normal number for every byte up to 253
-    const float inv = __uint_as_float((254u - byte) << 23);
-    const bool some = byte != 255u;
+      for (int i = 0; i < 16; ++i) y[i] = copysignf(0.f, x[i]);
+    } else {
+      const float r = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = some ? x[i] * inv : 0.f;
-  }
-  if constexpr (FMT == MX_INT8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        int q = __float2int_rn(y[4 * i + j]);
-        q = q > 127 ? 127 : q < -127 ? -127 : q;
-        v |= (uint32_t)(q & 255) << (8 * j);
+      for (int i = 0; i < 16; ++i) {
+        const float y0 = __fmul_rn(x[i], r);
+        y[i] = __fmaf_rn(__fmaf_rn(-y0, s, x[i]), r, y0);
       }
-      c.w[i] = v;
     }
+    c.w[0] = e2m1_word(y);
+    c.w[1] = e2m1_word(y + 8);
+    if (byte == 0x7Fu) c.w[0] = c.w[1] = 0u;
   } else {
+    // times 2^(127 - byte), a normal number for every byte up to 253: exact
+    // (but where the product is far below every code)
+    const float inv = __uint_as_float((254u - byte) << 23);
+    if constexpr (FMT == MX_INT8) {
+      // x inv + 1.5 * 2^23 rounds to the nearest whole number (even on a tie),
+      // two's complement in the low byte; only a block whose amax lies within
+      // half a step of 128 can round to +-128, which saturates
+      constexpr float ROUND = 12582912.f;
+      const bool sat = amax * inv >= 127.5f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t v = 0;
+      for (int i = 0; i < 4; ++i) {
+        uint32_t v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v |= e2m1_pair(y[8 * i + 2 * j], y[8 * i + 2 * j + 1]) << (8 * j);
-      c.w[i] = v;
+        for (int j = 0; j < 4; ++j) {
+          float f = __fmaf_rn(x[4 * i + j], inv, ROUND);
+          if (sat) f = fminf(fmaxf(f, ROUND - 127.f), ROUND + 127.f);
+          v[j] = __float_as_uint(f);
+        }
+        c.w[i] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040),
+                             0x5410);
+        if (byte == 255u) c.w[i] = 0u;
+      }
+    } else {
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = x[i] * inv;
+      c.w[0] = e2m1_word(y);
+      c.w[1] = e2m1_word(y + 8);
+      if (byte == 255u) c.w[0] = c.w[1] = 0u;
     }
   }
 }
@@ -151,16 +174,36 @@ __device__ __forceinline__ void mx_encode16(const float (&x)[16], uint32_t byte,
 template <int FMT>
 __device__ __forceinline__ void mx_decode16(const MxCodes<FMT>& c, float scale, float (&x)[16]) {
   if constexpr (FMT == MX_INT8) {
+    // code + 128 as the low byte of 2^23 is an fp32 number: (2^23 + 128 + code)
+    // s - (2^23 + 128) s in one FMA is code * s.  (A scale above 2^103 would
+    // overflow the second product; from there on it multiplies the code.)
+    constexpr float BASE = 8388736.f;
+    const bool big = !(scale < 1.0e31f);
+    const float s = big ? 1.f : scale, off = -BASE * s;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      x[i] = (float)(int8_t)((c.w[i >> 2] >> (8 * (i & 3))) & 255u) * scale;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = c.w[i] ^ 0x80808080u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t v = __byte_perm(w, 0x4B000000u, 0x7540 + j);
+        x[4 * i + j] = __fmaf_rn(__uint_as_float(v), s, off);
+      }
+    }
+    if (big) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= scale;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t h = e2m1_half2((c.w[i >> 2] >> (8 * (i & 3))) & 255u);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      x[2 * i] = f.x * scale;
-      x[2 * i + 1] = f.y * scale;
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h[4];
+      e2m1_halves(c.w[i], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        x[8 * i + 2 * j] = f.x * scale;
+        x[8 * i + 2 * j + 1] = f.y * scale;
+      }
     }
   }
 }
@@ -206,6 +249,33 @@ __device__ __forceinline__ MxRow16<T> mx_load16(const T* p, int n, bool vec) {
     memcpy(&r, e, sizeof(r));
   }
   return r;
+}
+// Largest magnitude of 16 loaded values, as fp32 bits: a NaN counts above
+// infinity, infinity above all numbers.  16-bit types compare their magnitude's
+// bits two at a time.
+template <typename T>
+__device__ __forceinline__ uint32_t mx_max_abs16(const MxRow16<T>& r) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < MxRow16<T>::VECS; ++i)
+      m = max(max(max(m, r.v[i].x & 0x7FFFFFFFu), r.v[i].y & 0x7FFFFFFFu),
+              max(r.v[i].z & 0x7FFFFFFFu, r.v[i].w & 0x7FFFFFFFu));
+    return m;
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < MxRow16<T>::VECS; ++i) {
+      m = __vmaxu2(m, r.v[i].x & 0x7FFF7FFFu);
+      m = __vmaxu2(m, r.v[i].y & 0x7FFF7FFFu);
+      m = __vmaxu2(m, r.v[i].z & 0x7FFF7FFFu);
+      m = __vmaxu2(m, r.v[i].w & 0x7FFF7FFFu);
+    }
+    const unsigned short h = (unsigned short)max(m & 0xFFFFu, m >> 16);
+    T e;
+    memcpy(&e, &h, 2);
+    return __float_as_uint(MxIo<T>::to(e)) & 0x7FFFFFFFu;
+  }
 }
 template <typename T>
 __device__ __forceinline__ void mx_unpack16(const MxRow16<T>& r, float (&x)[16]) {

@@ -1,0 +1,429 @@
+// Products of a few rows with a large 4-bit stored operand,
+//
+//   C[m, n] = act(alpha * sum_k A[m, k] sb[n, k/b] qb[n, k] + beta * C + bias[n]),
+//
+// B stored [N, K]: one new token, or a small serving batch, through a
+// projection.  Bound by the bytes of B, each read once.
+//
+// A block takes 128 rows of B and a slice of K; the blocks of a cluster share
+// the rows and split K, so that a weight of a few dozen row ranges still keeps
+// every SM loading.  A producer warp brings 128 x 256 codes, their scale tiles
+// and the matching columns of A into a ring of stages by TMA; four warps multiply
+// 32 rows each with m16n8k16 warp MMAs, the codes as the 16-row operand.  The
+// K order within a 32-code group is the loads': lane c of a quad holds codes 8c
+// .. 8c + 7 (one word) and the same eight columns of A (one 16-byte load).
+//   Power-of-two scales are applied to the fp32 sums of a 32-code group, which
+// are exact products of codes and A; e4m3 scales to the codes, in fp16 (a 4-bit
+// significand times a 2-bit one: exact), since a group spans two of their blocks.
+// bf16 products take the codes as bf16 (exact too).
+//   The slices' fp32 sums are joined through distributed shared memory in rank
+// order, so a result does not depend on timing.  The MMA's 128 columns of the
+// tensor memory path would be 8 to 32 of 128 used here, and its operands 16-bit
+// on both sides; the warp MMAs are nowhere near a limit.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx_format.cuh"
+#include "tensor_map.h"
+
+namespace gb300 {
+namespace {
+
+constexpr int ROWS = 128;          // rows of B a block takes
+constexpr int KSTEP = 256;         // codes of K a stage holds
+constexpr int WARPS = 4;
+constexpr int ST_THREADS = 32 * (WARPS + 1);
+constexpr int MAX_RING = 5;
+constexpr int MAX_SPLIT = 8;       // blocks of a cluster (the portable limit)
+constexpr int SMEM_MAX = 227 * 1024;
+
+// A's type: fp16, bf16, or codes of B's format
+enum { X_F16 = 1, X_BF16 = 2, X_FP4 = 3 };
+
+template <int FMT, int XT, int NT>
+struct SCfg {
+  static constexpr int TPS = KSTEP / mx_block(FMT) / 4;
+  static constexpr int W_BYTES = ROWS * 128;
+  static constexpr int X_BYTES = XT == X_FP4 ? 8 * NT * 128 : 8 * NT * KSTEP * 2;
+  static constexpr int S_BYTES = TPS * 512;
+  static constexpr int XS_BYTES = XT == X_FP4 ? TPS * 512 : 0;
+  static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES + XS_BYTES;
+  static constexpr int SUMS = ROWS * 8 * NT * 4;
+  static constexpr int smem(int ring) { return ring * STAGE + SUMS + 1024 + 256; }
+  static constexpr int RING_MAX = (SMEM_MAX - SUMS - 1280) / STAGE;
+  static constexpr int RING = RING_MAX < MAX_RING ? RING_MAX : MAX_RING;
+};
+
+struct SParams {
+  int M, N, K;
+  int stages;       // K stages in all
+  int per;          // and of a block
+  int ring;
+  void* C;
+  int64_t ldc;
+  int out;          // element type of C and bias
+  float alpha, beta;
+  Epilogue ep;
+  unsigned int* status;
+  uint64_t timeout_ns;
+  int fault_injection;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_to_bf162(uint32_t h) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t h, __half2 s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h), s);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ __half2 e4m3_half2(uint32_t byte) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
+  return __half2half2(__half(h));
+}
+
+template <typename T>
+__device__ __forceinline__ void finish(const SParams& p, int m, int n, float v) {
+  T* c = static_cast<T*>(p.C) + (int64_t)m * p.ldc + n;
+  v *= p.alpha;
+  if (p.beta != 0.f) v = __fmaf_rn(p.beta, MxIo<T>::to(*c), v);
+  *c = MxIo<T>::from(apply_epilogue<T>(v, p.ep, n));
+}
+
+template <int FMT, int XT, int NT>
+__global__ void __launch_bounds__(ST_THREADS)
+    mx_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
+                     const __grid_constant__ CUtensorMap tmX,
+                     const __grid_constant__ CUtensorMap tmXS, const SParams p) {
+  using C_ = SCfg<FMT, XT, NT>;
+  constexpr int TPS = C_::TPS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t sums = base + (uint32_t)(p.ring * C_::STAGE);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(base_ptr + p.ring * C_::STAGE + C_::SUMS);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(MAX_RING + s); };
+  volatile uint32_t* const abort_flag = reinterpret_cast<uint32_t*>(bars + 2 * MAX_RING);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster is a row of the grid
+  const int n0 = (int)blockIdx.y * ROWS;
+  const int m0 = (int)blockIdx.z * 8 * NT;
+  const int k_lo = rank * p.per, k_hi = min(p.stages, k_lo + p.per);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.ring; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), WARPS);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
+
+  float acc[2][NT][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+
+  if (warp == WARPS) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, pending = 0, pend_phase = 0;
+      for (int k = k_lo; k < k_hi; ++k) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) break;
+        if (p.fault_injection == 1 && k == k_lo) {
+          if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+          continue;
+        }
+        const uint32_t w = base + (uint32_t)(stage * C_::STAGE), x = w + C_::W_BYTES;
+        const uint32_t s = x + C_::X_BYTES, xs = s + C_::S_BYTES;
+        const uint32_t bar = full_bar(stage);
+        mbar_arrive_expect_tx(bar, (uint32_t)C_::STAGE);
+        tma_load_3d(w, &tmW, k * 128, n0, 0, bar);
+        tma_load_3d(s, &tmS, 0, k * TPS, n0 >> 7, bar);
+        if constexpr (XT == X_FP4) {
+          tma_load_3d(x, &tmX, k * 128, m0, 0, bar);
+          tma_load_3d(xs, &tmXS, 0, k * TPS, m0 >> 7, bar);
+        } else {
+          // 32 columns a box: [group][row][64 bytes]
+#pragma unroll
+          for (int b = 0; b < KSTEP / 32; ++b)
+            tma_load_3d(x + (uint32_t)(b * 8 * NT * 64), &tmX, k * KSTEP + 32 * b, m0, 0, bar);
+        }
+        pending |= 1u << stage;
+        pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+      }
+      // every load issued lands before the block's shared memory is released
+      for (int s = 0; s < p.ring; ++s)
+        if (pending & (1u << s))
+          mbar_wait_drain(full_bar(s), (pend_phase >> s) & 1u, p.timeout_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ products
+    const int g = lane >> 2, c = lane & 3;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int k = k_lo; k < k_hi; ++k) {
+      bool ok = false;
+      if (lane == 0) ok = mbar_wait(full_bar(stage), phase, wc);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      const uint32_t w = base + (uint32_t)(stage * C_::STAGE), x = w + C_::W_BYTES;
+      const uint32_t s = x + C_::X_BYTES, xs = s + C_::S_BYTES;
+      // scale words of rows g, g + 8, g + 16, g + 24 of the warp's 32
+      uint32_t sw[TPS][4];
+#pragma unroll
+      for (int t = 0; t < TPS; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sw[t][i] = lds32(s + (uint32_t)(t * 512 + (g + 8 * i) * 16 + 4 * warp));
+#pragma unroll
+      for (int b = 0; b < KSTEP / 32; ++b) {
+        // B's codes: rows g + 8i, eight a lane
+        uint32_t wa[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * warp + g + 8 * i;
+          const uint32_t v = lds32(w + (uint32_t)(r * 128 + ((b ^ (r & 7)) * 16) + 4 * c));
+          e2m1_halves(v, wa[i]);
+          if constexpr (FMT == MX_FP4_E4M3) {
+            const int blk = 2 * b + (c >> 1);  // of the stage's 16
+            const __half2 sc = e4m3_half2((sw[b / 2][i] >> (8 * (blk & 3))) & 255u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wa[i][j] = half2_mul(wa[i][j], sc);
+          }
+          if constexpr (XT == X_BF16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wa[i][j] = half2_to_bf162(wa[i][j]);
+          }
+        }
+        float sc[4];
+        if constexpr (FMT == MX_FP4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[i] = e8m0_value((sw[b / 4][i] >> (8 * (b & 3))) & 255u);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t xb[4];
+          if constexpr (XT == X_FP4) {
+            const int r = 8 * j + g;
+            e2m1_halves(lds32(x + (uint32_t)(r * 128 + ((b ^ (r & 7)) * 16) + 4 * c)), xb);
+            if constexpr (FMT == MX_FP4_E4M3) {
+              const int blk = 2 * b + (c >> 1), row = (m0 & 127) + r;
+              const uint32_t word = lds32(xs + (uint32_t)((blk >> 2) * 512 + (row & 31) * 16 +
+                                                          (row >> 5) * 4));
+              const __half2 xsc = e4m3_half2((word >> (8 * (blk & 3))) & 255u);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) xb[e] = half2_mul(xb[e], xsc);
+            }
+          } else {
+            const uint4 v = lds128(x + (uint32_t)((b * 8 * NT + 8 * j + g) * 64 + 16 * c));
+            xb[0] = v.x; xb[1] = v.y; xb[2] = v.z; xb[3] = v.w;
+          }
+          float xsc[2] = {1.f, 1.f};
+          if constexpr (XT == X_FP4 && FMT == MX_FP4) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = (m0 & 127) + 8 * j + 2 * c + e;
+              const uint32_t word =
+                  lds32(xs + (uint32_t)((b >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4));
+              xsc[e] = e8m0_value((word >> (8 * (b & 3))) & 255u);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a0[4] = {wa[2 * i][0], wa[2 * i + 1][0], wa[2 * i][1], wa[2 * i + 1][1]};
+            const uint32_t a1[4] = {wa[2 * i][2], wa[2 * i + 1][2], wa[2 * i][3], wa[2 * i + 1][3]};
+            if constexpr (FMT == MX_FP4) {
+              float part[4] = {0.f, 0.f, 0.f, 0.f};
+              if constexpr (XT == X_BF16) {
+                mma_bf16(part, a0, xb[0], xb[1]);
+                mma_bf16(part, a1, xb[2], xb[3]);
+              } else {
+                mma_f16(part, a0, xb[0], xb[1]);
+                mma_f16(part, a1, xb[2], xb[3]);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float v = part[e];
+                if constexpr (XT == X_FP4) v *= xsc[e & 1];
+                acc[i][j][e] = __fmaf_rn(v, sc[2 * i + (e >> 1)], acc[i][j][e]);
+              }
+            } else {
+              if constexpr (XT == X_BF16) {
+                mma_bf16(acc[i][j], a0, xb[0], xb[1]);
+                mma_bf16(acc[i][j], a1, xb[2], xb[3]);
+              } else {
+                mma_f16(acc[i][j], a0, xb[0], xb[1]);
+                mma_f16(acc[i][j], a1, xb[2], xb[3]);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(stage));
+      if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+    }
+    // this block's sums: [row of C][row of B]
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = 32 * warp + 16 * i + g + 8 * (e >> 1), m = 8 * j + 2 * c + (e & 1);
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + (uint32_t)((m * ROWS + n) * 4)),
+                       "f"(acc[i][j][e]));
+        }
+  }
+  // ------------------------------------------------------------ join
+  // (a block alone is a cluster of one: the barriers then are the block's)
+  cluster_sync();
+  const int share = (ROWS + splits - 1) / splits;
+  const int n_lo = rank * share, n_cnt = min(ROWS, n_lo + share) - n_lo;
+  const int mc = min(8 * NT, p.M - m0);
+  for (int i = threadIdx.x; i < n_cnt * mc; i += ST_THREADS) {
+    const int m = i / n_cnt, n = n_lo + i % n_cnt;
+    if (n0 + n >= p.N) continue;
+    float v = 0.f;
+    const uint32_t mine = sums + (uint32_t)((m * ROWS + n) * 4);
+    for (int r = 0; r < splits; ++r) {
+      float f;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(mapa_shared(mine, (uint32_t)r)));
+      v += f;
+    }
+    if (p.out == 0) finish<float>(p, m0 + m, n0 + n, v);
+    else if (p.out == 1) finish<__half>(p, m0 + m, n0 + n, v);
+    else finish<__nv_bfloat16>(p, m0 + m, n0 + n, v);
+  }
+  cluster_sync();  // no block leaves while another reads its sums
+}
+
+// ---------------------------------------------------------------- host side
+template <int FMT, int XT, int NT>
+cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
+  using C_ = SCfg<FMT, XT, NT>;
+  auto kern = mx_stream_kernel<FMT, XT, NT>;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::smem(C_::RING));
+  if (attr != cudaSuccess) return attr;
+  SParams p;
+  p.M = a.M; p.N = a.N; p.K = a.K;
+  p.stages = (a.K + KSTEP - 1) / KSTEP;
+  const int64_t rb = ((int64_t)a.N + ROWS - 1) / ROWS;
+  const int64_t mg = ((int64_t)a.M + 8 * NT - 1) / (8 * NT);
+  if (rb > 65535 || mg > 65535) return cudaErrorNotSupported;
+  // The most slices of K whose blocks are all resident at once (a slice's
+  // stages, up to the ring, are its block's loads in flight); one where even
+  // that is more than the GPU holds.
+  int splits = 1;
+  p.per = p.stages;
+  for (int s = MAX_SPLIT; s > 1; --s) {
+    const int per = (p.stages + s - 1) / s, n = (p.stages + per - 1) / per;
+    const int ring = per < C_::RING ? per : C_::RING;
+    const int64_t slots = (int64_t)a.num_sms * (SMEM_MAX / (C_::smem(ring) + 1024));
+    if (rb * mg * n <= slots) {
+      splits = n;
+      p.per = per;
+      break;
+    }
+  }
+  p.ring = p.per < C_::RING ? p.per : C_::RING;
+  p.C = a.C; p.ldc = a.ldc; p.out = a.out;
+  p.alpha = a.alpha; p.beta = a.beta;
+  p.ep = a.ep;
+  p.status = ctx.status;
+  p.timeout_ns = ctx.timeout_ns;
+  p.fault_injection = a.fault_injection;
+  const int64_t kbytes = ((int64_t)a.K + 1) / 2;
+  const int64_t tiles = mx_scale_tiles(FMT, a.K);
+  CUtensorMap mW, mS, mX, mXS;
+  memset(&mXS, 0, sizeof(mXS));
+  const CUtensorMapDataType U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  auto scales = [&](CUtensorMap* m, const void* s, int64_t rows) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, s, tiles, 128, 128, 128, C_::TPS,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, (rows + 127) / 128, tiles * 128, 4);
+  };
+  bool ok = make_map(&mW, U8, a.B, a.N, kbytes, a.ldb, 128, ROWS, CU_TENSOR_MAP_SWIZZLE_128B, 1, 0, 1) &&
+            scales(&mS, a.Bs, a.N);
+  if constexpr (XT == X_FP4)
+    ok = ok && make_map(&mX, U8, a.A, a.M, kbytes, a.lda, 128, 8 * NT, CU_TENSOR_MAP_SWIZZLE_128B, 1, 0, 1) &&
+         scales(&mXS, a.As, a.M);
+  else
+    ok = ok && make_map(&mX, XT == X_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        a.A, a.M, a.K, a.lda, 32, 8 * NT, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (!ok) return cudaErrorNotSupported;
+  ctx.grid = (int)(splits * rb * mg);
+  const cudaError_t e =
+      launch_kernel(kern, dim3((unsigned)splits, (unsigned)rb, (unsigned)mg), dim3(ST_THREADS),
+                    (size_t)C_::smem(p.ring), ctx.stream, splits, mW, mS, mX, mXS, p);
+  if (e == cudaSuccess) ctx.launches++;
+  return e;
+}
+
+template <int FMT, int XT>
+cudaError_t launch_stream_nt(const MxStreamArgs& a, LaunchCtx& ctx) {
+  if (a.M <= 8) return launch_stream<FMT, XT, 1>(a, ctx);
+  if (a.M <= 16) return launch_stream<FMT, XT, 2>(a, ctx);
+  return launch_stream<FMT, XT, 4>(a, ctx);
+}
+template <int FMT>
+cudaError_t launch_stream_x(const MxStreamArgs& a, LaunchCtx& ctx) {
+  if (a.As) return launch_stream_nt<FMT, X_FP4>(a, ctx);
+  if (a.out == 1) return launch_stream_nt<FMT, X_F16>(a, ctx);
+  return launch_stream_nt<FMT, X_BF16>(a, ctx);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
+  return a.format == MX_FP4 ? launch_stream_x<MX_FP4>(a, ctx)
+                            : launch_stream_x<MX_FP4_E4M3>(a, ctx);
+}
+
+}  // namespace gb300

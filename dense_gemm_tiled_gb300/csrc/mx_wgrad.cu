@@ -1,0 +1,376 @@
+// Gradient of a low-rank adapter from an 8-bit checkpoint,
+//
+//   C[m, n] = act(alpha * sum_t A[t, m] s[t, n/32] q[t, n] + beta * C + bias[n]),
+//
+// A [T, M] fp16 or bf16 with M up to 64 columns, q the checkpoint of the
+// layer's input, [T, N] (the tn product of "Metal GEMM Kernels for LoRA Training
+// on Apple Silicon", section 5, with its right operand stored in 8 bits).
+// Bound by the bytes of the checkpoint, each read once.
+//
+// A block takes 128 columns of the checkpoint and a slice of T; a cluster's
+// blocks share the columns and split T.  A producer warp brings 64 rows of q (128-
+// byte swizzle), their scale tile and the same rows of A into a ring by TMA.
+// Four warps: two halves of the columns, two halves of each stage's rows.  The
+// warp MMA (m16n8k16) wants pairs of t for one column: a lane reads 8 bytes of
+// four rows and interleaves them with byte permutes, so one pass makes the
+// operands of eight 8-column tiles (column 8g + j of the half in tile j).  A
+// comes through ldmatrix.trans.
+//   A code becomes fp16 by putting its byte into 1024's fraction (1024 + q + 128,
+// exact) and taking 1152 away; the scale, a power of two within fp16's normal
+// range, multiplies it exactly.  Other scales, and bf16, go through fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx_format.cuh"
+#include "tensor_map.h"
+
+namespace gb300 {
+namespace {
+
+constexpr int COLS = 128;   // columns of the checkpoint a block takes
+constexpr int TSTEP = 64;   // rows of it a stage holds
+constexpr int WG_WARPS = 4;
+constexpr int WG_THREADS = 32 * (WG_WARPS + 1);
+constexpr int WG_RING = 6;
+constexpr int WG_SPLIT = 8;
+constexpr int WG_SMEM_MAX = 227 * 1024;
+
+template <int MT>
+struct GCfg {
+  static constexpr int Q_BYTES = TSTEP * 128;
+  static constexpr int A_BYTES = TSTEP * 32 * MT;
+  static constexpr int S_BYTES = 1024;  // one 512-byte tile, its slot a swizzle period
+  static constexpr int STAGE = Q_BYTES + A_BYTES + S_BYTES;
+  static constexpr uint32_t TX = Q_BYTES + A_BYTES + 512;
+  static constexpr int SUMS = 16 * MT * COLS * 4;
+  static constexpr int smem(int ring) { return ring * STAGE + SUMS + 1024 + 256; }
+};
+
+struct GParams {
+  int M, N, K;
+  int stages, per, ring;
+  void* C;
+  int64_t ldc;
+  float alpha, beta;
+  Epilogue ep;
+  unsigned int* status;
+  uint64_t timeout_ns;
+  int fault_injection;
+};
+
+template <typename T>
+__device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                       uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// Pairs (row 0, row 1) of eight columns' values as 16-bit operands: w0, w1 the
+// two rows' codes (each offset by 128), b0, b1 their scale bytes.
+template <typename T>
+__device__ __forceinline__ void code_pairs(uint2 w0, uint2 w1, uint32_t b0, uint32_t b1,
+                                           uint32_t (&out)[8]) {
+  const uint32_t a[2] = {w0.x, w0.y}, b[2] = {w1.x, w1.y};
+  // both scales normal fp16 numbers: 2^-14 .. 2^15
+  const bool fast = std::is_same<T, __half>::value && b0 - 113u < 30u && b1 - 113u < 30u;
+  if (fast) {
+    const uint32_t sbits = ((b0 - 112u) << 10) | ((b1 - 112u) << 26);
+    const __half2 s = *reinterpret_cast<const __half2*>(&sbits);
+    const __half2 off = __float2half2_rn(-1152.f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t lo = __byte_perm(a[h], b[h], 0x5140), hi = __byte_perm(a[h], b[h], 0x7362);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t v = __byte_perm(j < 2 ? lo : hi, 0x64646464u, (j & 1) ? 0x4342 : 0x4140);
+        const __half2 x = __hmul2(__hadd2(*reinterpret_cast<const __half2*>(&v), off), s);
+        out[4 * h + j] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
+  } else {
+    // code + 128 in the fraction of 2^23, less 2^23 + 128: the code; times its
+    // scale: exact in fp32 and, within its range, in the 16-bit type
+    const float s0 = e8m0_value(b0), s1 = e8m0_value(b1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = __uint_as_float(__byte_perm(a[h], 0x4B000000u, 0x7540 + j)) - 8388736.f;
+        const float y = __uint_as_float(__byte_perm(b[h], 0x4B000000u, 0x7540 + j)) - 8388736.f;
+        out[4 * h + j] = pack2<T>(x * s0, y * s1);
+      }
+  }
+}
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(WG_THREADS)
+    mx_wgrad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmS,
+                    const __grid_constant__ CUtensorMap tmA, const GParams p) {
+  using C_ = GCfg<MT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t sums = base + (uint32_t)(p.ring * C_::STAGE);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(base_ptr + p.ring * C_::STAGE + C_::SUMS);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(WG_RING + s); };
+  volatile uint32_t* const abort_flag = reinterpret_cast<uint32_t*>(bars + 2 * WG_RING);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = (int)gridDim.x, rank = (int)blockIdx.x;
+  const int n0 = (int)blockIdx.y * COLS;
+  const int k_lo = rank * p.per, k_hi = min(p.stages, k_lo + p.per);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.ring; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), WG_WARPS);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
+
+  float acc[MT][8][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+  const int g = lane >> 2, c = lane & 3;
+  const int half = warp & 1, part = warp >> 1;  // columns 64 half .. +63; steps 2 part, 2 part + 1
+
+  if (warp == WG_WARPS) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, pending = 0, pend_phase = 0;
+      for (int k = k_lo; k < k_hi; ++k) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) break;
+        if (p.fault_injection == 1 && k == k_lo) {
+          if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+          continue;
+        }
+        const uint32_t q = base + (uint32_t)(stage * C_::STAGE), a = q + C_::Q_BYTES;
+        const uint32_t bar = full_bar(stage);
+        mbar_arrive_expect_tx(bar, C_::TX);
+        tma_load_3d(q, &tmQ, n0, k * TSTEP, 0, bar);
+        tma_load_3d(a, &tmA, 0, k * TSTEP, 0, bar);
+        tma_load_3d(a + C_::A_BYTES, &tmS, 0, (int)blockIdx.y, (k * TSTEP) >> 7, bar);
+        pending |= 1u << stage;
+        pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+      }
+      for (int s = 0; s < p.ring; ++s)
+        if (pending & (1u << s))
+          mbar_wait_drain(full_bar(s), (pend_phase >> s) & 1u, p.timeout_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ products
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int k = k_lo; k < k_hi; ++k) {
+      bool ok = false;
+      if (lane == 0) ok = mbar_wait(full_bar(stage), phase, wc);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      const uint32_t q = base + (uint32_t)(stage * C_::STAGE), a = q + C_::Q_BYTES;
+      const uint32_t s = a + C_::A_BYTES + (uint32_t)(2 * half + (g >> 2));
+      const int t_in = (k * TSTEP) & 127;  // the stage's place in its scale tile
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const int t0 = (2 * part + kk) * 16;  // rows t0 .. t0 + 15 of the stage
+        uint32_t am[MT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          // 8 x 8 blocks (rows t, columns m): t half by lane bit 4, m half by bit 3
+          const int t = t0 + (lane & 7) + ((lane >> 4) << 3);
+          const int ch = 2 * i + ((lane >> 3) & 1);  // 16-byte chunk of A's row
+          // (the swizzle of a row of 32 MT bytes)
+          const int sw = MT == 4 ? (t & 7) : MT == 2 ? ((t >> 1) & 3) : ((t >> 2) & 1);
+          ldmatrix_x4_trans(a + (uint32_t)(t * 32 * MT + ((ch ^ sw) * 16)), am[i]);
+        }
+        uint2 w[4];
+        uint32_t sb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = t0 + 2 * c + (i & 1) + 8 * (i >> 1);
+          const int ch = 4 * half + (g >> 1);
+          w[i] = lds64(q + (uint32_t)(t * 128 + ((ch ^ (t & 7)) * 16) + 8 * (g & 1)));
+          w[i].x ^= 0x80808080u;
+          w[i].y ^= 0x80808080u;
+          const int ts = t_in + t;
+          sb[i] = lds8(s + (uint32_t)((ts & 31) * 16 + (ts >> 5) * 4));
+        }
+        uint32_t lo[8], hi[8];
+        code_pairs<T>(w[0], w[1], sb[0], sb[1], lo);
+        code_pairs<T>(w[2], w[3], sb[2], sb[3], hi);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) mma_16<T>(acc[i][j], am[i], lo[j], hi[j]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(stage));
+      if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+    }
+  }
+  // ------------------------------------------------------------ join
+  // the two row halves' sums, then the slices' (the tile's element (i, j, e) is
+  // row 16 i + g + 8 (e / 2), column 64 half + 8 (2 c + e % 2) + j)
+  for (int turn = 1; turn >= 0; --turn) {
+    if (warp < WG_WARPS && part == turn) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int m = 16 * i + g + 8 * (e >> 1), n = 64 * half + 8 * (2 * c + (e & 1)) + j;
+            const uint32_t at = sums + (uint32_t)((m * COLS + n) * 4);
+            float v = acc[i][j][e];
+            if (turn == 0) {
+              float o;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(o) : "r"(at));
+              v += o;
+            }
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v));
+          }
+    }
+    if (turn == 1) __syncthreads();
+  }
+  cluster_sync();
+  const int share = (COLS + splits - 1) / splits;
+  const int n_lo = rank * share, n_cnt = min(COLS, n_lo + share) - n_lo;
+  for (int i = threadIdx.x; i < n_cnt * p.M; i += WG_THREADS) {
+    const int m = i / n_cnt, n = n_lo + i % n_cnt;
+    if (n0 + n >= p.N) continue;
+    const uint32_t mine = sums + (uint32_t)((m * COLS + n) * 4);
+    float v = 0.f;
+    for (int r = 0; r < splits; ++r) {
+      float f;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(mapa_shared(mine, (uint32_t)r)));
+      v += f;
+    }
+    T* dst = static_cast<T*>(p.C) + (int64_t)m * p.ldc + n0 + n;
+    v *= p.alpha;
+    if (p.beta != 0.f) v = __fmaf_rn(p.beta, MxIo<T>::to(*dst), v);
+    *dst = MxIo<T>::from(apply_epilogue<T>(v, p.ep, n0 + n));
+  }
+  cluster_sync();
+}
+
+template <typename T, int MT>
+cudaError_t launch_wgrad(const MxStreamArgs& a, LaunchCtx& ctx) {
+  using C_ = GCfg<MT>;
+  auto kern = mx_wgrad_kernel<T, MT>;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::smem(WG_RING));
+  if (attr != cudaSuccess) return attr;
+  GParams p;
+  p.M = a.M; p.N = a.N; p.K = a.K;
+  p.stages = (a.K + TSTEP - 1) / TSTEP;
+  const int64_t cb = ((int64_t)a.N + COLS - 1) / COLS;
+  if (cb > 65535) return cudaErrorNotSupported;
+  // the most slices of T whose blocks are all resident at once
+  int splits = 1;
+  p.per = p.stages;
+  for (int s = WG_SPLIT; s > 1; --s) {
+    const int per = (p.stages + s - 1) / s, n = (p.stages + per - 1) / per;
+    const int ring = per < WG_RING ? per : WG_RING;
+    const int64_t slots = (int64_t)a.num_sms * (WG_SMEM_MAX / (C_::smem(ring) + 1024));
+    if (cb * n <= slots) {
+      splits = n;
+      p.per = per;
+      break;
+    }
+  }
+  p.ring = p.per < WG_RING ? p.per : WG_RING;
+  p.C = a.C; p.ldc = a.ldc;
+  p.alpha = a.alpha; p.beta = a.beta;
+  p.ep = a.ep;
+  p.status = ctx.status;
+  p.timeout_ns = ctx.timeout_ns;
+  p.fault_injection = a.fault_injection;
+  const int64_t tiles = mx_scale_tiles(MX_INT8, a.N);
+  CUtensorMap mQ, mS, mA;
+  const CUtensorMapSwizzle sw = MT == 4   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : MT == 2 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                          : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUtensorMapDataType ty = std::is_same<T, __half>::value
+                                     ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!make_map(&mQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, a.K, a.N, a.ldb, 128, TSTEP,
+                CU_TENSOR_MAP_SWIZZLE_128B, 1, 0, 1) ||
+      !make_map(&mS, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.Bs, tiles, 128, 128, 128, 1,
+                CU_TENSOR_MAP_SWIZZLE_NONE, ((int64_t)a.K + 127) / 128, tiles * 128, 4) ||
+      !make_map(&mA, ty, a.A, a.K, a.M, a.lda, 16 * MT, TSTEP, sw))
+    return cudaErrorNotSupported;
+  ctx.grid = (int)(splits * cb);
+  const cudaError_t e = launch_kernel(kern, dim3((unsigned)splits, (unsigned)cb), dim3(WG_THREADS),
+                                      (size_t)C_::smem(p.ring), ctx.stream, splits, mQ, mS, mA, p);
+  if (e == cudaSuccess) ctx.launches++;
+  return e;
+}
+
+template <typename T>
+cudaError_t launch_wgrad_t(const MxStreamArgs& a, LaunchCtx& ctx) {
+  if (a.M <= 16) return launch_wgrad<T, 1>(a, ctx);
+  if (a.M <= 32) return launch_wgrad<T, 2>(a, ctx);
+  return launch_wgrad<T, 4>(a, ctx);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_wgrad(const MxStreamArgs& a, LaunchCtx& ctx) {
+  return a.out == 1 ? launch_wgrad_t<__half>(a, ctx) : launch_wgrad_t<__nv_bfloat16>(a, ctx);
+}
+
+}  // namespace gb300

@@ -369,7 +369,8 @@ typedef enum {
     GEMM_PATH_TC_BATCHED = 7,  /* strided batch: one persistent tcgen05 launch */
     GEMM_PATH_PER_ENTRY = 8,   /* strided batch run entry by entry (unaligned operands) */
     GEMM_PATH_MX = 9,          /* microscaled storage: quantise, dequantise, act backward */
-    GEMM_PATH_MX_TC = 10       /* product of 4-bit operands: block-scaled tcgen05 kernel */
+    GEMM_PATH_MX_TC = 10,      /* product of 4-bit operands: block-scaled tcgen05 kernel */
+    GEMM_PATH_MX_STREAM = 11   /* few rows times a stored right operand, read once */
 } gemm_path_t;
 
 int gemm_last_path(void);

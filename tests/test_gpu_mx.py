@@ -326,3 +326,85 @@ def test_other_stream_and_graph(g):
     torch.cuda.synchronize()
     for t, e in zip(outs, eager):
         assert torch.equal(t, e)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt,variant,M,N,K", [
+    ("fp4", "nt", 1, 300, 20000), ("fp4", "nt", 13, 200, 20001), ("fp4_e4m3", "nt", 32, 130, 17000),
+    ("fp4_e4m3", "nt", 5, 20000, 300), ("int8", "tn", 32, 200, 20000), ("int8", "tn", 7, 130, 20001),
+    ("int8", "tn", 64, 9000, 300), ("int8", "tn", 16, 70, 9000)])
+def test_few_rows_long_sums(g, dtype, fmt, variant, M, N, K):
+    """The streaming kernels past one fill of their rings and one cluster."""
+    tA, tB = variant[0] == "t", variant[1] == "t"
+    r = np.random.default_rng(300 + M)
+    A = matrix(K if tA else M, M if tA else K, dtype, 61)
+    B, b = stored(g, (r.standard_normal((N, K) if tB else (K, N)) * 0.05).astype(np.float32), fmt)
+    a = f64(A)
+    a, b = (a.T if tA else a), (b.T if tB else b)
+    C = torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda")
+    g.gemm_mx(A, B, C, transA=tA, transB=tB)
+    assert g.last_path() == "mx_stream"
+    check_product(C, a, b, dtype)
+    first = C.clone()
+    g.gemm_mx(A, B, C, transA=tA, transB=tB)
+    assert torch.equal(C, first)
+
+
+@pytest.mark.parametrize("fmt", FP4)
+def test_few_rows_of_two_stored_operands(g, fmt):
+    for M, N, K in [(1, 5000, 700), (9, 300, 9001), (32, 200, 12000), (17, 129, 31)]:
+        r = np.random.default_rng(400 + M)
+        A, a = stored(g, r.standard_normal((M, K)).astype(np.float32), fmt)
+        B, b = stored(g, (r.standard_normal((N, K)) * 0.05).astype(np.float32), fmt)
+        C = torch.full((M, N), float("nan"), device="cuda")
+        g.gemm_mx(A, B, C)
+        assert g.last_path() == "mx_stream"
+        check_product(C, a, b.T, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_wgrad_scales_past_fp16(g, dtype):
+    """Checkpoint rows whose power of two is no normal fp16 number, beside
+    ordinary ones; their products are far below or within fp32's range."""
+    r = np.random.default_rng(9)
+    x = r.standard_normal((200, 140)).astype(np.float32)
+    x[3] *= 2.0 ** -17
+    x[70] *= 2.0 ** -12
+    x[71, :32] = 0.0
+    if dtype == "bf16":
+        x[5] *= 2.0 ** 40
+        x[6] *= 2.0 ** -40
+    B, b = stored(g, x, "int8")
+    A = matrix(200, 24, dtype, 3)
+    C = torch.empty((24, 140), dtype=DT[dtype], device="cuda")
+    g.gemm_mx(A, B, C, transA=True)
+    assert g.last_path() == "mx_stream"
+    check_product(C, f64(A).T, b, dtype)
+
+
+@pytest.mark.parametrize("case", ["mx4", "stream", "wgrad"])
+def test_bounded_waits(lib_path, gpu, case):
+    """A load that never comes ends as a status, not as a hang (the library's own
+    test hook: the producer leaves out its first load)."""
+    from dense_gemm_tiled_gb300 import binding as g
+    r = np.random.default_rng(1)
+    B, _ = stored(g, r.standard_normal((256, 512)).astype(np.float32), "int8" if case == "wgrad" else "fp4")
+    M = 200 if case == "mx4" else 8
+    A = stored(g, r.standard_normal((M, 512)).astype(np.float32), "fp4")[0] if case == "mx4" else \
+        matrix(*((256, 8) if case == "wgrad" else (8, 512)), "f16", 1)
+    C = torch.empty((M, 512 if case == "wgrad" else 256), dtype=torch.float16, device="cuda")
+    call = lambda: g.gemm_mx(A, B, C, transA=case == "wgrad", transB=case == "stream")  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    want = C.clone()
+    g.set_wait_timeout_ns(20_000_000)
+    g.set_fault_injection(1)
+    try:
+        call()
+        assert g.check_device_status() == g.ERR_TIMEOUT
+    finally:
+        g.set_fault_injection(0)
+        g.set_wait_timeout_ns(0)
+    call()
+    assert g.check_device_status() == g.OK
+    assert torch.equal(C, want)
