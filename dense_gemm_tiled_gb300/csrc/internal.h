@@ -244,6 +244,7 @@ struct MxQuantArgs {
   void* q;
   int64_t ldq;
   void* s;
+  int num_sms;
 };
 struct MxDequantArgs {
   int format, out, rows, cols;
@@ -252,6 +253,7 @@ struct MxDequantArgs {
   const void* s;
   void* Y;
   int64_t ldy;
+  int num_sms;
 };
 struct MxActBwdArgs {
   int out, rows, cols, act;
@@ -264,6 +266,7 @@ struct MxActBwdArgs {
   int64_t lddx;
   float* dbias;  // column sums of dX, or null
   float* part;   // mx_act_backward_scratch bytes when dbias is given
+  int num_sms;
 };
 // C[M,N] = act(alpha * A B^T + beta * C + bias), A [M,K] and B [N,K] 4-bit
 struct Mx4Args {
@@ -307,7 +310,7 @@ cudaError_t launch_mx_stream(const MxStreamArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_wgrad(const MxStreamArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, LaunchCtx& ctx);
-size_t mx_act_backward_scratch(int rows, int cols);
+size_t mx_act_backward_scratch(int rows, int cols, int num_sms);  // (0: none needed)
 cudaError_t launch_mx_act_backward(const MxActBwdArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx4(const Mx4Args& a, LaunchCtx& ctx);
 

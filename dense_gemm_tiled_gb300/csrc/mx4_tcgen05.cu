@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "hgemm_tcgen05.cuh"
@@ -36,24 +37,28 @@ namespace {
 
 constexpr int KSTAGE = 256;   // codes of K a stage holds: one 128-byte swizzle row
 constexpr int KMMA = 64;      // codes of K an MMA takes
-constexpr int EPI = 4;        // epilogue warps
+constexpr int EPI = 8;        // epilogue warps: two per lane quarter, half of the columns each
 constexpr int MX_THREADS = 64 + 32 * EPI;
 
 template <int FMT, int BN, bool PAIR>
 struct MxCfg {
   static constexpr int TPS = KSTAGE / mx_block(FMT) / 4;  // scale tiles of a stage and 128 rows
   static constexpr int NBLK = (BN + 127) / 128;           // 128-row ranges of B
+  static constexpr int HALVES = BN >= 128 ? 2 : 1;        // epilogue warps in use per quarter
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = (PAIR ? BN / 2 : BN) * 128;
   static constexpr int SFA_BYTES = TPS * 512;
   static constexpr int SFB_BYTES = NBLK * TPS * 512;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;
-  static constexpr int STAGING_BYTES = EPI * 2 * 4096;
+  static constexpr int STAGING_BYTES = 4 * HALVES * 4096;
   static constexpr int FIXED = 1024 + 512;
   static constexpr int RAW = (SMEM_LIMIT - FIXED - STAGING_BYTES) / (STAGE_BYTES + SF_BYTES);
   static constexpr int SF_COLS = TPS * 4 * (1 + NBLK);    // tensor-memory columns of a stage
-  static constexpr int NACC = 2;
+  // Accumulators: two, so that a tile's epilogue runs under the next tile's
+  // main loop; one where two of 256 columns would leave no room for the scales
+  // (the epilogue then takes the whole accumulator into registers first).
+  static constexpr int NACC = BN == 256 ? 1 : 2;
   static constexpr int FIT = (512 - NACC * BN) / SF_COLS;
   static constexpr int STAGES = RAW < FIT ? (RAW < 8 ? RAW : 8) : (FIT < 8 ? FIT : 8);
   static_assert(STAGES >= 3, "ring");
@@ -112,11 +117,15 @@ __device__ __forceinline__ constexpr uint32_t mx_idesc(uint32_t sf_id) {
          ((FMT == MX_FP4 ? 1u : 0u) << 23) | ((uint32_t)(M_ROWS >> 4) << 24) | (sf_id << 29);
 }
 
+// One block-scaled product, 128 x BN a block or 256 x BN a pair of blocks
+// (cta_group::2: each block holds its 128 rows of A and half of the B tile, and
+// the scales of all of it).
 template <typename T, int FMT, int BN, bool PAIR>
 __global__ void __launch_bounds__(MX_THREADS, 1)
     mx4_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmSA,
-                  const __grid_constant__ CUtensorMap tmSB, const MxTcParams mp) {
+                  const __grid_constant__ CUtensorMap tmSB,
+                  const __grid_constant__ CUtensorMap tmC, const MxTcParams mp) {
   using C_ = MxCfg<FMT, BN, PAIR>;
   // bytes that complete a stage (a pair's: both blocks', on the even block's barrier)
   constexpr uint32_t STAGE_TX = (uint32_t)(C_::STAGE_BYTES + C_::SF_BYTES) * (PAIR ? 2u : 1u);
@@ -154,7 +163,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
     }
     for (int b = 0; b < NACC; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), (PAIR ? 2 : 1) * 32 * EPI);
+      mbar_init(acce_bar(b), (PAIR ? 2 : 1) * 32 * 4 * C_::HALVES);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
@@ -251,6 +260,11 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         if (!mbar_wait(acce_bar(buf), acc_phase ^ 1u, wc)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
+        // a 64-column tile may start in the middle of a 128-row range: its scale
+        // columns start two words on
+        int m0, n0, bz;
+        tile_origin<PAIR, BN>(p, t, rank, m0, n0, bz);
+        const uint32_t tb_off = (uint32_t)((n0 & 127) / 32);
         for (int kb = 0; kb < mp.stages_k; ++kb) {
           if (!mbar_wait(full_bar(stage), phase, wc)) { ok = false; break; }
           tc_fence_after();
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
             tc_mma_mx4<FMT, PAIR>(d_tmem, make_sdesc(sa + (uint32_t)kk * 32u, 16u, 1024u),
                                   make_sdesc(sb + (uint32_t)kk * 32u, 16u, 1024u),
                                   mx_idesc<FMT, BN, PAIR ? 256 : 128>(id), (kb | kk) != 0 ? 1u : 0u,
-                                  ta + (uint32_t)(4 * tile), tb + (uint32_t)(4 * NBLK * tile));
+                                  ta + (uint32_t)(4 * tile), tb + tb_off + (uint32_t)(4 * NBLK * tile));
           }
           if constexpr (PAIR) tc_commit_pair_mc(empty_bar(stage), (uint16_t)3u);
           else tc_commit(empty_bar(stage));
@@ -294,15 +308,20 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;
+    const int q = warp & 3;   // tensor-memory lanes 32q .. 32q + 31
     const int ew = warp - 2;
+    const int hh = ew / 4;    // its share of the columns
+    constexpr int CW = BN / C_::HALVES;        // columns of a share
+    constexpr int KBOX = 128 / (int)sizeof(T);  // columns of a store box (128 bytes a row)
+    const uint32_t sbuf = staging_addr + (uint32_t)(ew * 4096);
     auto release_acc = [&](int buf) {
       tc_fence_before();
       if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(acce_bar(buf), 0u));
       else mbar_arrive(acce_bar(buf));
     };
+    const bool epi = p.ep.bias != nullptr || p.ep.act != 0;
     int it = 0;
-    for (int t = worker; t < p.tiles; t += workers, ++it) {
+    for (int t = worker; hh < C_::HALVES && t < p.tiles; t += workers, ++it) {
       int m0, n0, bz;
       tile_origin<PAIR, BN>(p, t, rank, m0, n0, bz);
       const int buf = it % NACC;
@@ -312,29 +331,82 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
       got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
       if (!got) break;
       tc_fence_after();
-      const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
-      const int gm = m0 + q * 32 + lane;
+      const int gn0 = n0 + hh * CW, gm0 = m0 + q * 32;
+      const uint32_t t_row =
+          tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + hh * CW);
+      if (p.c_tma && p.beta == 0.f) {
+        // The share into registers, finished and rounded; the accumulator is
+        // free from there on.
+        uint32_t o[CW * (int)sizeof(T) / 4];
+#pragma unroll
+        for (int c = 0; c < CW / 32; ++c) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(t_row + (uint32_t)(c * 32), r);
+          tmem_ld_wait();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[j]);
+          if (epi) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (gn0 + c * 32 + j < p.N) v[j] = apply_epilogue<T>(v[j], p.ep, gn0 + c * 32 + j);
+          }
+          if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[c * 32 + j] = __float_as_uint(v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const typename Elem<T>::T2 h = Elem<T>::pack(v[2 * j], v[2 * j + 1]);
+              o[c * 16 + j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+        }
+        release_acc(buf);
+        // 32-row boxes through this warp's staging buffer (128-byte swizzle:
+        // 16-byte chunk w of row l at chunk w ^ (l & 7))
+#pragma unroll
+        for (int b = 0; b < CW / KBOX; ++b) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int w = 0; w < 8; ++w)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             sbuf + (uint32_t)(lane * 128 + ((w ^ (lane & 7)) * 16))),
+                         "r"(o[b * 32 + 4 * w]), "r"(o[b * 32 + 4 * w + 1]),
+                         "r"(o[b * 32 + 4 * w + 2]), "r"(o[b * 32 + 4 * w + 3])
+                         : "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && gm0 < p.M && gn0 + b * KBOX < p.N) {
+            tma_store_3d(&tmC, gn0 + b * KBOX, gm0, 0, sbuf);
+            bulk_commit();
+          }
+        }
+        continue;
+      }
+      // C read (beta), or rows off 16-byte alignment
+      const int gm = gm0 + lane;
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = 0; c < CW / 32; ++c) {
         uint32_t r[32];
         __syncwarp();
         tmem_ld_32x32b_x32(t_row + (uint32_t)(c * 32), r);
         tmem_ld_wait();
-        if (c == BN / 32 - 1) release_acc(buf);
-        const int gn0 = n0 + c * 32;
+        if (c == CW / 32 - 1) release_acc(buf);
         if (!p.c_vec_ok) {
-          if (m0 + q * 32 < p.M)
-            store_c32_staged<T>(p, 0, m0 + q * 32, gn0, staging_addr + (uint32_t)(ew * 4096), r,
-                                lane);
+          if (gm0 < p.M) store_c32_staged<T>(p, 0, gm0, gn0 + c * 32, sbuf, r, lane);
           continue;
         }
         if (gm >= p.M) continue;
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        store_c32<T>(p, 0, gm, gn0, v);
+        store_c32<T>(p, 0, gm, gn0 + c * 32, v);
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -353,6 +425,30 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
 bool scale_map(CUtensorMap* m, const void* s, int64_t rows, int64_t tiles, int box) {
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, s, tiles, 128, 128, 128, box,
                   CU_TENSOR_MAP_SWIZZLE_NONE, (rows + 127) / 128, tiles * 128, 4);
+}
+
+// Blocks (or pairs) resident at once: an SM each (pairs: as many as the GPU's
+// clusters of two allow, queried once).
+template <typename T, int FMT, int BN, bool PAIR>
+int mx4_slots(int num_sms) {
+  if (!PAIR) return num_sms;
+  static const int slots = [num_sms] {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * (num_sms / 2));
+    cfg.blockDim = dim3(MX_THREADS);
+    cfg.dynamicSmemBytes = MxCfg<FMT, BN, PAIR>::SMEM_BYTES;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, mx4_tc_kernel<T, FMT, BN, PAIR>, &cfg) != cudaSuccess)
+      n = 0;
+    return n > 0 ? n : num_sms / 2;
+  }();
+  return slots;
 }
 
 template <typename T, int FMT, int BN, bool PAIR>
@@ -380,29 +476,71 @@ cudaError_t launch_mx4_cfg(const Mx4Args& a, LaunchCtx& ctx) {
   p.c_vec_ok = ((uintptr_t)a.C & 15u) == 0 && (a.ldc % VEC) == 0;
   p.batch = 1;
   p.ep = a.ep;
+  p.c_tma = p.c_vec_ok;
   mp.s_tiles = (int)mx_scale_tiles(FMT, a.K);
   mp.stages_k = (a.K + KSTAGE - 1) / KSTAGE;
   const int64_t kbytes = ((int64_t)a.K + 1) / 2;
-  CUtensorMap mA, mB, mSA, mSB;
+  CUtensorMap mA, mB, mSA, mSB, mC;
+  memset(&mC, 0, sizeof(mC));
   const CUtensorMapSwizzle SW = CU_TENSOR_MAP_SWIZZLE_128B;
   const CUtensorMapDataType U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!make_map(&mA, U8, a.A, a.M, kbytes, a.lda, 128, 128, SW, 1, 0, 1) ||
       !make_map(&mB, U8, a.B, a.N, kbytes, a.ldb, 128, PAIR ? BN / 2 : BN, SW, 1, 0, 1) ||
       !scale_map(&mSA, a.As, a.M, mp.s_tiles, C_::TPS) ||
-      !scale_map(&mSB, a.Bs, a.N, mp.s_tiles, C_::TPS))
+      !scale_map(&mSB, a.Bs, a.N, mp.s_tiles, C_::TPS) ||
+      (p.c_tma && !make_map(&mC, Elem<T>::TMA, a.C, a.M, a.N, a.ldc, 128 / (int)sizeof(T), 32, SW, 1,
+                            0, (int)sizeof(T))))
     return cudaErrorNotSupported;
-  const int workers = (int)min((int64_t)(PAIR ? a.num_sms / 2 : a.num_sms), tiles);
+  const int workers = (int)min((int64_t)mx4_slots<T, FMT, BN, PAIR>(a.num_sms), tiles);
   ctx.grid = PAIR ? 2 * workers : workers;
   const cudaError_t e = launch_kernel(kern, dim3(ctx.grid), dim3(MX_THREADS), C_::SMEM_BYTES,
-                                      ctx.stream, PAIR ? 2 : 1, mA, mB, mSA, mSB, mp);
+                                      ctx.stream, PAIR ? 2 : 1, mA, mB, mSA, mSB, mC, mp);
   if (e == cudaSuccess) ctx.launches++;
   return e;
 }
 
+// Tile: the one with the least estimated time, rounds of tiles x (K stages x
+// the bytes a block loads for a stage + the time of a tile's epilogue and start,
+// as bytes).
+enum { TILE_256_PAIR, TILE_128_PAIR, TILE_128, TILE_64, TILES };
+int mx4_pick(int M, int N, int K, int num_sms) {
+  static const int forced = [] {
+    const char* e = getenv("GEMM_GB300_MX_TILE");
+    return e ? atoi(e) : -1;
+  }();
+  if (forced >= 0 && forced < TILES) return forced;
+  const struct { int bm, bn, slots, kib, fixed; } shape[TILES] = {
+      {256, 256, num_sms / 2, 35, 140}, {256, 128, num_sms / 2, 26, 80},
+      {128, 128, num_sms, 34, 80}, {128, 64, num_sms, 26, 60}};
+  const int64_t stages = ((int64_t)K + KSTAGE - 1) / KSTAGE;
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < TILES; ++i) {
+    const int64_t tiles = (((int64_t)M + shape[i].bm - 1) / shape[i].bm) *
+                          (((int64_t)N + shape[i].bn - 1) / shape[i].bn);
+    const int64_t rounds = (tiles + shape[i].slots - 1) / shape[i].slots;
+    const double cost = (double)rounds * ((double)stages * shape[i].kib + shape[i].fixed);
+    if (i == 0 || cost < least) {
+      least = cost;
+      best = i;
+    }
+  }
+  return best;
+}
+
+template <typename T, int FMT>
+cudaError_t launch_mx4_f(const Mx4Args& a, LaunchCtx& ctx) {
+  switch (mx4_pick(a.M, a.N, a.K, a.num_sms)) {
+    case TILE_256_PAIR: return launch_mx4_cfg<T, FMT, 256, true>(a, ctx);
+    case TILE_128_PAIR: return launch_mx4_cfg<T, FMT, 128, true>(a, ctx);
+    case TILE_128: return launch_mx4_cfg<T, FMT, 128, false>(a, ctx);
+    default: return launch_mx4_cfg<T, FMT, 64, false>(a, ctx);
+  }
+}
 template <typename T>
 cudaError_t launch_mx4_t(const Mx4Args& a, LaunchCtx& ctx) {
-  if (a.format == MX_FP4) return launch_mx4_cfg<T, MX_FP4, 128, false>(a, ctx);
-  return launch_mx4_cfg<T, MX_FP4_E4M3, 128, false>(a, ctx);
+  return a.format == MX_FP4 ? launch_mx4_f<T, MX_FP4>(a, ctx)
+                            : launch_mx4_f<T, MX_FP4_E4M3>(a, ctx);
 }
 
 }  // namespace

@@ -131,7 +131,7 @@ int gemm_mx_quantize(int format, int transX, int64_t rows, int64_t cols, int dty
   if (rc != GEMM_OK) return rc;
   LaunchCtx ctx{(cudaStream_t)stream, st.status, st.timeout_ns, 0};
   MxQuantArgs a{format, dtype, transX, (int)rows, (int)cols, mult, X, ldx, Y, ldy, act, q, ldq,
-                scales};
+                scales, st.sms};
   return api_done(GEMM_PATH_MX, ctx, launch_mx_quantize(a, ctx));
 }
 
@@ -153,7 +153,7 @@ int gemm_mx_dequantize(int format, int64_t rows, int64_t cols, const void* q, in
   rc = api_state(&st);
   if (rc != GEMM_OK) return rc;
   LaunchCtx ctx{(cudaStream_t)stream, st.status, st.timeout_ns, 0};
-  MxDequantArgs a{format, dtype, (int)rows, (int)cols, q, ldq, scales, Y, ldy};
+  MxDequantArgs a{format, dtype, (int)rows, (int)cols, q, ldq, scales, Y, ldy, st.sms};
   return api_done(GEMM_PATH_MX, ctx, launch_mx_dequantize(a, ctx));
 }
 
@@ -192,10 +192,11 @@ int gemm_mx_act_backward(int64_t rows, int64_t cols, int dtype, int act, const v
   if (rc != GEMM_OK) return rc;
   LaunchCtx ctx{(cudaStream_t)stream, st.status, st.timeout_ns, 0};
   MxActBwdArgs a{dtype, (int)rows, (int)cols, act, dY, lddy, q, ldq, scales, dX, lddx, dbias,
-                 nullptr};
+                 nullptr, st.sms};
   Scratch ws;
-  if (dbias) {
-    const cudaError_t ce = ws.get(mx_act_backward_scratch(a.rows, a.cols), ctx.stream);
+  const size_t need = dbias ? mx_act_backward_scratch(a.rows, a.cols, st.sms) : 0;
+  if (need > 0) {
+    const cudaError_t ce = ws.get(need, ctx.stream);
     if (ce != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, ce);
     a.part = static_cast<float*>(ws.ptr);
   }
@@ -323,7 +324,7 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
   Scratch ws;
   cudaError_t ce = ws.get((size_t)(br * ldw * e), stream);
   if (ce != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, ce);
-  MxDequantArgs d{format, dtype, (int)br, (int)bc, B, ldb, Bs, ws.ptr, ldw};
+  MxDequantArgs d{format, dtype, (int)br, (int)bc, B, ldb, Bs, ws.ptr, ldw, st.sms};
   ce = launch_mx_dequantize(d, ctx);
   rc = api_done(GEMM_PATH_NONE, ctx, ce);
   if (rc != GEMM_OK) return rc;

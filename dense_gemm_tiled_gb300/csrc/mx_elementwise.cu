@@ -8,10 +8,11 @@
 //   dX     dx_rc = dy_rc * act'(q_rc s_rb),   dbias_c = sum_r dx_rc
 //
 // All are bound by HBM: each element is read once and written once.  A thread
-// takes 16 consecutive elements of a row (two or four 16-byte loads), four such
-// units in flight; 8 threads a row cover 128 columns, so a warp reads whole
-// 256-byte row segments, and a block of 8 warps a tile of 128 rows x 128
-// columns, whose scales are one tile of the storage (two for 16-column blocks).
+// keeps one unit of 16 columns and walks down the rows, two units (two 32-byte
+// loads of a 16-bit type) in flight; 8 threads a row cover 128 columns, and a
+// block of 8 warps 64 rows x 128 columns at a time.  The grid is the column
+// strips times as many blocks a strip as fill the GPU, so that a strip's column
+// sums stay in registers until its blocks join them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -25,8 +26,11 @@
 namespace gb300 {
 namespace {
 
-constexpr int TILE = 128;     // rows and columns of a block's tile
+constexpr int STRIP = 128;    // columns of a block
+constexpr int UNITS = 2;      // units of a thread in flight
+constexpr int TILE_ROWS = 32 * UNITS;
 constexpr int THREADS = 256;
+constexpr int BLOCKS_PER_SM = 4;
 
 struct QuantParams {
   const void* X;
@@ -39,8 +43,9 @@ struct QuantParams {
   int64_t ldq;
   uint8_t* s;
   int64_t s_tiles;   // scale tiles of a 128-row range
-  int64_t tiles_n, tiles;
-  int vec_x, vec_y;  // 16-byte accesses allowed
+  int64_t tiles_m;   // row tiles (the last 128-row range in full: its padding is written)
+  int64_t tiles_n, tiles;  // (transposed form)
+  int vec_x, vec_y;
 };
 
 // bits of |mult| * (a magnitude given by its bits), with a NaN's kept a NaN's
@@ -54,62 +59,66 @@ __device__ __forceinline__ uint32_t max_abs_bits(const float (&x)[16]) {
   return m;
 }
 
-// Phi(x) = (1 + erf(x / sqrt 2)) / 2 and e = exp(-x^2 / 2), which the gelu and
-// its derivative share:  erfc(z) = t (a1 + t (a2 + ... )) exp(-z^2), t = 1 / (1 +
-// p z), z >= 0, within 1.5e-7 (M. Abramowitz and I. Stegun, "Handbook of
-// Mathematical Functions", 7.1.26).  One exponential, one reciprocal and about
-// ten other instructions; with erff and expf these kernels were bound by
-// arithmetic (16384 x 5632 bf16, forward and backward: 465 us).
-__device__ __forceinline__ float normal_cdf(float x, float& e) {
-  const float z = fabsf(x) * 0.70710678118654752f;
+// c = erfc(|x| / sqrt 2) / 2 = Phi(-|x|) and e = exp(-x^2 / 2), which the gelu
+// and its derivative share:  erfc(z) = t (a1 + t (a2 + ... )) exp(-z^2), t = 1 /
+// (1 + p z), within 1.5e-7 (M. Abramowitz and I. Stegun, "Handbook of
+// Mathematical Functions", 7.1.26).  One exponential, one reciprocal and nine
+// other instructions; with erff and expf these kernels were bound by arithmetic
+// (16384 x 5632 bf16, forward and backward: 465 us against 257).
+__device__ __forceinline__ float normal_tail(float x, float& e) {
   float t;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, z, 1.f)));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-0.72134752044448170f * x * x));
-  float c = fmaf(t, 1.061405429f, -1.453152027f);
-  c = fmaf(t, c, 1.421413741f);
-  c = fmaf(t, c, -0.284496736f);
-  c = fmaf(t, c, 0.254829592f);
-  c = 0.5f * t * c * e;
-  return x < 0.f ? c : 1.f - c;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f * 0.70710678f, fabsf(x), 1.f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-0.72134752f * x * x));
+  float c = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  c = fmaf(t, c, 0.5f * 1.421413741f);
+  c = fmaf(t, c, 0.5f * -0.284496736f);
+  c = fmaf(t, c, 0.5f * 0.254829592f);
+  return t * c * e;
 }
-__device__ __forceinline__ float act_value(float x, int act) {
-  if (act == 1) return x > 0.f ? x : 0.f;
-  if (act == 2) {
+template <int ACT>
+__device__ __forceinline__ float act_value(float x) {
+  if (ACT == 1) return x > 0.f ? x : 0.f;
+  if (ACT == 2) {  // x Phi(x) = max(x, 0) - |x| Phi(-|x|)
     float e;
-    return x * normal_cdf(x, e);
+    const float c = normal_tail(x, e);
+    return fmaf(-fabsf(x), c, x > 0.f ? x : 0.f);
   }
   return x;
 }
 
 // ACT: the activation of Y, or -1 without Y
 template <typename T, int FMT, int ACT>
-__global__ void __launch_bounds__(THREADS) mx_quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) mx_quantize_kernel(const QuantParams p) {
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = lane & 7;
-  for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
-    const int64_t tm = t / p.tiles_n;
-    const int64_t c0 = (t - tm * p.tiles_n) * TILE + u * 16;
-    const int n = (int)min((int64_t)16, max((int64_t)0, (int64_t)p.cols - c0));
-    const int64_t r0 = tm * TILE + warp * 16 + (lane >> 3);
-    MxRow16<T> in[4];
+  const int64_t c0 = (int64_t)blockIdx.x * STRIP + u * 16;
+  const int n = (int)min((int64_t)16, max((int64_t)0, (int64_t)p.cols - c0));
+  const int64_t qcol = c0 / 16 * mx_bytes16<FMT>();
+  const bool has_codes = qcol < mx_row_bytes(FMT, p.cols);
+  const int64_t st = c0 / (4 * mx_block(FMT));
+  // the lane that writes a scale word
+  const bool has_word = (mx_block(FMT) == 32 ? u == 0 : (u & 3) == 0) && st < p.s_tiles;
+  for (int64_t tm = blockIdx.y; tm < p.tiles_m; tm += gridDim.y) {
+    const int64_t r0 = tm * TILE_ROWS + warp * 4 * UNITS + (lane >> 3);
+    MxRow16<T> in[UNITS];
+    int64_t row[UNITS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = r0 + 4 * j;
-      in[j] = mx_load16<T>(static_cast<const T*>(p.X) + r * p.ldx + c0, r < p.rows ? n : 0,
-                           p.vec_x != 0);
-    }
+    for (int j = 0; j < UNITS; ++j)
+      row[j] = min(r0 + 4 * j, (int64_t)p.rows - 1) * p.ldx;  // (rows past the end: not stored)
+    mx_load_units<T, UNITS>(static_cast<const T*>(p.X) + c0, row, n, p.vec_x, in);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < UNITS; ++j) {
       const int64_t r = r0 + 4 * j;
+      const bool real = r < p.rows;
       float x[16];
       mx_unpack16<T>(in[j], x);
-      if (ACT >= 0 && r < p.rows) {
+      if (ACT >= 0 && real) {
         float y[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = act_value(x[i], ACT);
-        mx_store16<T>(static_cast<T*>(p.Y) + r * p.ldy + c0, n, p.vec_y != 0, y);
+        for (int i = 0; i < 16; ++i) y[i] = act_value<ACT>(x[i]);
+        mx_store16<T>(static_cast<T*>(p.Y) + r * p.ldy + c0, n, p.vec_y, y);
       }
       // (the largest of |mult x| is |mult| times the largest |x|: rounding keeps order)
       uint32_t m = mx_max_abs16<T>(in[j]);
@@ -119,32 +128,25 @@ __global__ void __launch_bounds__(THREADS) mx_quantize_kernel(const QuantParams 
         for (int i = 0; i < 16; ++i) x[i] *= p.mult;
       }
       if (mx_block(FMT) == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      const bool real = r < p.rows && n > 0;
       uint32_t byte = mx_scale_byte<FMT>(__uint_as_float(m));
       MxCodes<FMT> c;
       mx_encode16<FMT>(x, byte, __uint_as_float(m), c);
       // (codes of absent columns up to the row's 16-byte unit are written as 0)
-      if (r < p.rows && c0 / 16 * mx_bytes16<FMT>() < mx_row_bytes(FMT, p.cols))
-        mx_store_codes<FMT>(p.q + r * p.ldq + c0 / 16 * mx_bytes16<FMT>(), c);
-      // four blocks' scale bytes as a word; absent rows and blocks 0
-      byte = real ? byte : 0u;
+      if (real && has_codes) mx_store_codes<FMT>(p.q + r * p.ldq + qcol, c);
+      // four blocks' scale bytes as a word; absent rows and blocks 0 (of a 32-
+      // column block's two units only the second may be absent)
+      uint32_t w;
       if (mx_block(FMT) == 32) {
-        // the block's second unit may be absent while its first is not
-        byte = __shfl_sync(0xffffffffu, byte, lane & ~1);
-        uint32_t w = byte << (8 * (u >> 1));
+        w = real && n > 0 && (u & 1) == 0 ? byte << (4 * u) : 0u;
         w |= __shfl_xor_sync(0xffffffffu, w, 2);
         w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        const int64_t st = c0 / 128;
-        if (u == 0 && st < p.s_tiles)
-          *reinterpret_cast<uint32_t*>(p.s + mx_scale_word(r, st, p.s_tiles)) = w;
       } else {
-        uint32_t w = byte << (8 * (u & 3));
+        w = real && n > 0 ? byte << (8 * (u & 3)) : 0u;
         w |= __shfl_xor_sync(0xffffffffu, w, 1);
         w |= __shfl_xor_sync(0xffffffffu, w, 2);
-        const int64_t st = c0 / 64;
-        if ((u & 3) == 0 && st < p.s_tiles)
-          *reinterpret_cast<uint32_t*>(p.s + mx_scale_word(r, st, p.s_tiles)) = w;
       }
+      if (has_word)
+        *reinterpret_cast<uint32_t*>(p.s + mx_scale_word(r, st, p.s_tiles)) = w;
     }
   }
 }
@@ -176,15 +178,16 @@ __global__ void __launch_bounds__(TT_THREADS) mx_quantize_t_kernel(const QuantPa
     const T* src = static_cast<const T*>(p.X) + c0 * p.ldx + r;
     struct alignas(2 * sizeof(T)) Two { T a, b; };
     Two in[32];
+    // (the paths apart, so that a whole tile's loads are issued together)
+    if (p.vec_x && nr == 2 && nc == 32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      in[i].a = in[i].b = MxIo<T>::from(0.f);
-      if (i < nc) {
-        if (p.vec_x && nr == 2) in[i] = *reinterpret_cast<const Two*>(src + i * p.ldx);
-        else {
-          if (nr > 0) in[i].a = src[i * p.ldx];
-          if (nr > 1) in[i].b = src[i * p.ldx + 1];
-        }
+      for (int i = 0; i < 32; ++i) in[i] = *reinterpret_cast<const Two*>(src + i * p.ldx);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        in[i].a = in[i].b = MxIo<T>::from(0.f);
+        if (i < nc && nr > 0) in[i].a = src[i * p.ldx];
+        if (i < nc && nr > 1) in[i].b = src[i * p.ldx + 1];
       }
     }
 #pragma unroll
@@ -241,46 +244,38 @@ struct DequantParams {
   int rows, cols;
   void* Y;
   int64_t ldy;
-  int64_t tiles_n, tiles;
+  int64_t tiles_m;
   int vec_y;
 };
 
-// the scale of 16-column unit starting at c0 of row r
-template <int FMT>
-__device__ __forceinline__ float unit_scale(const uint8_t* s, int64_t s_tiles, int64_t r,
-                                            int64_t c0) {
-  const int64_t b = c0 / mx_block(FMT);
-  return mx_scale_value<FMT>(s[mx_scale_word(r, b >> 2, s_tiles) + (b & 3)]);
-}
-
 template <typename T, int FMT>
-__global__ void __launch_bounds__(THREADS) mx_dequantize_kernel(const DequantParams p) {
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM)
+    mx_dequantize_kernel(const DequantParams p) {
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
-    const int64_t tm = t / p.tiles_n;
-    const int64_t c0 = (t - tm * p.tiles_n) * TILE + (lane & 7) * 16;
-    const int n = (int)min((int64_t)16, (int64_t)p.cols - c0);
-    if (n <= 0) continue;
-    const int64_t r0 = tm * TILE + warp * 16 + (lane >> 3);
-    MxCodes<FMT> c[4];
-    float s[4];
+  const int64_t c0 = (int64_t)blockIdx.x * STRIP + (lane & 7) * 16;
+  const int n = (int)min((int64_t)16, (int64_t)p.cols - c0);
+  if (n <= 0) return;
+  const uint8_t* const q = p.q + c0 / 16 * mx_bytes16<FMT>();
+  const int64_t b = c0 / mx_block(FMT);
+  for (int64_t tm = blockIdx.y; tm < p.tiles_m; tm += gridDim.y) {
+    const int64_t r0 = tm * TILE_ROWS + warp * 4 * UNITS + (lane >> 3);
+    MxCodes<FMT> c[UNITS];
+    uint32_t byte[UNITS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = r0 + 4 * j;
-      if (r < p.rows) {
-        c[j] = mx_load_codes<FMT>(p.q + r * p.ldq + c0 / 16 * mx_bytes16<FMT>());
-        s[j] = unit_scale<FMT>(p.s, p.s_tiles, r, c0);
-      }
+    for (int j = 0; j < UNITS; ++j) {
+      const int64_t r = min(r0 + 4 * j, (int64_t)p.rows - 1);
+      c[j] = mx_load_codes<FMT>(q + r * p.ldq);
+      byte[j] = p.s[mx_scale_word(r, b >> 2, p.s_tiles) + (b & 3)];
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < UNITS; ++j) {
       const int64_t r = r0 + 4 * j;
       if (r >= p.rows) continue;
       float x[16];
-      mx_decode16<FMT>(c[j], s[j], x);
-      mx_store16<T>(static_cast<T*>(p.Y) + r * p.ldy + c0, n, p.vec_y != 0, x);
+      mx_decode16<FMT>(c[j], mx_scale_value<FMT>(byte[j]), x);
+      mx_store16<T>(static_cast<T*>(p.Y) + r * p.ldy + c0, n, p.vec_y, x);
     }
   }
 }
@@ -295,8 +290,8 @@ struct ActBwdParams {
   int rows, cols;
   void* dX;
   int64_t lddx;
-  float* part;  // [tiles_m][cols] column sums of a tile, or null
-  int64_t tiles_n, tiles;
+  float* part;  // [blocks of a strip][cols] column sums, or null
+  int64_t tiles_m;
   int vec_in, vec_out;
 };
 
@@ -307,89 +302,103 @@ __device__ __forceinline__ float act_slope(float x) {
   if (ACT == 1) return x > 0.f ? 1.f : 0.f;
   if (ACT == 2) {
     float e;
-    const float c = normal_cdf(x, e);
-    return fmaf(0.39894228040143268f * x, e, c);
+    const float c = normal_tail(x, e);
+    return fmaf(0.39894228040143268f * x, e, x < 0.f ? c : 1.f - c);
   }
   return 1.f;
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(THREADS) mx_act_backward_kernel(const ActBwdParams p) {
-  __shared__ float colsum[8][TILE];
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM - 1)
+    mx_act_backward_kernel(const ActBwdParams p) {
+  __shared__ float colsum[8][STRIP];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = lane & 7;
-  for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
-    const int64_t tm = t / p.tiles_n;
-    const int64_t cc0 = (t - tm * p.tiles_n) * TILE, c0 = cc0 + u * 16;
-    const int n = (int)min((int64_t)16, max((int64_t)0, (int64_t)p.cols - c0));
-    const int64_t r0 = tm * TILE + warp * 16 + (lane >> 3);
-    float sum[16];
+  const int64_t cc0 = (int64_t)blockIdx.x * STRIP, c0 = cc0 + u * 16;
+  const int n = (int)min((int64_t)16, max((int64_t)0, (int64_t)p.cols - c0));
+  const int64_t b = c0 / 32;
+  float sum[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum[i] = 0.f;
-    MxRow16<T> in[4];
-    MxCodes<MX_INT8> c[4];
-    float s[4];
+  for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+  for (int64_t tm = blockIdx.y; n > 0 && tm < p.tiles_m; tm += gridDim.y) {
+    const int64_t r0 = tm * TILE_ROWS + warp * 4 * UNITS + (lane >> 3);
+    MxRow16<T> in[UNITS];
+    MxCodes<MX_INT8> c[UNITS];
+    uint32_t byte[UNITS];
+    int64_t row[UNITS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = r0 + 4 * j;
-      if (r < p.rows && n > 0) {
-        in[j] = mx_load16<T>(static_cast<const T*>(p.dY) + r * p.lddy + c0, n, p.vec_in != 0);
-        c[j] = mx_load_codes<MX_INT8>(p.q + r * p.ldq + c0);
-        s[j] = unit_scale<MX_INT8>(p.s, p.s_tiles, r, c0);
-      }
+    for (int j = 0; j < UNITS; ++j) {
+      const int64_t r = min(r0 + 4 * j, (int64_t)p.rows - 1);
+      row[j] = r * p.lddy;
+      c[j] = mx_load_codes<MX_INT8>(p.q + r * p.ldq + c0);
+      byte[j] = p.s[mx_scale_word(r, b >> 2, p.s_tiles) + (b & 3)];
     }
+    mx_load_units<T, UNITS>(static_cast<const T*>(p.dY) + c0, row, n, p.vec_in, in);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < UNITS; ++j) {
       const int64_t r = r0 + 4 * j;
-      if (r >= p.rows || n <= 0) continue;
+      if (r >= p.rows) continue;
       float dy[16], x[16];
-      mx_unpack16<T>(in[j], dy);
-      mx_decode16<MX_INT8>(c[j], s[j], x);
+      mx_unpack16<T>(in[j], dy);  // (absent columns 0)
+      mx_decode16<MX_INT8>(c[j], e8m0_value(byte[j]), x);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         dy[i] *= act_slope<ACT>(x[i]);
-        sum[i] += i < n ? dy[i] : 0.f;
+        sum[i] += dy[i];
       }
-      mx_store16<T>(static_cast<T*>(p.dX) + r * p.lddx + c0, n, p.vec_out != 0, dy);
+      mx_store16<T>(static_cast<T*>(p.dX) + r * p.lddx + c0, n, p.vec_out, dy);
     }
-    if (p.part) {
-      // the warp's 16 rows, then the block's 128, in a fixed order
+  }
+  if (p.part) {
+    // the warp's rows, then the block's, in a fixed order
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
-        if (lane < 8) colsum[warp][u * 16 + i] = sum[i];
-      }
-      __syncthreads();
-      if (threadIdx.x < TILE && cc0 + threadIdx.x < p.cols) {
-        float v = 0.f;
+    for (int i = 0; i < 16; ++i) {
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
+      if (lane < 8) colsum[warp][u * 16 + i] = sum[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < STRIP && cc0 + threadIdx.x < p.cols) {
+      float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) v += colsum[w][threadIdx.x];
-        p.part[tm * p.cols + cc0 + threadIdx.x] = v;
-      }
-      __syncthreads();
+      for (int w = 0; w < 8; ++w) v += colsum[w][threadIdx.x];
+      p.part[blockIdx.y * (int64_t)p.cols + cc0 + threadIdx.x] = v;
     }
   }
 }
 
-// out[c] = sum over tile rows of part[.][c], in order
-__global__ void mx_column_sum_kernel(const float* part, int64_t tiles_m, int cols, float* out) {
+// out[c] = sum of the blocks' column sums, in order
+__global__ void mx_column_sum_kernel(const float* part, int blocks, int cols, float* out) {
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= cols) return;
   float v = 0.f;
-  for (int64_t t = 0; t < tiles_m; ++t) v += part[t * cols + c];
+#pragma unroll 8
+  for (int t = 0; t < blocks; ++t) v += part[(int64_t)t * cols + c];
   out[c] = v;
 }
 
-inline bool vec_ok(const void* p, int64_t ld, int64_t es) {
-  return ((uintptr_t)p % 16) == 0 && (ld * es) % 16 == 0;
+inline int vec_of(const void* p, int64_t ld, int64_t es) {
+  if (((uintptr_t)p % 32) == 0 && (ld * es) % 32 == 0) return MX_VEC32;
+  if (((uintptr_t)p % 16) == 0 && (ld * es) % 16 == 0) return MX_VEC16;
+  return MX_SCALAR;
 }
 inline unsigned grid_of(int64_t tiles) {
   return (unsigned)(tiles < (1ll << 30) ? tiles : (1ll << 30));
+}
+// Column strips x blocks a strip: one row tile a block while that fits the GPU
+// `per_sm` blocks deep, else equal numbers of row tiles in about that many
+// blocks.
+dim3 strip_grid(int64_t cols, int64_t tiles_m, int sms, int per_sm) {
+  const int64_t strips = (cols + STRIP - 1) / STRIP;
+  const int64_t room = (int64_t)sms * per_sm;
+  const int64_t iters = (strips * tiles_m + room - 1) / room;
+  int64_t blocks = (tiles_m + iters - 1) / iters;
+  if (blocks > 65535) blocks = 65535;
+  return dim3((unsigned)strips, (unsigned)blocks);
 }
 
 template <typename T, int FMT>
@@ -402,7 +411,7 @@ cudaError_t quantize_t(const MxQuantArgs& a, LaunchCtx& ctx) {
   p.q = static_cast<uint8_t*>(a.q); p.ldq = a.ldq;
   p.s = static_cast<uint8_t*>(a.s);
   p.s_tiles = mx_scale_tiles(FMT, a.cols);
-  p.vec_y = a.Y && vec_ok(a.Y, a.ldy, sizeof(T));
+  p.vec_y = a.Y ? vec_of(a.Y, a.ldy, sizeof(T)) : MX_SCALAR;
   const int64_t rows128 = ((int64_t)a.rows + 127) / 128;
   cudaError_t e;
   if (a.transX) {
@@ -413,15 +422,15 @@ cudaError_t quantize_t(const MxQuantArgs& a, LaunchCtx& ctx) {
     e = launch_kernel(mx_quantize_t_kernel<T, FMT>, dim3(ctx.grid), dim3(TT_THREADS), 0,
                       ctx.stream, 1, p);
   } else {
-    p.vec_x = vec_ok(a.X, a.ldx, sizeof(T));
-    p.tiles_n = ((int64_t)a.cols + TILE - 1) / TILE;
-    p.tiles = rows128 * p.tiles_n;
-    ctx.grid = (int)grid_of(p.tiles);
+    p.vec_x = vec_of(a.X, a.ldx, sizeof(T));
+    p.tiles_m = rows128 * (128 / TILE_ROWS);
+    const dim3 grid = strip_grid(a.cols, p.tiles_m, a.num_sms, BLOCKS_PER_SM);
+    ctx.grid = (int)(grid.x * grid.y);
     auto kern = !a.Y         ? mx_quantize_kernel<T, FMT, -1>
                 : a.act == 2 ? mx_quantize_kernel<T, FMT, 2>
                 : a.act == 1 ? mx_quantize_kernel<T, FMT, 1>
                              : mx_quantize_kernel<T, FMT, 0>;
-    e = launch_kernel(kern, dim3(ctx.grid), dim3(THREADS), 0, ctx.stream, 1, p);
+    e = launch_kernel(kern, grid, dim3(THREADS), 0, ctx.stream, 1, p);
   }
   if (e == cudaSuccess) ctx.launches++;
   return e;
@@ -435,15 +444,17 @@ cudaError_t dequantize_t(const MxDequantArgs& a, LaunchCtx& ctx) {
   p.s_tiles = mx_scale_tiles(FMT, a.cols);
   p.rows = a.rows; p.cols = a.cols;
   p.Y = a.Y; p.ldy = a.ldy;
-  p.vec_y = vec_ok(a.Y, a.ldy, sizeof(T));
-  p.tiles_n = ((int64_t)a.cols + TILE - 1) / TILE;
-  p.tiles = ((int64_t)a.rows + TILE - 1) / TILE * p.tiles_n;
-  ctx.grid = (int)grid_of(p.tiles);
-  const cudaError_t e = launch_kernel(mx_dequantize_kernel<T, FMT>, dim3(ctx.grid),
-                                      dim3(THREADS), 0, ctx.stream, 1, p);
+  p.vec_y = vec_of(a.Y, a.ldy, sizeof(T));
+  p.tiles_m = ((int64_t)a.rows + TILE_ROWS - 1) / TILE_ROWS;
+  const dim3 grid = strip_grid(a.cols, p.tiles_m, a.num_sms, 2 * BLOCKS_PER_SM);
+  ctx.grid = (int)(grid.x * grid.y);
+  const cudaError_t e =
+      launch_kernel(mx_dequantize_kernel<T, FMT>, grid, dim3(THREADS), 0, ctx.stream, 1, p);
   if (e == cudaSuccess) ctx.launches++;
   return e;
 }
+
+inline int64_t act_tiles(int rows) { return ((int64_t)rows + TILE_ROWS - 1) / TILE_ROWS; }
 
 template <typename T>
 cudaError_t act_backward_t(const MxActBwdArgs& a, LaunchCtx& ctx) {
@@ -455,21 +466,21 @@ cudaError_t act_backward_t(const MxActBwdArgs& a, LaunchCtx& ctx) {
   p.rows = a.rows; p.cols = a.cols;
   p.dX = a.dX; p.lddx = a.lddx;
   p.part = a.dbias ? a.part : nullptr;
-  p.vec_in = vec_ok(a.dY, a.lddy, sizeof(T));
-  p.vec_out = vec_ok(a.dX, a.lddx, sizeof(T));
-  p.tiles_n = ((int64_t)a.cols + TILE - 1) / TILE;
-  const int64_t tiles_m = ((int64_t)a.rows + TILE - 1) / TILE;
-  p.tiles = tiles_m * p.tiles_n;
-  ctx.grid = (int)grid_of(p.tiles);
+  p.vec_in = vec_of(a.dY, a.lddy, sizeof(T));
+  p.vec_out = vec_of(a.dX, a.lddx, sizeof(T));
+  p.tiles_m = act_tiles(a.rows);
+  const dim3 grid = strip_grid(a.cols, p.tiles_m, a.num_sms, BLOCKS_PER_SM - 1);
+  ctx.grid = (int)(grid.x * grid.y);
   auto kern = a.act == 2   ? mx_act_backward_kernel<T, 2>
               : a.act == 1 ? mx_act_backward_kernel<T, 1>
                            : mx_act_backward_kernel<T, 0>;
-  cudaError_t e =
-      launch_kernel(kern, dim3(ctx.grid), dim3(THREADS), 0, ctx.stream, 1, p);
+  // (a strip with one block has its sums at once)
+  if (a.dbias && grid.y == 1) p.part = a.dbias;
+  cudaError_t e = launch_kernel(kern, grid, dim3(THREADS), 0, ctx.stream, 1, p);
   if (e == cudaSuccess) ctx.launches++;
-  if (e == cudaSuccess && a.dbias) {
-    e = launch_kernel(mx_column_sum_kernel, dim3((unsigned)((a.cols + 127) / 128)), dim3(128), 0,
-                      ctx.stream, 1, (const float*)a.part, tiles_m, a.cols, a.dbias);
+  if (e == cudaSuccess && a.dbias && grid.y > 1) {
+    e = launch_kernel(mx_column_sum_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(64), 0,
+                      ctx.stream, 1, (const float*)a.part, (int)grid.y, a.cols, a.dbias);
     if (e == cudaSuccess) ctx.launches++;
   }
   return e;
@@ -498,8 +509,9 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, LaunchCtx& ctx) {
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, LaunchCtx& ctx) {
   GB300_MX_FORMATS(dequantize_t, a, ctx)
 }
-size_t mx_act_backward_scratch(int rows, int cols) {
-  return (size_t)(((int64_t)rows + TILE - 1) / TILE) * cols * sizeof(float);
+size_t mx_act_backward_scratch(int rows, int cols, int num_sms) {
+  const dim3 grid = strip_grid(cols, act_tiles(rows), num_sms, BLOCKS_PER_SM - 1);
+  return grid.y > 1 ? (size_t)grid.y * cols * sizeof(float) : 0;
 }
 cudaError_t launch_mx_act_backward(const MxActBwdArgs& a, LaunchCtx& ctx) {
   switch (a.out) {

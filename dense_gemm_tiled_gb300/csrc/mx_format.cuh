@@ -209,8 +209,8 @@ __device__ __forceinline__ void mx_decode16(const MxCodes<FMT>& c, float scale, 
 }
 
 // ---------------------------------------------------------------- 16 values of a row
-// Loads and stores of 16 consecutive elements as fp32: 16-byte accesses where
-// the rows allow, otherwise (or at a row's end) element by element, absent
+// Loads and stores of 16 consecutive elements as fp32: 32- or 16-byte accesses
+// where the rows allow, otherwise (or at a row's end) element by element, absent
 // elements 0.
 template <typename T>
 struct MxIo;
@@ -236,20 +236,49 @@ struct MxRow16 {
   uint4 v[VECS];
 };
 
-template <typename T>
-__device__ __forceinline__ MxRow16<T> mx_load16(const T* p, int n, bool vec) {
-  MxRow16<T> r;
-  if (vec && n >= 16) {
-#pragma unroll
-    for (int i = 0; i < MxRow16<T>::VECS; ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
-  } else {
-    T e[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) e[i] = i < n ? p[i] : MxIo<T>::from(0.f);
-    memcpy(&r, e, sizeof(r));
-  }
-  return r;
+// How a row's 16-element units may be accessed: 32 bytes at a time, 16, or
+// element by element.
+enum { MX_SCALAR = 0, MX_VEC16 = 1, MX_VEC32 = 2 };
+
+__device__ __forceinline__ void mx_ld32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                 "=r"(b.w)
+               : "l"(p));
 }
+__device__ __forceinline__ void mx_st32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+// U units of 16 elements, `step` elements apart (n elements of each exist);
+// with the loads of a vector path issued together.
+template <typename T, int U>
+__device__ __forceinline__ void mx_load_units(const T* p, const int64_t (&row)[U], int n, int vec,
+                                              MxRow16<T> (&in)[U]) {
+  if (n == 16 && vec == MX_VEC32) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int i = 0; i < MxRow16<T>::VECS; i += 2)
+        mx_ld32(p + row[j] + i * (16 / (int)sizeof(T)), in[j].v[i], in[j].v[i + 1]);
+  } else if (n == 16 && vec == MX_VEC16) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int i = 0; i < MxRow16<T>::VECS; ++i)
+        in[j].v[i] = reinterpret_cast<const uint4*>(p + row[j])[i];
+  } else {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      T e[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) e[i] = i < n ? p[row[j] + i] : MxIo<T>::from(0.f);
+      memcpy(&in[j], e, sizeof(in[j]));
+    }
+  }
+}
+
 // Largest magnitude of 16 loaded values, as fp32 bits: a NaN counts above
 // infinity, infinity above all numbers.  16-bit types compare their magnitude's
 // bits two at a time.
@@ -285,13 +314,17 @@ __device__ __forceinline__ void mx_unpack16(const MxRow16<T>& r, float (&x)[16])
   for (int i = 0; i < 16; ++i) x[i] = MxIo<T>::to(e[i]);
 }
 template <typename T>
-__device__ __forceinline__ void mx_store16(T* p, int n, bool vec, const float (&x)[16]) {
+__device__ __forceinline__ void mx_store16(T* p, int n, int vec, const float (&x)[16]) {
   T e[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) e[i] = MxIo<T>::from(x[i]);
-  if (vec && n >= 16) {
-    MxRow16<T> r;
-    memcpy(&r, e, sizeof(r));
+  MxRow16<T> r;
+  memcpy(&r, e, sizeof(r));
+  if (n == 16 && vec == MX_VEC32) {
+#pragma unroll
+    for (int i = 0; i < MxRow16<T>::VECS; i += 2)
+      mx_st32(p + i * (16 / (int)sizeof(T)), r.v[i], r.v[i + 1]);
+  } else if (n == 16 && vec == MX_VEC16) {
 #pragma unroll
     for (int i = 0; i < MxRow16<T>::VECS; ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
   } else {

@@ -38,7 +38,7 @@ constexpr int ROWS = 128;          // rows of B a block takes
 constexpr int KSTEP = 256;         // codes of K a stage holds
 constexpr int WARPS = 4;
 constexpr int ST_THREADS = 32 * (WARPS + 1);
-constexpr int MAX_RING = 5;
+constexpr int MAX_RING = 3;
 constexpr int MAX_SPLIT = 8;       // blocks of a cluster (the portable limit)
 constexpr int SMEM_MAX = 227 * 1024;
 

@@ -16,8 +16,9 @@
 // operands of eight 8-column tiles (column 8g + j of the half in tile j).  A
 // comes through ldmatrix.trans.
 //   A code becomes fp16 by putting its byte into 1024's fraction (1024 + q + 128,
-// exact) and taking 1152 away; the scale, a power of two within fp16's normal
-// range, multiplies it exactly.  Other scales, and bf16, go through fp32.
+// exact); one FMA by the scale takes 1152 times the scale away, exactly while
+// the scale is a power of two between 2^-14 and 2^5.  Other scales, and bf16, go
+// through fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,7 +39,7 @@ constexpr int COLS = 128;   // columns of the checkpoint a block takes
 constexpr int TSTEP = 64;   // rows of it a stage holds
 constexpr int WG_WARPS = 4;
 constexpr int WG_THREADS = 32 * (WG_WARPS + 1);
-constexpr int WG_RING = 6;
+constexpr int WG_RING = 4;
 constexpr int WG_SPLIT = 8;
 constexpr int WG_SMEM_MAX = 227 * 1024;
 
@@ -113,19 +114,22 @@ template <typename T>
 __device__ __forceinline__ void code_pairs(uint2 w0, uint2 w1, uint32_t b0, uint32_t b1,
                                            uint32_t (&out)[8]) {
   const uint32_t a[2] = {w0.x, w0.y}, b[2] = {w1.x, w1.y};
-  // both scales normal fp16 numbers: 2^-14 .. 2^15
-  const bool fast = std::is_same<T, __half>::value && b0 - 113u < 30u && b1 - 113u < 30u;
+  // both scales normal fp16 numbers with 1152 times them in range: 2^-14 .. 2^5
+  const bool fast = std::is_same<T, __half>::value && b0 - 113u < 20u && b1 - 113u < 20u;
   if (fast) {
     const uint32_t sbits = ((b0 - 112u) << 10) | ((b1 - 112u) << 26);
     const __half2 s = *reinterpret_cast<const __half2*>(&sbits);
-    const __half2 off = __float2half2_rn(-1152.f);
+    // -1152 s: -1152's bits with the scale's exponent added
+    const uint32_t obits = ((0xE480u + (b0 << 10) - (127u << 10)) & 0xFFFFu) |
+                           ((0xE480u + (b1 << 10) - (127u << 10)) << 16);
+    const __half2 off = *reinterpret_cast<const __half2*>(&obits);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t lo = __byte_perm(a[h], b[h], 0x5140), hi = __byte_perm(a[h], b[h], 0x7362);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t v = __byte_perm(j < 2 ? lo : hi, 0x64646464u, (j & 1) ? 0x4342 : 0x4140);
-        const __half2 x = __hmul2(__hadd2(*reinterpret_cast<const __half2*>(&v), off), s);
+        const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&v), s, off);
         out[4 * h + j] = *reinterpret_cast<const uint32_t*>(&x);
       }
     }
@@ -213,6 +217,25 @@ __global__ void __launch_bounds__(WG_THREADS)
     }
   } else {
     // ------------------------------------------------------------ products
+    // this lane's places within a stage: rows 2 c + (i & 1) + 8 (i >> 1) of a
+    // 16-row step (the swizzle goes by the row's last three bits: the same for
+    // every step)
+    uint32_t at_q[2], at_a[MT], at_s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * c + i;
+      at_q[i] = (uint32_t)(t * 128 + (((4 * half + (g >> 1)) ^ t) * 16) + 8 * (g & 1) + part * 4096);
+      at_s[i] = (uint32_t)(C_::Q_BYTES + C_::A_BYTES + t * 16 + 2 * half + (g >> 2) + part * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      // 8 x 8 blocks (rows t, columns m): t half by lane bit 4, m half by bit 3
+      const int t = (lane & 7) + ((lane >> 4) << 3);
+      const int ch = 2 * i + ((lane >> 3) & 1);  // 16-byte chunk of A's row
+      // (the swizzle of a row of 32 MT bytes)
+      const int sw = MT == 4 ? (t & 7) : MT == 2 ? ((t >> 1) & 3) : ((t >> 2) & 1);
+      at_a[i] = (uint32_t)(C_::Q_BYTES + (t + part * 32) * 32 * MT + ((ch ^ sw) * 16));
+    }
     int stage = 0;
     uint32_t phase = 0;
     for (int k = k_lo; k < k_hi; ++k) {
@@ -220,33 +243,24 @@ __global__ void __launch_bounds__(WG_THREADS)
       if (lane == 0) ok = mbar_wait(full_bar(stage), phase, wc);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
-      const uint32_t q = base + (uint32_t)(stage * C_::STAGE), a = q + C_::Q_BYTES;
-      const uint32_t s = a + C_::A_BYTES + (uint32_t)(2 * half + (g >> 2));
-      const int t_in = (k * TSTEP) & 127;  // the stage's place in its scale tile
+      const uint32_t q = base + (uint32_t)(stage * C_::STAGE);
+      // (64 rows on: two words on in the scale tile's rows)
+      const uint32_t s_in = q + (uint32_t)(((k * TSTEP) & 127) / 32 * 4);
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const int t0 = (2 * part + kk) * 16;  // rows t0 .. t0 + 15 of the stage
+      for (int kk = 0; kk < 2; ++kk) {  // rows 32 part + 16 kk .. + 15 of the stage
         uint32_t am[MT][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          // 8 x 8 blocks (rows t, columns m): t half by lane bit 4, m half by bit 3
-          const int t = t0 + (lane & 7) + ((lane >> 4) << 3);
-          const int ch = 2 * i + ((lane >> 3) & 1);  // 16-byte chunk of A's row
-          // (the swizzle of a row of 32 MT bytes)
-          const int sw = MT == 4 ? (t & 7) : MT == 2 ? ((t >> 1) & 3) : ((t >> 2) & 1);
-          ldmatrix_x4_trans(a + (uint32_t)(t * 32 * MT + ((ch ^ sw) * 16)), am[i]);
-        }
+        for (int i = 0; i < MT; ++i)
+          ldmatrix_x4_trans(q + at_a[i] + (uint32_t)(kk * 16 * 32 * MT), am[i]);
         uint2 w[4];
         uint32_t sb[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 2 * c + (i & 1) + 8 * (i >> 1);
-          const int ch = 4 * half + (g >> 1);
-          w[i] = lds64(q + (uint32_t)(t * 128 + ((ch ^ (t & 7)) * 16) + 8 * (g & 1)));
+          const uint32_t down = (uint32_t)(kk * 16 + 8 * (i >> 1));
+          w[i] = lds64(q + at_q[i & 1] + down * 128u);
           w[i].x ^= 0x80808080u;
           w[i].y ^= 0x80808080u;
-          const int ts = t_in + t;
-          sb[i] = lds8(s + (uint32_t)((ts & 31) * 16 + (ts >> 5) * 4));
+          sb[i] = lds8(s_in + at_s[i & 1] + down * 16u);
         }
         uint32_t lo[8], hi[8];
         code_pairs<T>(w[0], w[1], sb[0], sb[1], lo);
