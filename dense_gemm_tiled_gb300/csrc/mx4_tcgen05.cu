@@ -71,32 +71,57 @@ struct MxTcParams {
   int stages_k;        // K stages of a tile
 };
 
-// 32 rows x 16 bytes at `sdesc` -> 32 lanes x 4 columns, in each lane quarter
-template <bool PAIR>
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t sdesc) {
-  if constexpr (PAIR)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-                 : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-                 : "memory");
+// One thread of a warp whose 32 threads all take the same path: the issuing
+// loops keep the whole warp together, so that addresses and descriptors live in
+// uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
-// descriptor of an unswizzled scale tile: 8-row groups of 128 bytes
-__device__ __forceinline__ uint64_t scale_sdesc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
+
+// Shared-memory descriptors as (low word, constant high word): the low word
+// holds the address >> 4, so a step along K or a ring stage is an addition.
+//   codes: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart
+//   scale tile: no swizzle, 8-row groups 128 bytes apart
+constexpr uint32_t CODES_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t SCALES_HI = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+
+// 32 rows x 16 bytes of a scale tile -> 32 lanes x 4 columns, in each lane quarter
+template <bool PAIR>
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t lo) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(lo), "n"(SCALES_HI)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(lo), "n"(SCALES_HI)
+        : "memory");
 }
 
 #define GB300_MX_MMA(GROUP, KIND)                                                       \
   asm volatile(                                                                         \
-      "{\n\t.reg .pred p;\n\t"                                                          \
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"                                     \
       "setp.ne.b32 p, %4, 0;\n\t"                                                       \
+      "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"                              \
       "tcgen05.mma.cta_group::" GROUP ".kind::" KIND                                    \
-      " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),                                \
-      "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)                        \
+      " [%0], da, db, %3, [%5], [%6], p;\n\t}" ::"r"(d),                                \
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb), "n"(CODES_HI)     \
       : "memory")
 template <int FMT, bool PAIR>
-__device__ __forceinline__ void tc_mma_mx4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
-                                           uint32_t acc, uint32_t sfa, uint32_t sfb) {
+__device__ __forceinline__ void tc_mma_mx4(uint32_t d, uint32_t a_lo, uint32_t b_lo,
+                                           uint32_t idesc, uint32_t acc, uint32_t sfa,
+                                           uint32_t sfb) {
   if constexpr (FMT == MX_FP4) {
     if constexpr (PAIR) GB300_MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
     else GB300_MX_MMA("1", "mxf4.block_scale.scale_vec::2X");
@@ -249,7 +274,10 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool leader = elect_one();
+      const uint32_t a_lo0 = desc_lo(tiles_addr), b_lo0 = desc_lo(tiles_addr + C_::A_BYTES);
+      const uint32_t fa_lo0 = desc_lo(sf_addr), fb_lo0 = desc_lo(sf_addr + C_::SFA_BYTES);
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
@@ -257,7 +285,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
       for (int t = worker; ok && t < p.tiles; t += workers, ++it) {
         const int buf = it % NACC;
         const uint32_t acc_phase = (uint32_t)(it / NACC) & 1u;
-        if (!mbar_wait(acce_bar(buf), acc_phase ^ 1u, wc)) { ok = false; break; }
+        ok = __all_sync(0xffffffffu, mbar_wait(acce_bar(buf), acc_phase ^ 1u, wc));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
         // a 64-column tile may start in the middle of a 128-row range: its scale
@@ -266,45 +295,57 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         tile_origin<PAIR, BN>(p, t, rank, m0, n0, bz);
         const uint32_t tb_off = (uint32_t)((n0 & 127) / 32);
         for (int kb = 0; kb < mp.stages_k; ++kb) {
-          if (!mbar_wait(full_bar(stage), phase, wc)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, wc));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = tiles_addr + (uint32_t)(stage * C_::STAGE_BYTES);
-          const uint32_t sb = sa + (uint32_t)C_::A_BYTES;
-          const uint32_t fa = sf_addr + (uint32_t)(stage * C_::SF_BYTES);
-          const uint32_t fb = fa + (uint32_t)C_::SFA_BYTES;
+          const uint32_t a_lo = a_lo0 + (uint32_t)(stage * (C_::STAGE_BYTES >> 4));
+          const uint32_t b_lo = b_lo0 + (uint32_t)(stage * (C_::STAGE_BYTES >> 4));
+          const uint32_t fa_lo = fa_lo0 + (uint32_t)(stage * (C_::SF_BYTES >> 4));
+          const uint32_t fb_lo = fb_lo0 + (uint32_t)(stage * (C_::SF_BYTES >> 4));
           const uint32_t ta = sf_tmem + (uint32_t)(stage * C_::SF_COLS);
           const uint32_t tb = ta + (uint32_t)(TPS * 4);
-          const int nt = min(TPS, mp.s_tiles - kb * TPS);
-          for (int i = 0; i < nt; ++i) {
-            tc_cp_scales<PAIR>(ta + (uint32_t)(4 * i), scale_sdesc(fa + (uint32_t)(512 * i)));
+          // tiles and MMAs past the end of K are left out (their scales do not exist)
+          const int nt = mp.s_tiles - kb * TPS;
+          const int nm = (p.K - kb * KSTAGE + KMMA - 1) / KMMA;
+          if (leader) {
 #pragma unroll
-            for (int r = 0; r < NBLK; ++r)
-              tc_cp_scales<PAIR>(tb + (uint32_t)(4 * (i * NBLK + r)),
-                                 scale_sdesc(fb + (uint32_t)(512 * (r * TPS + i))));
-          }
-          // MMAs past the end of K are left out (their scales do not exist)
-          const int nm = min(KSTAGE / KMMA, (p.K - kb * KSTAGE + KMMA - 1) / KMMA);
+            for (int i = 0; i < TPS; ++i) {
+              if (i >= nt) break;
+              tc_cp_scales<PAIR>(ta + (uint32_t)(4 * i), fa_lo + (uint32_t)(32 * i));
 #pragma unroll
-          for (int kk = 0; kk < KSTAGE / KMMA; ++kk) {
-            if (kk >= nm) break;
-            const int tile = kk * TPS / (KSTAGE / KMMA);          // its scale tile
-            const uint32_t id = FMT == MX_FP4 ? 2u * (kk & 1) : 0u;  // and byte within the words
-            tc_mma_mx4<FMT, PAIR>(d_tmem, make_sdesc(sa + (uint32_t)kk * 32u, 16u, 1024u),
-                                  make_sdesc(sb + (uint32_t)kk * 32u, 16u, 1024u),
-                                  mx_idesc<FMT, BN, PAIR ? 256 : 128>(id), (kb | kk) != 0 ? 1u : 0u,
-                                  ta + (uint32_t)(4 * tile), tb + tb_off + (uint32_t)(4 * NBLK * tile));
+              for (int r = 0; r < NBLK; ++r)
+                tc_cp_scales<PAIR>(tb + (uint32_t)(4 * (i * NBLK + r)),
+                                   fb_lo + (uint32_t)(32 * (r * TPS + i)));
+            }
+#pragma unroll
+            for (int kk = 0; kk < KSTAGE / KMMA; ++kk) {
+              if (kk >= nm) break;
+              const int tile = kk * TPS / (KSTAGE / KMMA);             // its scale tile
+              const uint32_t id = FMT == MX_FP4 ? 2u * (kk & 1) : 0u;  // and byte within the words
+              tc_mma_mx4<FMT, PAIR>(d_tmem, a_lo + (uint32_t)(2 * kk), b_lo + (uint32_t)(2 * kk),
+                                    mx_idesc<FMT, BN, PAIR ? 256 : 128>(id),
+                                    (kb | kk) != 0 ? 1u : 0u, ta + (uint32_t)(4 * tile),
+                                    tb + tb_off + (uint32_t)(4 * NBLK * tile));
+            }
+            if constexpr (PAIR) tc_commit_pair_mc(empty_bar(stage), (uint16_t)3u);
+            else tc_commit(empty_bar(stage));
           }
-          if constexpr (PAIR) tc_commit_pair_mc(empty_bar(stage), (uint16_t)3u);
-          else tc_commit(empty_bar(stage));
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        if constexpr (PAIR) tc_commit_pair_mc(accf_bar(buf), (uint16_t)3u);
-        else tc_commit(accf_bar(buf));
+        if (leader) {
+          if constexpr (PAIR) tc_commit_pair_mc(accf_bar(buf), (uint16_t)3u);
+          else tc_commit(accf_bar(buf));
+        }
+        __syncwarp();
       }
-      if constexpr (PAIR) tc_commit_pair_mc(drain_bar, (uint16_t)1u);
-      else tc_commit(drain_bar);
-      mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
+      if (leader) {
+        if constexpr (PAIR) tc_commit_pair_mc(drain_bar, (uint16_t)1u);
+        else tc_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue
