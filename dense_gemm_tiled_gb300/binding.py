@@ -350,28 +350,31 @@ class Mx:
     tensor of `rows` rows (row pitch a multiple of 16 bytes, at least
     mx_row_bytes), and `scales`, a contiguous uint8 CUDA tensor of at least
     mx_scale_bytes elements.  fmt: 'fp4', 'fp4_e4m3' or 'int8'."""
-    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "pitch")
+    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "pitch", "ptr", "sptr")
 
     def __init__(self, codes, scales, fmt, rows, cols):
         code = MX_FORMATS.get(fmt)
         if code is None:
             raise ValueError(f"unknown format {fmt!r}")
-        shape, stride = codes.shape, codes.stride()
         if not (codes.is_cuda and scales.is_cuda):
             raise ValueError("stored operands are CUDA tensors")
-        if codes.element_size() != 1 or scales.element_size() != 1:
+        if codes.itemsize != 1 or scales.itemsize != 1:
             raise TypeError("codes and scales are bytes")
-        need = _lib.gemm_mx_row_bytes(code, cols)
+        # (mx_row_bytes and mx_scale_bytes, without a call into the library)
+        need = ((cols if code == 2 else (cols + 1) >> 1) + 15) & -16
+        blocks = (cols + 15) >> 4 if code == 1 else (cols + 31) >> 5
+        shape, stride = codes.shape, codes.stride()
         if len(shape) != 2 or shape[0] != rows or shape[1] < need or \
                 (shape[1] > 1 and stride[1] != 1):
             raise ValueError(f"codes: {rows} rows of at least {need} bytes, contiguous within a row")
-        if scales.numel() < _lib.gemm_mx_scale_bytes(code, rows, cols) or \
+        if scales.numel() < ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512 or \
                 not scales.is_contiguous():
             raise ValueError("scales: a contiguous tensor of mx_scale_bytes(fmt, rows, cols) bytes")
         self.codes, self.scales, self.fmt, self.format = codes, scales, fmt, code
-        self.rows, self.cols = int(rows), int(cols)
+        self.rows, self.cols = rows, cols
         # (a single row's pitch is not used: any valid one)
         self.pitch = stride[0] if rows > 1 else max(need, 16)
+        self.ptr, self.sptr = codes.data_ptr() or None, scales.data_ptr() or None
 
 
 def mx_empty(rows, cols, fmt, device="cuda") -> Mx:
@@ -416,8 +419,8 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     rc = _lib.gemm_mx_quantize(
         Q.format, int(transX), Q.rows, Q.cols, dtype, float(mult), X.data_ptr() or None, _ld(X),
         ACTS[act], (Y.data_ptr() or None) if Y is not None else None,
-        _ld(Y) if Y is not None else 0, Q.codes.data_ptr() or None, Q.pitch,
-        Q.scales.data_ptr() or None, _handle(stream, X))
+        _ld(Y) if Y is not None else 0, Q.ptr, Q.pitch,
+        Q.sptr, _handle(stream, X))
     if rc != OK:
         raise GemmError(rc)
     return Q
@@ -428,8 +431,8 @@ def mx_dequantize(Q, Y, stream=None):
     dtype = _plain_code(Y, "mx_dequantize()")
     if tuple(Y.shape) != (Q.rows, Q.cols):
         raise ValueError(f"Y is {tuple(Y.shape)}, expected {(Q.rows, Q.cols)}")
-    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, Q.codes.data_ptr() or None, Q.pitch,
-                                 Q.scales.data_ptr() or None, dtype, Y.data_ptr() or None, _ld(Y),
+    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, Q.ptr, Q.pitch,
+                                 Q.sptr, dtype, Y.data_ptr() or None, _ld(Y),
                                  _handle(stream, Y))
     if rc != OK:
         raise GemmError(rc)
@@ -452,7 +455,7 @@ def mx_act_backward(dY, Q, dX, act="gelu", dbias=None, stream=None):
         raise ValueError("dbias: a contiguous float32 CUDA tensor of cols elements")
     rc = _lib.gemm_mx_act_backward(
         Q.rows, Q.cols, dtype, ACTS[act], dY.data_ptr() or None, _ld(dY),
-        Q.codes.data_ptr() or None, Q.pitch, Q.scales.data_ptr() or None, dX.data_ptr() or None,
+        Q.ptr, Q.pitch, Q.sptr, dX.data_ptr() or None,
         _ld(dX), (dbias.data_ptr() or None) if dbias is not None else None, _handle(stream, dY))
     if rc != OK:
         raise GemmError(rc)
@@ -469,43 +472,52 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
     A and B Mx of the same 4-bit format, both stored along K (A [M, K], B
     [N, K]): C = act(alpha * A @ B.T + beta * C + bias); transA and transB stay
     False.  Returns C."""
-    dtype = _plain_code(C, "gemm_mx()")
-    M, N = C.shape
-    stored_a = isinstance(A, Mx)
-    if stored_a:
+    dt = C.dtype
+    dtype = _DTYPES.get(dt)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    if not C.is_cuda:
+        raise ValueError("gemm_mx() takes CUDA tensors")
+    sc = C.shape
+    if len(sc) != 2:
+        raise ValueError("matrices are 2-D")
+    M, N = sc
+    bp = None
+    if bias is not None:
+        if not bias.is_cuda or bias.dtype != dt or bias.numel() != N or not bias.is_contiguous():
+            raise ValueError("bias: a contiguous CUDA tensor of N elements of C's dtype")
+        bp = bias.data_ptr() or None
+    s = (stream.cuda_stream if stream is not None else _current_stream(C.get_device())) or None
+    if isinstance(A, Mx):
         if transA or transB:
             raise ValueError("two stored operands are both stored along K")
-        if A.fmt != B.fmt:
+        if A.format != B.format:
             raise TypeError("both operands have the same format")
-        K, Kb, Ma, Nb = A.cols, B.cols, A.rows, B.rows
+        K = A.cols
+        if K != B.cols:
+            raise ValueError(f"inner dimensions differ: {K} vs {B.cols}")
+        if A.rows != M or B.rows != N:
+            raise ValueError(f"C is {(M, N)}, expected {(A.rows, B.rows)}")
+        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, alpha, beta, A.ptr, A.pitch, A.sptr, B.ptr,
+                           B.pitch, B.sptr, C.data_ptr() or None, _ld_of(sc, C.stride()), bp,
+                           ACTS[act], s)
     else:
-        if A.dtype != C.dtype:
+        if A.dtype != dt:
             raise TypeError("A and C must share a dtype")
-        if A.dim() != 2:
+        sa = A.shape
+        if len(sa) != 2:
             raise ValueError("matrices are 2-D")
         if not A.is_cuda:
             raise ValueError("gemm_mx() takes CUDA tensors")
-        Ma, K = (A.shape[1], A.shape[0]) if transA else (A.shape[0], A.shape[1])
+        Ma, K = (sa[1], sa[0]) if transA else sa
         Kb, Nb = (B.cols, B.rows) if transB else (B.rows, B.cols)
-    if K != Kb:
-        raise ValueError(f"inner dimensions differ: {K} vs {Kb}")
-    if Ma != M or Nb != N:
-        raise ValueError(f"C is {(M, N)}, expected {(Ma, Nb)}")
-    if bias is not None and (not bias.is_cuda or bias.dtype != C.dtype or bias.numel() != N or
-                             not bias.is_contiguous()):
-        raise ValueError("bias: a contiguous CUDA tensor of N elements of C's dtype")
-    bp = (bias.data_ptr() or None) if bias is not None else None
-    s = _handle(stream, C)
-    if stored_a:
-        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, float(alpha), float(beta),
-                           A.codes.data_ptr() or None, A.pitch, A.scales.data_ptr() or None,
-                           B.codes.data_ptr() or None, B.pitch, B.scales.data_ptr() or None,
-                           C.data_ptr() or None, _ld(C), bp, ACTS[act], s)
-    else:
-        rc = _lib.gemm_mx(B.format, int(transA), int(transB), M, N, K, dtype, float(alpha),
-                          float(beta), A.data_ptr() or None, _ld(A), B.codes.data_ptr() or None,
-                          B.pitch, B.scales.data_ptr() or None, C.data_ptr() or None, _ld(C), bp,
-                          ACTS[act], s)
+        if K != Kb:
+            raise ValueError(f"inner dimensions differ: {K} vs {Kb}")
+        if Ma != M or Nb != N:
+            raise ValueError(f"C is {(M, N)}, expected {(Ma, Nb)}")
+        rc = _lib.gemm_mx(B.format, 1 if transA else 0, 1 if transB else 0, M, N, K, dtype, alpha,
+                          beta, A.data_ptr() or None, _ld_of(sa, A.stride()), B.ptr, B.pitch,
+                          B.sptr, C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
     if rc != OK:
         raise GemmError(rc)
     return C

@@ -8,8 +8,8 @@
 // A block takes 128 rows of B and a slice of K; the blocks of a cluster share
 // the rows and split K, so that a weight of a few dozen row ranges still keeps
 // every SM loading.  A producer warp brings 128 x 256 codes, their scale tiles
-// and the matching columns of A into a ring of stages by TMA; four warps multiply
-// 32 rows each with m16n8k16 warp MMAs, the codes as the 16-row operand.  The
+// and the matching columns of A into a ring of stages by TMA; eight warps
+// multiply 16 rows each with m16n8k16 warp MMAs, the codes as the 16-row operand.  The
 // K order within a 32-code group is the loads': lane c of a quad holds codes 8c
 // .. 8c + 7 (one word) and the same eight columns of A (one 16-byte load).
 //   Power-of-two scales are applied to the fp32 sums of a 32-code group, which
@@ -36,9 +36,10 @@ namespace {
 
 constexpr int ROWS = 128;          // rows of B a block takes
 constexpr int KSTEP = 256;         // codes of K a stage holds
-constexpr int WARPS = 4;
+constexpr int WARPS = 8;            // 16 rows of B each
 constexpr int ST_THREADS = 32 * (WARPS + 1);
 constexpr int MAX_RING = 3;
+constexpr int SUM_PITCH = ROWS + 4;  // (a quad's four columns in different banks)
 constexpr int MAX_SPLIT = 8;       // blocks of a cluster (the portable limit)
 constexpr int SMEM_MAX = 227 * 1024;
 
@@ -53,7 +54,7 @@ struct SCfg {
   static constexpr int S_BYTES = TPS * 512;
   static constexpr int XS_BYTES = XT == X_FP4 ? TPS * 512 : 0;
   static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES + XS_BYTES;
-  static constexpr int SUMS = ROWS * 8 * NT * 4;
+  static constexpr int SUMS = SUM_PITCH * 8 * NT * 4;
   static constexpr int smem(int ring) { return ring * STAGE + SUMS + 1024 + 256; }
   static constexpr int RING_MAX = (SMEM_MAX - SUMS - 1280) / STAGE;
   static constexpr int RING = RING_MAX < MAX_RING ? RING_MAX : MAX_RING;
@@ -159,13 +160,11 @@ __global__ void __launch_bounds__(ST_THREADS)
   pdl_trigger();
   const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
 
-  float acc[2][NT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
   if (warp == WARPS) {
     // ------------------------------------------------------------ producer
@@ -205,6 +204,10 @@ __global__ void __launch_bounds__(ST_THREADS)
   } else {
     // ------------------------------------------------------------ products
     const int g = lane >> 2, c = lane & 3;
+    // this lane's places in a stage: row 16 warp + g of the codes (the 128-byte
+    // swizzle goes by g), its scale word
+    const uint32_t w_at = (uint32_t)((16 * warp + g) * 128 + 4 * c);
+    const uint32_t s_at = (uint32_t)(((16 * warp + g) & 31) * 16 + (warp >> 1) * 4);
     int stage = 0;
     uint32_t phase = 0;
     for (int k = k_lo; k < k_hi; ++k) {
@@ -214,21 +217,20 @@ __global__ void __launch_bounds__(ST_THREADS)
       if (!ok) break;
       const uint32_t w = base + (uint32_t)(stage * C_::STAGE), x = w + C_::W_BYTES;
       const uint32_t s = x + C_::X_BYTES, xs = s + C_::S_BYTES;
-      // scale words of rows g, g + 8, g + 16, g + 24 of the warp's 32
-      uint32_t sw[TPS][4];
+      // scale words of rows g and g + 8 of the warp's 16
+      uint32_t sw[TPS][2];
 #pragma unroll
       for (int t = 0; t < TPS; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sw[t][i] = lds32(s + (uint32_t)(t * 512 + (g + 8 * i) * 16 + 4 * warp));
+        for (int i = 0; i < 2; ++i)
+          sw[t][i] = lds32(s + s_at + (uint32_t)(t * 512 + i * 128));
 #pragma unroll
       for (int b = 0; b < KSTEP / 32; ++b) {
-        // B's codes: rows g + 8i, eight a lane
-        uint32_t wa[4][4];
+        // B's codes: rows g and g + 8, eight a lane
+        uint32_t wa[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 32 * warp + g + 8 * i;
-          const uint32_t v = lds32(w + (uint32_t)(r * 128 + ((b ^ (r & 7)) * 16) + 4 * c));
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t v = lds32(w + w_at + (uint32_t)(i * 1024) + (uint32_t)((b ^ g) * 16));
           e2m1_halves(v, wa[i]);
           if constexpr (FMT == MX_FP4_E4M3) {
             const int blk = 2 * b + (c >> 1);  // of the stage's 16
@@ -241,17 +243,19 @@ __global__ void __launch_bounds__(ST_THREADS)
             for (int j = 0; j < 4; ++j) wa[i][j] = half2_to_bf162(wa[i][j]);
           }
         }
-        float sc[4];
+        const uint32_t a0[4] = {wa[0][0], wa[1][0], wa[0][1], wa[1][1]};
+        const uint32_t a1[4] = {wa[0][2], wa[1][2], wa[0][3], wa[1][3]};
+        float sc[2];
         if constexpr (FMT == MX_FP4) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[i] = e8m0_value((sw[b / 4][i] >> (8 * (b & 3))) & 255u);
+          for (int i = 0; i < 2; ++i) sc[i] = e8m0_value((sw[b / 4][i] >> (8 * (b & 3))) & 255u);
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           uint32_t xb[4];
           if constexpr (XT == X_FP4) {
             const int r = 8 * j + g;
-            e2m1_halves(lds32(x + (uint32_t)(r * 128 + ((b ^ (r & 7)) * 16) + 4 * c)), xb);
+            e2m1_halves(lds32(x + (uint32_t)(r * 128 + ((b ^ g) * 16) + 4 * c)), xb);
             if constexpr (FMT == MX_FP4_E4M3) {
               const int blk = 2 * b + (c >> 1), row = (m0 & 127) + r;
               const uint32_t word = lds32(xs + (uint32_t)((blk >> 2) * 512 + (row & 31) * 16 +
@@ -264,43 +268,36 @@ __global__ void __launch_bounds__(ST_THREADS)
             const uint4 v = lds128(x + (uint32_t)((b * 8 * NT + 8 * j + g) * 64 + 16 * c));
             xb[0] = v.x; xb[1] = v.y; xb[2] = v.z; xb[3] = v.w;
           }
-          float xsc[2] = {1.f, 1.f};
-          if constexpr (XT == X_FP4 && FMT == MX_FP4) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int row = (m0 & 127) + 8 * j + 2 * c + e;
-              const uint32_t word =
-                  lds32(xs + (uint32_t)((b >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4));
-              xsc[e] = e8m0_value((word >> (8 * (b & 3))) & 255u);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a0[4] = {wa[2 * i][0], wa[2 * i + 1][0], wa[2 * i][1], wa[2 * i + 1][1]};
-            const uint32_t a1[4] = {wa[2 * i][2], wa[2 * i + 1][2], wa[2 * i][3], wa[2 * i + 1][3]};
-            if constexpr (FMT == MX_FP4) {
-              float part[4] = {0.f, 0.f, 0.f, 0.f};
-              if constexpr (XT == X_BF16) {
-                mma_bf16(part, a0, xb[0], xb[1]);
-                mma_bf16(part, a1, xb[2], xb[3]);
-              } else {
-                mma_f16(part, a0, xb[0], xb[1]);
-                mma_f16(part, a1, xb[2], xb[3]);
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float v = part[e];
-                if constexpr (XT == X_FP4) v *= xsc[e & 1];
-                acc[i][j][e] = __fmaf_rn(v, sc[2 * i + (e >> 1)], acc[i][j][e]);
-              }
+          if constexpr (FMT == MX_FP4) {
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (XT == X_BF16) {
+              mma_bf16(part, a0, xb[0], xb[1]);
+              mma_bf16(part, a1, xb[2], xb[3]);
             } else {
-              if constexpr (XT == X_BF16) {
-                mma_bf16(acc[i][j], a0, xb[0], xb[1]);
-                mma_bf16(acc[i][j], a1, xb[2], xb[3]);
-              } else {
-                mma_f16(acc[i][j], a0, xb[0], xb[1]);
-                mma_f16(acc[i][j], a1, xb[2], xb[3]);
+              mma_f16(part, a0, xb[0], xb[1]);
+              mma_f16(part, a1, xb[2], xb[3]);
+            }
+            if constexpr (XT == X_FP4) {
+              // the scales of A's rows 2c and 2c + 1 of this tile
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int row = (m0 & 127) + 8 * j + 2 * c + e;
+                const uint32_t word =
+                    lds32(xs + (uint32_t)((b >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4));
+                const float xsc = e8m0_value((word >> (8 * (b & 3))) & 255u);
+                part[e] *= xsc;
+                part[2 + e] *= xsc;
               }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = __fmaf_rn(part[e], sc[e >> 1], acc[j][e]);
+          } else {
+            if constexpr (XT == X_BF16) {
+              mma_bf16(acc[j], a0, xb[0], xb[1]);
+              mma_bf16(acc[j], a1, xb[2], xb[3]);
+            } else {
+              mma_f16(acc[j], a0, xb[0], xb[1]);
+              mma_f16(acc[j], a1, xb[2], xb[3]);
             }
           }
         }
@@ -311,15 +308,13 @@ __global__ void __launch_bounds__(ST_THREADS)
     }
     // this block's sums: [row of C][row of B]
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int n = 32 * warp + 16 * i + g + 8 * (e >> 1), m = 8 * j + 2 * c + (e & 1);
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + (uint32_t)((m * ROWS + n) * 4)),
-                       "f"(acc[i][j][e]));
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int n = 16 * warp + g + 8 * (e >> 1), m = 8 * j + 2 * c + (e & 1);
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + (uint32_t)((m * SUM_PITCH + n) * 4)),
+                     "f"(acc[j][e]));
+      }
   }
   // ------------------------------------------------------------ join
   // (a block alone is a cluster of one: the barriers then are the block's)
@@ -331,7 +326,7 @@ __global__ void __launch_bounds__(ST_THREADS)
     const int m = i / n_cnt, n = n_lo + i % n_cnt;
     if (n0 + n >= p.N) continue;
     float v = 0.f;
-    const uint32_t mine = sums + (uint32_t)((m * ROWS + n) * 4);
+    const uint32_t mine = sums + (uint32_t)((m * SUM_PITCH + n) * 4);
     for (int r = 0; r < splits; ++r) {
       float f;
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(mapa_shared(mine, (uint32_t)r)));

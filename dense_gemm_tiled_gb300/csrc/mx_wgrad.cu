@@ -10,14 +10,14 @@
 // A block takes 128 columns of the checkpoint and a slice of T; a cluster's
 // blocks share the columns and split T.  A producer warp brings 64 rows of q (128-
 // byte swizzle), their scale tile and the same rows of A into a ring by TMA.
-// Four warps: two halves of the columns, two halves of each stage's rows.  The
-// warp MMA (m16n8k16) wants pairs of t for one column: a lane reads 8 bytes of
-// four rows and interleaves them with byte permutes, so one pass makes the
-// operands of eight 8-column tiles (column 8g + j of the half in tile j).  A
+// Eight warps: four quarters of the columns, two halves of each stage's rows.
+// The warp MMA (m16n8k16) wants pairs of t for one column: a lane reads 4 bytes
+// of four rows and interleaves them with byte permutes, so one pass makes the
+// operands of four 8-column tiles (column 4g + j of the quarter in tile j).  A
 // comes through ldmatrix.trans.
 //   A code becomes fp16 by putting its byte into 1024's fraction (1024 + q + 128,
 // exact); one FMA by the scale takes 1152 times the scale away, exactly while
-// the scale is a power of two between 2^-14 and 2^5.  Other scales, and bf16, go
+// the scale is a power of two between 2^-14 and 2.  Other scales, and bf16, go
 // through fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -37,9 +37,10 @@ namespace {
 
 constexpr int COLS = 128;   // columns of the checkpoint a block takes
 constexpr int TSTEP = 64;   // rows of it a stage holds
-constexpr int WG_WARPS = 4;
+constexpr int WG_WARPS = 8;
 constexpr int WG_THREADS = 32 * (WG_WARPS + 1);
 constexpr int WG_RING = 4;
+constexpr int WG_PITCH = COLS + 2;  // of the sums (fewer lanes a bank)
 constexpr int WG_SPLIT = 8;
 constexpr int WG_SMEM_MAX = 227 * 1024;
 
@@ -50,7 +51,7 @@ struct GCfg {
   static constexpr int S_BYTES = 1024;  // one 512-byte tile, its slot a swizzle period
   static constexpr int STAGE = Q_BYTES + A_BYTES + S_BYTES;
   static constexpr uint32_t TX = Q_BYTES + A_BYTES + 512;
-  static constexpr int SUMS = 16 * MT * COLS * 4;
+  static constexpr int SUMS = 16 * MT * WG_PITCH * 4;
   static constexpr int smem(int ring) { return ring * STAGE + SUMS + 1024 + 256; }
 };
 
@@ -87,9 +88,9 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t a, uint32_t (&r)[4]) 
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a));
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
@@ -108,43 +109,37 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// Pairs (row 0, row 1) of eight columns' values as 16-bit operands: w0, w1 the
-// two rows' codes (each offset by 128), b0, b1 their scale bytes.
+// Pairs (row 0, row 1) of four columns' values as 16-bit operands: a, b the two
+// rows' codes (each offset by 128), s0, s1 their scale bytes.
 template <typename T>
-__device__ __forceinline__ void code_pairs(uint2 w0, uint2 w1, uint32_t b0, uint32_t b1,
-                                           uint32_t (&out)[8]) {
-  const uint32_t a[2] = {w0.x, w0.y}, b[2] = {w1.x, w1.y};
-  // both scales normal fp16 numbers with 1152 times them in range: 2^-14 .. 2^5
-  const bool fast = std::is_same<T, __half>::value && b0 - 113u < 20u && b1 - 113u < 20u;
-  if (fast) {
-    const uint32_t sbits = ((b0 - 112u) << 10) | ((b1 - 112u) << 26);
-    const __half2 s = *reinterpret_cast<const __half2*>(&sbits);
-    // -1152 s: -1152's bits with the scale's exponent added
-    const uint32_t obits = ((0xE480u + (b0 << 10) - (127u << 10)) & 0xFFFFu) |
-                           ((0xE480u + (b1 << 10) - (127u << 10)) << 16);
-    const __half2 off = *reinterpret_cast<const __half2*>(&obits);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __byte_perm(a[h], b[h], 0x5140), hi = __byte_perm(a[h], b[h], 0x7362);
+__device__ __forceinline__ void code_pairs(uint32_t a, uint32_t b, uint32_t s0, uint32_t s1,
+                                           uint32_t (&out)[4]) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const uint32_t t = s0 | (s1 << 16);
+    // both scales between 2^-14 and 2 (activations below 254): they and 1152
+    // times them are normal fp16 numbers
+    if (((t - 0x00710071u) & 0xFFF0FFF0u) == 0u) {
+      const uint32_t sbits = (t - 0x00700070u) << 10;
+      const __half2 s = *reinterpret_cast<const __half2*>(&sbits);
+      const __half2 off = __hmul2(s, __float2half2_rn(-1152.f));
+      const uint32_t lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t v = __byte_perm(j < 2 ? lo : hi, 0x64646464u, (j & 1) ? 0x4342 : 0x4140);
         const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&v), s, off);
-        out[4 * h + j] = *reinterpret_cast<const uint32_t*>(&x);
+        out[j] = *reinterpret_cast<const uint32_t*>(&x);
       }
+      return;
     }
-  } else {
-    // code + 128 in the fraction of 2^23, less 2^23 + 128: the code; times its
-    // scale: exact in fp32 and, within its range, in the 16-bit type
-    const float s0 = e8m0_value(b0), s1 = e8m0_value(b1);
+  }
+  // code + 128 in the fraction of 2^23, less 2^23 + 128: the code; times its
+  // scale: exact in fp32 and, within its range, in the 16-bit type
+  const float f0 = e8m0_value(s0), f1 = e8m0_value(s1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = __uint_as_float(__byte_perm(a[h], 0x4B000000u, 0x7540 + j)) - 8388736.f;
-        const float y = __uint_as_float(__byte_perm(b[h], 0x4B000000u, 0x7540 + j)) - 8388736.f;
-        out[4 * h + j] = pack2<T>(x * s0, y * s1);
-      }
+  for (int j = 0; j < 4; ++j) {
+    const float x = __uint_as_float(__byte_perm(a, 0x4B000000u, 0x7540 + j)) - 8388736.f;
+    const float y = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540 + j)) - 8388736.f;
+    out[j] = pack2<T>(x * f0, y * f1);
   }
 }
 
@@ -180,15 +175,15 @@ __global__ void __launch_bounds__(WG_THREADS)
   pdl_trigger();
   const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
 
-  float acc[MT][8][4];
+  float acc[MT][4][4];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
   const int g = lane >> 2, c = lane & 3;
-  const int half = warp & 1, part = warp >> 1;  // columns 64 half .. +63; steps 2 part, 2 part + 1
+  const int quarter = warp & 3, part = warp >> 2;  // columns 32 quarter ..; rows 32 part .. of a stage
 
   if (warp == WG_WARPS) {
     // ------------------------------------------------------------ producer
@@ -224,8 +219,8 @@ __global__ void __launch_bounds__(WG_THREADS)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * c + i;
-      at_q[i] = (uint32_t)(t * 128 + (((4 * half + (g >> 1)) ^ t) * 16) + 8 * (g & 1) + part * 4096);
-      at_s[i] = (uint32_t)(C_::Q_BYTES + C_::A_BYTES + t * 16 + 2 * half + (g >> 2) + part * 4);
+      at_q[i] = (uint32_t)(t * 128 + (((2 * quarter + (g >> 2)) ^ t) * 16) + 4 * (g & 3) + part * 4096);
+      at_s[i] = (uint32_t)(C_::Q_BYTES + C_::A_BYTES + t * 16 + quarter + part * 4);
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -252,22 +247,19 @@ __global__ void __launch_bounds__(WG_THREADS)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
           ldmatrix_x4_trans(q + at_a[i] + (uint32_t)(kk * 16 * 32 * MT), am[i]);
-        uint2 w[4];
-        uint32_t sb[4];
+        uint32_t w[4], sb[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t down = (uint32_t)(kk * 16 + 8 * (i >> 1));
-          w[i] = lds64(q + at_q[i & 1] + down * 128u);
-          w[i].x ^= 0x80808080u;
-          w[i].y ^= 0x80808080u;
+          w[i] = lds32(q + at_q[i & 1] + down * 128u) ^ 0x80808080u;
           sb[i] = lds8(s_in + at_s[i & 1] + down * 16u);
         }
-        uint32_t lo[8], hi[8];
+        uint32_t lo[4], hi[4];
         code_pairs<T>(w[0], w[1], sb[0], sb[1], lo);
         code_pairs<T>(w[2], w[3], sb[2], sb[3], hi);
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int i = 0; i < MT; ++i) mma_16<T>(acc[i][j], am[i], lo[j], hi[j]);
       }
@@ -278,17 +270,18 @@ __global__ void __launch_bounds__(WG_THREADS)
   }
   // ------------------------------------------------------------ join
   // the two row halves' sums, then the slices' (the tile's element (i, j, e) is
-  // row 16 i + g + 8 (e / 2), column 64 half + 8 (2 c + e % 2) + j)
+  // row 16 i + g + 8 (e / 2), column 32 quarter + 4 (2 c + e % 2) + j)
   for (int turn = 1; turn >= 0; --turn) {
     if (warp < WG_WARPS && part == turn) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int m = 16 * i + g + 8 * (e >> 1), n = 64 * half + 8 * (2 * c + (e & 1)) + j;
-            const uint32_t at = sums + (uint32_t)((m * COLS + n) * 4);
+            const int m = 16 * i + g + 8 * (e >> 1);
+            const int n = 32 * quarter + 4 * (2 * c + (e & 1)) + j;
+            const uint32_t at = sums + (uint32_t)((m * WG_PITCH + n) * 4);
             float v = acc[i][j][e];
             if (turn == 0) {
               float o;
@@ -306,7 +299,7 @@ __global__ void __launch_bounds__(WG_THREADS)
   for (int i = threadIdx.x; i < n_cnt * p.M; i += WG_THREADS) {
     const int m = i / n_cnt, n = n_lo + i % n_cnt;
     if (n0 + n >= p.N) continue;
-    const uint32_t mine = sums + (uint32_t)((m * COLS + n) * 4);
+    const uint32_t mine = sums + (uint32_t)((m * WG_PITCH + n) * 4);
     float v = 0.f;
     for (int r = 0; r < splits; ++r) {
       float f;
