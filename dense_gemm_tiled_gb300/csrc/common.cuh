@@ -248,6 +248,30 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Element-wise sum, in rank order, of the four floats at this shared address in
+// each of the cluster's first `ranks` (at most 8) blocks, the loads issued
+// together.
+__device__ __forceinline__ float4 cluster_sum4(uint32_t addr, int ranks) {
+  float4 f[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    f[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < ranks) {
+      uint32_t a;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(r));
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(f[r].x), "=f"(f[r].y), "=f"(f[r].z), "=f"(f[r].w)
+                   : "r"(a));
+    }
+  }
+  float4 v = f[0];
+#pragma unroll
+  for (int r = 1; r < 8; ++r) {
+    if (r >= ranks) break;
+    v.x += f[r].x; v.y += f[r].y; v.z += f[r].z; v.w += f[r].w;
+  }
+  return v;
+}
 // Every thread of every block of the cluster arrives and waits (the barrier
 // instructions are warp-aligned, so each warp is reconverged first).
 __device__ __forceinline__ void cluster_sync() {
@@ -435,6 +459,27 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Clusters of `cluster_x` blocks resident at once.  A cluster lives within a
+// GPC, so these are fewer than the SMs' room for its blocks.
+inline int resident_clusters(const void* kern, int cluster_x, int threads, size_t smem) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster_x;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)cluster_x, 1024);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n;
 }
 
 }  // namespace gb300

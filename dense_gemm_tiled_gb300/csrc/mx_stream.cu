@@ -26,6 +26,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "mx_format.cuh"
@@ -118,11 +120,16 @@ __device__ __forceinline__ __half2 e4m3_half2(uint32_t byte) {
 }
 
 template <typename T>
-__device__ __forceinline__ void finish(const SParams& p, int m, int n, float v) {
-  T* c = static_cast<T*>(p.C) + (int64_t)m * p.ldc + n;
-  v *= p.alpha;
-  if (p.beta != 0.f) v = __fmaf_rn(p.beta, MxIo<T>::to(*c), v);
-  *c = MxIo<T>::from(apply_epilogue<T>(v, p.ep, n));
+__device__ __forceinline__ void finish4(const SParams& p, int m, int n, const float4& sum) {
+  T* const c = static_cast<T*>(p.C) + (int64_t)m * p.ldc + n;
+  const float v4[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (n + e >= p.N) break;
+    float v = p.alpha * v4[e];
+    if (p.beta != 0.f) v = __fmaf_rn(p.beta, MxIo<T>::to(c[e]), v);
+    c[e] = MxIo<T>::from(apply_epilogue<T>(v, p.ep, n + e));
+  }
 }
 
 template <int FMT, int XT, int NT>
@@ -319,22 +326,16 @@ __global__ void __launch_bounds__(ST_THREADS)
   // ------------------------------------------------------------ join
   // (a block alone is a cluster of one: the barriers then are the block's)
   cluster_sync();
-  const int share = (ROWS + splits - 1) / splits;
-  const int n_lo = rank * share, n_cnt = min(ROWS, n_lo + share) - n_lo;
+  // (a block finishes its share of the 128 columns, four a thread)
+  const int q_lo = rank * (ROWS / 4) / splits, q_cnt = (rank + 1) * (ROWS / 4) / splits - q_lo;
   const int mc = min(8 * NT, p.M - m0);
-  for (int i = threadIdx.x; i < n_cnt * mc; i += ST_THREADS) {
-    const int m = i / n_cnt, n = n_lo + i % n_cnt;
+  for (int i = threadIdx.x; i < q_cnt * mc; i += ST_THREADS) {
+    const int m = i / q_cnt, n = 4 * (q_lo + i % q_cnt);
     if (n0 + n >= p.N) continue;
-    float v = 0.f;
-    const uint32_t mine = sums + (uint32_t)((m * SUM_PITCH + n) * 4);
-    for (int r = 0; r < splits; ++r) {
-      float f;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(mapa_shared(mine, (uint32_t)r)));
-      v += f;
-    }
-    if (p.out == 0) finish<float>(p, m0 + m, n0 + n, v);
-    else if (p.out == 1) finish<__half>(p, m0 + m, n0 + n, v);
-    else finish<__nv_bfloat16>(p, m0 + m, n0 + n, v);
+    const float4 v = cluster_sum4(sums + (uint32_t)((m * SUM_PITCH + n) * 4), splits);
+    if (p.out == 0) finish4<float>(p, m0 + m, n0 + n, v);
+    else if (p.out == 1) finish4<__half>(p, m0 + m, n0 + n, v);
+    else finish4<__nv_bfloat16>(p, m0 + m, n0 + n, v);
   }
   cluster_sync();  // no block leaves while another reads its sums
 }
@@ -353,16 +354,22 @@ cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
   const int64_t rb = ((int64_t)a.N + ROWS - 1) / ROWS;
   const int64_t mg = ((int64_t)a.M + 8 * NT - 1) / (8 * NT);
   if (rb > 65535 || mg > 65535) return cudaErrorNotSupported;
-  // The most slices of K whose blocks are all resident at once (a slice's
-  // stages, up to the ring, are its block's loads in flight); one where even
-  // that is more than the GPU holds.
+  // The most slices of K whose clusters are all resident at once (a slice's
+  // stages, up to the ring, are its block's loads in flight); one where no split
+  // is.
   int splits = 1;
   p.per = p.stages;
   for (int s = MAX_SPLIT; s > 1; --s) {
     const int per = (p.stages + s - 1) / s, n = (p.stages + per - 1) / per;
     const int ring = per < C_::RING ? per : C_::RING;
-    const int64_t slots = (int64_t)a.num_sms * (SMEM_MAX / (C_::smem(ring) + 1024));
-    if (rb * mg * n <= slots) {
+    // (queried once for each cluster and ring size)
+    static std::atomic<int> slots[MAX_SPLIT + 1][MAX_RING + 1];
+    int have = slots[n][ring].load(std::memory_order_relaxed);
+    if (have == 0) {
+      have = 1 + resident_clusters((const void*)kern, n, ST_THREADS, (size_t)C_::smem(ring));
+      slots[n][ring].store(have, std::memory_order_relaxed);
+    }
+    if (rb * mg < have) {
       splits = n;
       p.per = per;
       break;

@@ -25,6 +25,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -40,9 +41,8 @@ constexpr int TSTEP = 64;   // rows of it a stage holds
 constexpr int WG_WARPS = 8;
 constexpr int WG_THREADS = 32 * (WG_WARPS + 1);
 constexpr int WG_RING = 4;
-constexpr int WG_PITCH = COLS + 2;  // of the sums (fewer lanes a bank)
+constexpr int WG_PITCH = COLS + 4;  // of the sums (a row's start moves by 16 bytes of a bank row)
 constexpr int WG_SPLIT = 8;
-constexpr int WG_SMEM_MAX = 227 * 1024;
 
 template <int MT>
 struct GCfg {
@@ -269,47 +269,47 @@ __global__ void __launch_bounds__(WG_THREADS)
     }
   }
   // ------------------------------------------------------------ join
-  // the two row halves' sums, then the slices' (the tile's element (i, j, e) is
-  // row 16 i + g + 8 (e / 2), column 32 quarter + 4 (2 c + e % 2) + j)
+  // the two row halves' sums, then the slices' (element (i, j, e) of the warp's
+  // tiles is row 16 i + g + 8 (e / 2), column 32 quarter + 4 (2 c + e % 2) + j)
   for (int turn = 1; turn >= 0; --turn) {
     if (warp < WG_WARPS && part == turn) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int e = 0; e < 4; ++e) {
+          const int m = 16 * i + g + 8 * (e >> 1), n = 32 * quarter + 4 * (2 * c + (e & 1));
+          const uint32_t at = sums + (uint32_t)((m * WG_PITCH + n) * 4);
+          float v[4] = {acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]};
+          if (turn == 0) {
+            float o[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
+                         : "r"(at));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = 16 * i + g + 8 * (e >> 1);
-            const int n = 32 * quarter + 4 * (2 * c + (e & 1)) + j;
-            const uint32_t at = sums + (uint32_t)((m * WG_PITCH + n) * 4);
-            float v = acc[i][j][e];
-            if (turn == 0) {
-              float o;
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(o) : "r"(at));
-              v += o;
-            }
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v));
+            for (int j = 0; j < 4; ++j) v[j] += o[j];
           }
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]),
+                       "f"(v[2]), "f"(v[3]));
+        }
     }
     if (turn == 1) __syncthreads();
   }
   cluster_sync();
-  const int share = (COLS + splits - 1) / splits;
-  const int n_lo = rank * share, n_cnt = min(COLS, n_lo + share) - n_lo;
-  for (int i = threadIdx.x; i < n_cnt * p.M; i += WG_THREADS) {
-    const int m = i / n_cnt, n = n_lo + i % n_cnt;
+  // (a block finishes its share of the 128 columns, four a thread)
+  const int q_lo = rank * (COLS / 4) / splits, q_cnt = (rank + 1) * (COLS / 4) / splits - q_lo;
+  for (int i = threadIdx.x; i < q_cnt * p.M; i += WG_THREADS) {
+    const int m = i / q_cnt, n = 4 * (q_lo + i % q_cnt);
     if (n0 + n >= p.N) continue;
-    const uint32_t mine = sums + (uint32_t)((m * WG_PITCH + n) * 4);
-    float v = 0.f;
-    for (int r = 0; r < splits; ++r) {
-      float f;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(mapa_shared(mine, (uint32_t)r)));
-      v += f;
+    const float4 sum = cluster_sum4(sums + (uint32_t)((m * WG_PITCH + n) * 4), splits);
+    const float v4[4] = {sum.x, sum.y, sum.z, sum.w};
+    T* const dst = static_cast<T*>(p.C) + (int64_t)m * p.ldc + n0 + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (n0 + n + e >= p.N) break;
+      float v = p.alpha * v4[e];
+      if (p.beta != 0.f) v = __fmaf_rn(p.beta, MxIo<T>::to(dst[e]), v);
+      dst[e] = MxIo<T>::from(apply_epilogue<T>(v, p.ep, n0 + n + e));
     }
-    T* dst = static_cast<T*>(p.C) + (int64_t)m * p.ldc + n0 + n;
-    v *= p.alpha;
-    if (p.beta != 0.f) v = __fmaf_rn(p.beta, MxIo<T>::to(*dst), v);
-    *dst = MxIo<T>::from(apply_epilogue<T>(v, p.ep, n0 + n));
   }
   cluster_sync();
 }
@@ -326,14 +326,20 @@ cudaError_t launch_wgrad(const MxStreamArgs& a, LaunchCtx& ctx) {
   p.stages = (a.K + TSTEP - 1) / TSTEP;
   const int64_t cb = ((int64_t)a.N + COLS - 1) / COLS;
   if (cb > 65535) return cudaErrorNotSupported;
-  // the most slices of T whose blocks are all resident at once
+  // the most slices of T whose clusters are all resident at once (queried once
+  // for each cluster and ring size)
   int splits = 1;
   p.per = p.stages;
   for (int s = WG_SPLIT; s > 1; --s) {
     const int per = (p.stages + s - 1) / s, n = (p.stages + per - 1) / per;
     const int ring = per < WG_RING ? per : WG_RING;
-    const int64_t slots = (int64_t)a.num_sms * (WG_SMEM_MAX / (C_::smem(ring) + 1024));
-    if (cb * n <= slots) {
+    static std::atomic<int> slots[WG_SPLIT + 1][WG_RING + 1];
+    int have = slots[n][ring].load(std::memory_order_relaxed);
+    if (have == 0) {
+      have = 1 + resident_clusters((const void*)kern, n, WG_THREADS, (size_t)C_::smem(ring));
+      slots[n][ring].store(have, std::memory_order_relaxed);
+    }
+    if (cb < have) {
       splits = n;
       p.per = per;
       break;
