@@ -59,35 +59,56 @@ __device__ __forceinline__ uint32_t max_abs_bits(const float (&x)[16]) {
   return m;
 }
 
-// c = erfc(|x| / sqrt 2) / 2 = Phi(-|x|) and e = exp(-x^2 / 2), which the gelu
-// and its derivative share:  erfc(z) = t (a1 + t (a2 + ... )) exp(-z^2), t = 1 /
-// (1 + p z), within 1.5e-7 (M. Abramowitz and I. Stegun, "Handbook of
-// Mathematical Functions", 7.1.26).  One exponential, one reciprocal and nine
-// other instructions; with erff and expf these kernels were bound by arithmetic
-// (16384 x 5632 bf16, forward and backward: 465 us against 257).
-__device__ __forceinline__ float normal_tail(float x, float& e) {
-  float t;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f * 0.70710678f, fabsf(x), 1.f)));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-0.72134752f * x * x));
-  float c = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-  c = fmaf(t, c, 0.5f * 1.421413741f);
-  c = fmaf(t, c, 0.5f * -0.284496736f);
-  c = fmaf(t, c, 0.5f * 0.254829592f);
-  return t * c * e;
+// For a pair x, given as n = -|x|: c = erfc(|x| / sqrt 2) / 2 = Phi(-|x|) and
+// e = exp(-x^2 / 2), which the gelu and its derivative share:
+//   erfc(z) = t (a1 + t (a2 + ... )) exp(-z^2),  t = 1 / (1 + p z),
+// within 1.5e-7 (M. Abramowitz and I. Stegun, "Handbook of Mathematical
+// Functions", 7.1.26).  A value costs an exponential, a reciprocal and five
+// paired operations; with erff and expf, the forward and backward pass at 16384
+// x 5632 bf16 took 465 us against 232 with scalar operations of this form.
+__device__ __forceinline__ f32x2 normal_tail2(f32x2 n, f32x2& e) {
+  float a, b;
+  unpair(fma2(n, pair(-0.3275911f * 0.70710678f), pair(1.f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  const f32x2 t = pair(a, b);
+  unpair(mul2(mul2(n, n), pair(-0.72134752f)), a, b);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+  e = pair(a, b);
+  f32x2 c = fma2(t, pair(0.5f * 1.061405429f), pair(0.5f * -1.453152027f));
+  c = fma2(t, c, pair(0.5f * 1.421413741f));
+  c = fma2(t, c, pair(0.5f * -0.284496736f));
+  c = fma2(t, c, pair(0.5f * 0.254829592f));
+  return mul2(mul2(t, c), e);
+}
+// -|x|, not below -64 (where c and e are 0 already), so that an infinity meets no
+// 0; a NaN stays one
+__device__ __forceinline__ float minus_abs(float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(-fabsf(x)), "f"(-64.f));
+  return r;
 }
 template <int ACT>
-__device__ __forceinline__ float act_value(float x) {
-  if (ACT == 1) return x > 0.f ? x : 0.f;
-  if (ACT == 2) {  // x Phi(x) = max(x, 0) - |x| Phi(-|x|)
-    float e;
-    const float c = normal_tail(x, e);
-    return fmaf(-fabsf(x), c, x > 0.f ? x : 0.f);
+__device__ __forceinline__ void act_values(const float (&x)[16], float (&y)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float m0 = x[i] > 0.f ? x[i] : 0.f, m1 = x[i + 1] > 0.f ? x[i + 1] : 0.f;
+    if (ACT == 2) {  // x Phi(x) = max(x, 0) - |x| Phi(-|x|)
+      const f32x2 n = pair(minus_abs(x[i]), minus_abs(x[i + 1]));
+      f32x2 e;
+      const f32x2 c = normal_tail2(n, e);
+      unpair(fma2(n, c, pair(m0, m1)), y[i], y[i + 1]);
+    } else {
+      y[i] = ACT == 1 ? m0 : x[i];
+      y[i + 1] = ACT == 1 ? m1 : x[i + 1];
+    }
   }
-  return x;
 }
 
 // ACT: the activation of Y, or -1 without Y
-template <typename T, int FMT, int ACT>
+// MULT: whether mult differs from 1
+template <typename T, int FMT, int ACT, bool MULT>
 __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) mx_quantize_kernel(const QuantParams p) {
   pdl_wait();
   pdl_trigger();
@@ -116,13 +137,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) mx_quantize_kernel(con
       mx_unpack16<T>(in[j], x);
       if (ACT >= 0 && real) {
         float y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = act_value<ACT>(x[i]);
+        act_values<ACT>(x, y);
         mx_store16<T>(static_cast<T*>(p.Y) + r * p.ldy + c0, n, p.vec_y, y);
       }
       // (the largest of |mult x| is |mult| times the largest |x|: rounding keeps order)
       uint32_t m = mx_max_abs16<T>(in[j]);
-      if (p.mult != 1.f) {
+      if (MULT) {
         m = scale_bits(m, p.mult);
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] *= p.mult;
@@ -158,7 +178,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) mx_quantize_kernel(con
 // row segments.
 constexpr int TT_ROWS = 64, TT_COLS = 128, TT_THREADS = 128;
 
-template <typename T, int FMT>
+template <typename T, int FMT, bool MULT>
 __global__ void __launch_bounds__(TT_THREADS) mx_quantize_t_kernel(const QuantParams p) {
   constexpr int ROW_BYTES = TT_COLS / 16 * mx_bytes16<FMT>();
   constexpr int PITCH = ROW_BYTES + 16;  // (rows two apart in different banks)
@@ -195,8 +215,12 @@ __global__ void __launch_bounds__(TT_THREADS) mx_quantize_t_kernel(const QuantPa
       float lo[16], hi[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        lo[i] = MxIo<T>::to(h ? in[i].b : in[i].a) * p.mult;
-        hi[i] = MxIo<T>::to(h ? in[16 + i].b : in[16 + i].a) * p.mult;
+        lo[i] = MxIo<T>::to(h ? in[i].b : in[i].a);
+        hi[i] = MxIo<T>::to(h ? in[16 + i].b : in[16 + i].a);
+        if (MULT) {
+          lo[i] *= p.mult;
+          hi[i] *= p.mult;
+        }
       }
       uint32_t ml = max_abs_bits(lo), mh = max_abs_bits(hi);
       if (mx_block(FMT) == 32) ml = mh = max(ml, mh);
@@ -291,38 +315,54 @@ struct ActBwdParams {
   void* dX;
   int64_t lddx;
   float* part;  // [blocks of a strip][cols] column sums, or null
+  float* dbias; // the sums themselves, where a strip's blocks are a cluster
   int64_t tiles_m;
   int vec_in, vec_out;
 };
 
-// act'(x): relu 1 where x > 0; gelu Phi(x) + x phi(x), the derivative of
-// x Phi(x)
+// dy act'(x): relu 1 where x > 0; gelu Phi(x) + x phi(x), the derivative of x
+// Phi(x), which is h = Phi(-|x|) - |x| phi(x) where x < 0 and 1 - h elsewhere.
 template <int ACT>
-__device__ __forceinline__ float act_slope(float x) {
-  if (ACT == 1) return x > 0.f ? 1.f : 0.f;
-  if (ACT == 2) {
-    float e;
-    const float c = normal_tail(x, e);
-    return fmaf(0.39894228040143268f * x, e, x < 0.f ? c : 1.f - c);
+__device__ __forceinline__ void act_gradients(const float (&x)[16], float (&dy)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    if (ACT == 1) {
+      dy[i] *= x[i] > 0.f ? 1.f : 0.f;
+      dy[i + 1] *= x[i + 1] > 0.f ? 1.f : 0.f;
+    } else if (ACT == 2) {
+      const f32x2 n = pair(minus_abs(x[i]), minus_abs(x[i + 1]));
+      f32x2 e;
+      const f32x2 c = normal_tail2(n, e);
+      const f32x2 h = fma2(mul2(n, pair(0.39894228f)), e, c);
+      float h0, h1, g0, g1;
+      unpair(h, h0, h1);
+      unpair(fma2(h, pair(-1.f), pair(1.f)), g0, g1);
+      const f32x2 s = pair(x[i] < 0.f ? h0 : g0, x[i + 1] < 0.f ? h1 : g1);
+      unpair(mul2(pair(dy[i], dy[i + 1]), s), dy[i], dy[i + 1]);
+    }
   }
-  return 1.f;
 }
 
-template <typename T, int ACT>
+// JOINED: a strip's blocks are a cluster (grid: blocks x strips), which joins
+// their column sums; otherwise (grid: strips x blocks) they go to `part`.
+template <typename T, int ACT, bool JOINED>
 __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM - 1)
     mx_act_backward_kernel(const ActBwdParams p) {
-  __shared__ float colsum[8][STRIP];
+  __shared__ __align__(16) float colsum[8][STRIP];
+  const unsigned strip = JOINED ? blockIdx.y : blockIdx.x;
+  const unsigned first = JOINED ? blockIdx.x : blockIdx.y;
+  const unsigned step = JOINED ? gridDim.x : gridDim.y;
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = lane & 7;
-  const int64_t cc0 = (int64_t)blockIdx.x * STRIP, c0 = cc0 + u * 16;
+  const int64_t cc0 = (int64_t)strip * STRIP, c0 = cc0 + u * 16;
   const int n = (int)min((int64_t)16, max((int64_t)0, (int64_t)p.cols - c0));
   const int64_t b = c0 / 32;
-  float sum[16];
+  f32x2 sum[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sum[i] = 0.f;
-  for (int64_t tm = blockIdx.y; n > 0 && tm < p.tiles_m; tm += gridDim.y) {
+  for (int i = 0; i < 8; ++i) sum[i] = 0ull;
+  for (int64_t tm = first; n > 0 && tm < p.tiles_m; tm += step) {
     const int64_t r0 = tm * TILE_ROWS + warp * 4 * UNITS + (lane >> 3);
     MxRow16<T> in[UNITS];
     MxCodes<MX_INT8> c[UNITS];
@@ -343,28 +383,44 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM - 1)
       float dy[16], x[16];
       mx_unpack16<T>(in[j], dy);  // (absent columns 0)
       mx_decode16<MX_INT8>(c[j], e8m0_value(byte[j]), x);
+      act_gradients<ACT>(x, dy);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        dy[i] *= act_slope<ACT>(x[i]);
-        sum[i] += dy[i];
-      }
+      for (int i = 0; i < 8; ++i) sum[i] = add2(sum[i], pair(dy[2 * i], dy[2 * i + 1]));
       mx_store16<T>(static_cast<T*>(p.dX) + r * p.lddx + c0, n, p.vec_out, dy);
     }
   }
-  if (p.part) {
+  if (JOINED || p.part) {
     // the warp's rows, then the block's, in a fixed order
+    float v16[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) unpair(sum[i], v16[2 * i], v16[2 * i + 1]);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
-      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
-      if (lane < 8) colsum[warp][u * 16 + i] = sum[i];
+      v16[i] += __shfl_xor_sync(0xffffffffu, v16[i], 8);
+      v16[i] += __shfl_xor_sync(0xffffffffu, v16[i], 16);
+      if (lane < 8) colsum[warp][u * 16 + i] = v16[i];
     }
     __syncthreads();
-    if (threadIdx.x < STRIP && cc0 + threadIdx.x < p.cols) {
-      float v = 0.f;
+    float v = 0.f;
+    if (threadIdx.x < STRIP) {
 #pragma unroll
       for (int w = 0; w < 8; ++w) v += colsum[w][threadIdx.x];
-      p.part[blockIdx.y * (int64_t)p.cols + cc0 + threadIdx.x] = v;
+    }
+    if constexpr (JOINED) {
+      __syncthreads();
+      if (threadIdx.x < STRIP) colsum[0][threadIdx.x] = v;
+      cluster_sync();
+      if (first == 0 && threadIdx.x < STRIP / 4) {
+        const int64_t c = cc0 + 4 * threadIdx.x;
+        const float4 s = cluster_sum4(smem_u32(&colsum[0][4 * threadIdx.x]), (int)step);
+        if (c < p.cols) p.dbias[c] = s.x;
+        if (c + 1 < p.cols) p.dbias[c + 1] = s.y;
+        if (c + 2 < p.cols) p.dbias[c + 2] = s.z;
+        if (c + 3 < p.cols) p.dbias[c + 3] = s.w;
+      }
+      cluster_sync();  // no block leaves while its sums are read
+    } else if (threadIdx.x < STRIP && cc0 + threadIdx.x < p.cols) {
+      p.part[first * (int64_t)p.cols + cc0 + threadIdx.x] = v;
     }
   }
 }
@@ -390,15 +446,14 @@ inline unsigned grid_of(int64_t tiles) {
   return (unsigned)(tiles < (1ll << 30) ? tiles : (1ll << 30));
 }
 // Column strips x blocks a strip: one row tile a block while that fits the GPU
-// `per_sm` blocks deep, else equal numbers of row tiles in about that many
-// blocks.
+// `per_sm` blocks deep, else equal numbers of row tiles in no more blocks than
+// are resident at once (a few blocks more would run alone after the others).
 dim3 strip_grid(int64_t cols, int64_t tiles_m, int sms, int per_sm) {
   const int64_t strips = (cols + STRIP - 1) / STRIP;
-  const int64_t room = (int64_t)sms * per_sm;
-  const int64_t iters = (strips * tiles_m + room - 1) / room;
-  int64_t blocks = (tiles_m + iters - 1) / iters;
-  if (blocks > 65535) blocks = 65535;
-  return dim3((unsigned)strips, (unsigned)blocks);
+  int64_t most = (int64_t)sms * per_sm / strips;
+  most = most < 1 ? 1 : most < tiles_m ? most : tiles_m;
+  const int64_t iters = (tiles_m + most - 1) / most;
+  return dim3((unsigned)strips, (unsigned)((tiles_m + iters - 1) / iters));
 }
 
 template <typename T, int FMT>
@@ -419,17 +474,23 @@ cudaError_t quantize_t(const MxQuantArgs& a, LaunchCtx& ctx) {
     p.tiles_n = ((int64_t)a.cols + TT_COLS - 1) / TT_COLS;
     p.tiles = rows128 * (128 / TT_ROWS) * p.tiles_n;
     ctx.grid = (int)grid_of(p.tiles);
-    e = launch_kernel(mx_quantize_t_kernel<T, FMT>, dim3(ctx.grid), dim3(TT_THREADS), 0,
-                      ctx.stream, 1, p);
+    auto kern = a.mult == 1.f ? mx_quantize_t_kernel<T, FMT, false>
+                              : mx_quantize_t_kernel<T, FMT, true>;
+    e = launch_kernel(kern, dim3(ctx.grid), dim3(TT_THREADS), 0, ctx.stream, 1, p);
   } else {
     p.vec_x = vec_of(a.X, a.ldx, sizeof(T));
     p.tiles_m = rows128 * (128 / TILE_ROWS);
     const dim3 grid = strip_grid(a.cols, p.tiles_m, a.num_sms, BLOCKS_PER_SM);
     ctx.grid = (int)(grid.x * grid.y);
-    auto kern = !a.Y         ? mx_quantize_kernel<T, FMT, -1>
-                : a.act == 2 ? mx_quantize_kernel<T, FMT, 2>
-                : a.act == 1 ? mx_quantize_kernel<T, FMT, 1>
-                             : mx_quantize_kernel<T, FMT, 0>;
+    const int act = a.Y ? a.act : -1;
+    auto kern = a.mult == 1.f ? (act == 2   ? mx_quantize_kernel<T, FMT, 2, false>
+                                 : act == 1 ? mx_quantize_kernel<T, FMT, 1, false>
+                                 : act == 0 ? mx_quantize_kernel<T, FMT, 0, false>
+                                            : mx_quantize_kernel<T, FMT, -1, false>)
+                              : (act == 2   ? mx_quantize_kernel<T, FMT, 2, true>
+                                 : act == 1 ? mx_quantize_kernel<T, FMT, 1, true>
+                                 : act == 0 ? mx_quantize_kernel<T, FMT, 0, true>
+                                            : mx_quantize_kernel<T, FMT, -1, true>);
     e = launch_kernel(kern, grid, dim3(THREADS), 0, ctx.stream, 1, p);
   }
   if (e == cudaSuccess) ctx.launches++;
@@ -454,6 +515,10 @@ cudaError_t dequantize_t(const MxDequantArgs& a, LaunchCtx& ctx) {
   return e;
 }
 
+// Up to 8 blocks a strip (the portable cluster) join their column sums
+// themselves; more leave them for a second kernel (512 x 5632, 8 blocks a strip:
+// two launches for the forward and backward pass instead of three).
+inline bool act_joined(const dim3& grid) { return grid.y <= 8 && grid.x <= 65535; }
 inline int64_t act_tiles(int rows) { return ((int64_t)rows + TILE_ROWS - 1) / TILE_ROWS; }
 
 template <typename T>
@@ -466,19 +531,27 @@ cudaError_t act_backward_t(const MxActBwdArgs& a, LaunchCtx& ctx) {
   p.rows = a.rows; p.cols = a.cols;
   p.dX = a.dX; p.lddx = a.lddx;
   p.part = a.dbias ? a.part : nullptr;
+  p.dbias = a.dbias;
   p.vec_in = vec_of(a.dY, a.lddy, sizeof(T));
   p.vec_out = vec_of(a.dX, a.lddx, sizeof(T));
   p.tiles_m = act_tiles(a.rows);
   const dim3 grid = strip_grid(a.cols, p.tiles_m, a.num_sms, BLOCKS_PER_SM - 1);
   ctx.grid = (int)(grid.x * grid.y);
-  auto kern = a.act == 2   ? mx_act_backward_kernel<T, 2>
-              : a.act == 1 ? mx_act_backward_kernel<T, 1>
-                           : mx_act_backward_kernel<T, 0>;
-  // (a strip with one block has its sums at once)
-  if (a.dbias && grid.y == 1) p.part = a.dbias;
-  cudaError_t e = launch_kernel(kern, grid, dim3(THREADS), 0, ctx.stream, 1, p);
+  cudaError_t e;
+  if (a.dbias && act_joined(grid)) {
+    auto kern = a.act == 2   ? mx_act_backward_kernel<T, 2, true>
+                : a.act == 1 ? mx_act_backward_kernel<T, 1, true>
+                             : mx_act_backward_kernel<T, 0, true>;
+    e = launch_kernel(kern, dim3(grid.y, grid.x), dim3(THREADS), 0, ctx.stream, (int)grid.y, p);
+    if (e == cudaSuccess) ctx.launches++;
+    return e;
+  }
+  auto kern = a.act == 2   ? mx_act_backward_kernel<T, 2, false>
+              : a.act == 1 ? mx_act_backward_kernel<T, 1, false>
+                           : mx_act_backward_kernel<T, 0, false>;
+  e = launch_kernel(kern, grid, dim3(THREADS), 0, ctx.stream, 1, p);
   if (e == cudaSuccess) ctx.launches++;
-  if (e == cudaSuccess && a.dbias && grid.y > 1) {
+  if (e == cudaSuccess && a.dbias) {
     e = launch_kernel(mx_column_sum_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(64), 0,
                       ctx.stream, 1, (const float*)a.part, (int)grid.y, a.cols, a.dbias);
     if (e == cudaSuccess) ctx.launches++;
@@ -511,7 +584,7 @@ cudaError_t launch_mx_dequantize(const MxDequantArgs& a, LaunchCtx& ctx) {
 }
 size_t mx_act_backward_scratch(int rows, int cols, int num_sms) {
   const dim3 grid = strip_grid(cols, act_tiles(rows), num_sms, BLOCKS_PER_SM - 1);
-  return grid.y > 1 ? (size_t)grid.y * cols * sizeof(float) : 0;
+  return act_joined(grid) ? 0 : (size_t)grid.y * cols * sizeof(float);
 }
 cudaError_t launch_mx_act_backward(const MxActBwdArgs& a, LaunchCtx& ctx) {
   switch (a.out) {

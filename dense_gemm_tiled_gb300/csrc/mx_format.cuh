@@ -74,6 +74,35 @@ __device__ __forceinline__ uint32_t mx_scale_byte(float amax) {
   return e > 0 ? (uint32_t)e : 0u;
 }
 
+// ---------------------------------------------------------------- pairs of fp32
+// Two IEEE fp32 operations an instruction; the elementwise kernels are near the
+// issue limit, so they work on pairs throughout.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 pair(float v) { return pair(v, v); }
+__device__ __forceinline__ void unpair(f32x2 p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // ---------------------------------------------------------------- elements
 // eight fp32 values -> eight e2m1 codes, the first in the lowest half byte
 // (nearest, ties to even, at most 6)
@@ -109,7 +138,7 @@ struct MxCodes {
 };
 
 // Codes of x / scale, the scale's byte already chosen from the block; `amax`
-// the block's largest magnitude.
+// the block's largest magnitude.  Whole warps.
 template <int FMT>
 __device__ __forceinline__ void mx_encode16(const float (&x)[16], uint32_t byte, float amax,
                                             MxCodes<FMT>& c) {
@@ -128,10 +157,11 @@ __device__ __forceinline__ void mx_encode16(const float (&x)[16], uint32_t byte,
       for (int i = 0; i < 16; ++i) y[i] = copysignf(0.f, x[i]);
     } else {
       const float r = __frcp_rn(s);
+      const f32x2 r2 = pair(r), s2 = pair(-s);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float y0 = __fmul_rn(x[i], r);
-        y[i] = __fmaf_rn(__fmaf_rn(-y0, s, x[i]), r, y0);
+      for (int i = 0; i < 16; i += 2) {
+        const f32x2 v = pair(x[i], x[i + 1]), y0 = mul2(v, r2);
+        unpair(fma2(fma2(y0, s2, v), r2, y0), y[i], y[i + 1]);
       }
     }
     c.w[0] = e2m1_word(y);
@@ -146,24 +176,27 @@ __device__ __forceinline__ void mx_encode16(const float (&x)[16], uint32_t byte,
       // two's complement in the low byte; only a block whose amax lies within
       // half a step of 128 can round to +-128, which saturates
       constexpr float ROUND = 12582912.f;
-      const bool sat = amax * inv >= 127.5f;
+      const f32x2 inv2 = pair(inv), round2 = pair(ROUND);
+      float f[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t v[4];
+      for (int i = 0; i < 16; i += 2)
+        unpair(fma2(pair(x[i], x[i + 1]), inv2, round2), f[i], f[i + 1]);
+      if (__any_sync(0xffffffffu, amax * inv >= 127.5f)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float f = __fmaf_rn(x[4 * i + j], inv, ROUND);
-          if (sat) f = fminf(fmaxf(f, ROUND - 127.f), ROUND + 127.f);
-          v[j] = __float_as_uint(f);
-        }
-        c.w[i] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040),
-                             0x5410);
-        if (byte == 255u) c.w[i] = 0u;
+        for (int i = 0; i < 16; ++i) f[i] = fminf(fmaxf(f[i], ROUND - 127.f), ROUND + 127.f);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c.w[i] = __byte_perm(
+            __byte_perm(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), 0x0040),
+            __byte_perm(__float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]), 0x0040),
+            0x5410);
+      if (byte == 255u) c.w[0] = c.w[1] = c.w[2] = c.w[3] = 0u;
     } else {
       float y[16];
+      const f32x2 inv2 = pair(inv);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = x[i] * inv;
+      for (int i = 0; i < 16; i += 2) unpair(mul2(pair(x[i], x[i + 1]), inv2), y[i], y[i + 1]);
       c.w[0] = e2m1_word(y);
       c.w[1] = e2m1_word(y + 8);
       if (byte == 255u) c.w[0] = c.w[1] = 0u;
@@ -179,17 +212,21 @@ __device__ __forceinline__ void mx_decode16(const MxCodes<FMT>& c, float scale, 
     // overflow the second product; from there on it multiplies the code.)
     constexpr float BASE = 8388736.f;
     const bool big = !(scale < 1.0e31f);
-    const float s = big ? 1.f : scale, off = -BASE * s;
+    const float s = big ? 1.f : scale;
+    const f32x2 s2 = pair(s), off2 = pair(-BASE * s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = c.w[i] ^ 0x80808080u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t v = __byte_perm(w, 0x4B000000u, 0x7540 + j);
-        x[4 * i + j] = __fmaf_rn(__uint_as_float(v), s, off);
-      }
+      for (int j = 0; j < 4; j += 2)
+        unpair(fma2(pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + j)),
+                         __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7541 + j))),
+                    s2, off2),
+               x[4 * i + j], x[4 * i + j + 1]);
     }
-    if (big) {
+    if (__any_sync(__activemask(), big)) {
+      // (the others of the warp multiply by 1)
+      scale = big ? scale : 1.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] *= scale;
     }
@@ -201,8 +238,7 @@ __device__ __forceinline__ void mx_decode16(const MxCodes<FMT>& c, float scale, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-        x[8 * i + 2 * j] = f.x * scale;
-        x[8 * i + 2 * j + 1] = f.y * scale;
+        unpair(mul2(pair(f.x, f.y), pair(scale)), x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
       }
     }
   }
@@ -280,27 +316,36 @@ __device__ __forceinline__ void mx_load_units(const T* p, const int64_t (&row)[U
 }
 
 // Largest magnitude of 16 loaded values, as fp32 bits: a NaN counts above
-// infinity, infinity above all numbers.  16-bit types compare their magnitude's
-// bits two at a time.
+// infinity, infinity above all numbers.  16-bit types two at a time.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b, __half*) {
+  const __half2 r = __hmax2_nan(__habs2(*reinterpret_cast<const __half2*>(&a)),
+                                __habs2(*reinterpret_cast<const __half2*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b, __nv_bfloat16*) {
+  const __nv_bfloat162 r = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 template <typename T>
 __device__ __forceinline__ uint32_t mx_max_abs16(const MxRow16<T>& r) {
+  uint32_t m = 0;
   if constexpr (sizeof(T) == 4) {
-    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < MxRow16<T>::VECS; ++i)
       m = max(max(max(m, r.v[i].x & 0x7FFFFFFFu), r.v[i].y & 0x7FFFFFFFu),
               max(r.v[i].z & 0x7FFFFFFFu, r.v[i].w & 0x7FFFFFFFu));
     return m;
   } else {
-    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < MxRow16<T>::VECS; ++i) {
-      m = __vmaxu2(m, r.v[i].x & 0x7FFF7FFFu);
-      m = __vmaxu2(m, r.v[i].y & 0x7FFF7FFFu);
-      m = __vmaxu2(m, r.v[i].z & 0x7FFF7FFFu);
-      m = __vmaxu2(m, r.v[i].w & 0x7FFF7FFFu);
+      m = max_abs2(m, r.v[i].x, (T*)nullptr);
+      m = max_abs2(m, r.v[i].y, (T*)nullptr);
+      m = max_abs2(m, r.v[i].z, (T*)nullptr);
+      m = max_abs2(m, r.v[i].w, (T*)nullptr);
     }
-    const unsigned short h = (unsigned short)max(m & 0xFFFFu, m >> 16);
+    // (as bits: a NaN's above infinity's)
+    const unsigned short h = (unsigned short)max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
     T e;
     memcpy(&e, &h, 2);
     return __float_as_uint(MxIo<T>::to(e)) & 0x7FFFFFFFu;

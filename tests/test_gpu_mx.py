@@ -408,3 +408,27 @@ def test_bounded_waits(lib_path, gpu, case):
     call()
     assert g.check_device_status() == g.OK
     assert torch.equal(C, want)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_activation_at_the_ends(g, dtype):
+    """gelu far out on both sides, at the type's ends and at infinities; a NaN
+    stays one; an infinite gradient stays infinite where the slope is not 0."""
+    top = torch.finfo(DT[dtype]).max
+    x = torch.tensor([[-top, -100.0, -64.0, -20.0, -8.0, -5.0, -0.0, 0.0, 5.0, 8.0, 20.0, 64.0, 100.0,
+                       top, float("inf"), float("-inf"), float("nan")]]).to(DT[dtype])
+    X = x.cuda()
+    Y, Q = torch.empty_like(X), filled(g, 1, 17, "int8")
+    g.mx_quantize(X, Q, act="gelu", Y=Y)
+    y, want = f64(Y)[0], mx_ref.gelu(f64(x)[0][:14])
+    assert np.all(np.abs(y[:14] - want) <= 2.0 ** -20 * (np.abs(f64(x)[0][:14]) + np.abs(want)) +
+                  2.0 ** -8 * np.abs(want))
+    assert y[14] == np.inf and y[15] == 0.0 and np.isnan(y[16])
+    X = torch.tensor([[-4.0, -1.0, 0.0, 1.0, 4.0, 0.5]], dtype=DT[dtype], device="cuda")
+    dY = torch.tensor([[1.0, 1.0, float("inf"), float("-inf"), float("nan"), 2.0]],
+                      dtype=DT[dtype], device="cuda")
+    Q, dX = filled(g, 1, 6, "int8"), torch.empty_like(dY)
+    g.mx_quantize(X, Q)
+    g.mx_act_backward(dY, Q, dX)
+    d = f64(dX)[0]
+    assert d[2] == np.inf and d[3] == -np.inf and np.isnan(d[4]) and np.isfinite(d[[0, 1, 5]]).all()
