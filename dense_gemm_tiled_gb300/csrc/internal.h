@@ -301,7 +301,20 @@ struct MxStreamArgs {
   Epilogue ep;
   int num_sms;
   int fault_injection;
+  int transA = 0, transB = 1;  // (launch_mx_mixed)
 };
+// The converted product: A of type `out`, 16-byte aligned rows, op(A) op(B).
+// pair: 256 x 256 tiles on block pairs; otherwise 128 columns x mt rows, K in
+// `splits` slices.  cudaErrorNotSupported (nothing launched) for the variants
+// that have no kernel (int8 but tn; transA otherwise).
+struct MixedPlan {
+  bool pair = false;
+  int mt = 128, splits = 1;
+};
+MixedPlan mixed_plan(int M, int N, int K, int num_sms);
+cudaError_t launch_mx_mixed(const MxStreamArgs& a, LaunchCtx& ctx);
+cudaError_t launch_mx_mixed_f16(const MxStreamArgs& a, LaunchCtx& ctx);
+cudaError_t launch_mx_mixed_bf16(const MxStreamArgs& a, LaunchCtx& ctx);
 // cudaErrorNotSupported (nothing launched) where the grid or a tensor map does
 // not take the problem
 cudaError_t launch_mx_stream(const MxStreamArgs& a, LaunchCtx& ctx);

@@ -20,7 +20,7 @@ constexpr int64_t LIM = (int64_t)1 << 31;
 
 // Rows up to which a product streams its 4-bit right operand.
 constexpr int64_t WGRAD_ROWS = 64;  // (columns of A, in the tn product)
-constexpr int64_t STREAM_ROWS = 128, STREAM_ROWS_4 = 32;
+constexpr int64_t STREAM_ROWS = 32, STREAM_ROWS_4 = 32;
 
 inline bool known_format(int f) { return f >= GEMM_MX_FP4 && f <= GEMM_MX_INT8; }
 inline bool known_type(int d) {
@@ -246,7 +246,7 @@ int gemm_mx4(int format, int64_t M, int64_t N, int64_t K, int dtype, float alpha
 int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype,
             float alpha, float beta, const void* A, int64_t lda, const void* B, int64_t ldb,
             const void* Bs, void* C, int64_t ldc, const void* bias, int act,
-            gemm_stream_t stream_) {
+            gemm_stream_t stream_h) {
   api_reset();
   if (!known_format(format) || (transA != 0 && transA != 1) || (transB != 0 && transB != 1))
     return GEMM_ERR_INVALID_ARG;
@@ -255,7 +255,7 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
   const int64_t e = type_bytes(dtype);
   const int64_t ar = transA ? K : M, ac = transA ? M : K;
   const int64_t br = transB ? N : K, bc = transB ? K : N;
-  cudaStream_t stream = (cudaStream_t)stream_;
+  cudaStream_t stream_ = (cudaStream_t)stream_h;
   Epilogue ep;
   ep.bias = bias;
   ep.act = act;
@@ -271,64 +271,56 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
   ApiState st;
   rc = api_state(&st);
   if (rc != GEMM_OK) return rc;
-  LaunchCtx ctx{stream, st.status, st.timeout_ns, 0};
+  LaunchCtx ctx{stream_, st.status, st.timeout_ns, 0};
   if (K == 0)
     return api_done(GEMM_PATH_SCALE, ctx,
                     launch_scale(dtype, (int)M, (int)N, C, ldc, beta, ctx, ep));
-  if (M <= STREAM_ROWS && transB && dtype != GEMM_F32 && format != GEMM_MX_INT8 &&
-      (!transA || M == 1)) {
-    // Few rows: B streamed once.  A's rows go through the tensor-memory-access
-    // unit: rows off 16-byte alignment (and a single row stored as a column) are
-    // copied into scratch first.
+  // 16-bit A: kernels that read B as it is stored.  A's rows go through the
+  // tensor-memory-access unit: rows off 16-byte alignment (and a single row
+  // stored as a column) are copied into scratch first.
+  const bool column = transA && M == 1;  // op(A) is one row
+  const bool fp4 = format != GEMM_MX_INT8;
+  const int tA = column && fp4 ? 0 : transA;
+  const bool stream = fp4 && transB && !tA && M <= STREAM_ROWS;
+  const bool wgrad = !fp4 && tA && !transB && M <= WGRAD_ROWS;
+  const bool converted = fp4 ? !tA : (tA && !transB);
+  if (dtype != GEMM_F32 && (stream || wgrad || converted)) {
     Scratch ws;
     const void* Ad = A;
     int64_t ldad = lda;
     cudaError_t ce = cudaSuccess;
-    const bool column = transA && lda != 1;
-    if (column || ((uintptr_t)A % 16) != 0 || (lda % 8 != 0 && M > 1)) {
-      ldad = (K + 7) / 8 * 8;
-      ce = ws.get((size_t)(M * ldad * 2), stream);
+    const int64_t rows = tA ? K : M, cols = tA ? M : K;
+    const bool strided = column && !tA && lda != 1;
+    if (strided || ((uintptr_t)A % 16) != 0 || (lda % 8 != 0 && rows > 1)) {
+      ldad = (cols + 7) / 8 * 8;
+      ce = ws.get((size_t)(rows * ldad * 2), stream_);
       if (ce == cudaSuccess)
-        ce = column ? launch_copy_rows(2, (int)K, 1, A, lda, ws.ptr, 1, ctx)
-                    : launch_repack_16((int)M, (int)K, A, transA ? K : lda, ws.ptr, ldad, ctx);
+        ce = strided ? launch_copy_rows(2, (int)K, 1, A, lda, ws.ptr, 1, ctx)
+                     : launch_repack_16((int)rows, (int)cols, A, rows == 1 ? cols : lda, ws.ptr,
+                                        ldad, ctx);
       Ad = ws.ptr;
       if (ce != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, ce);
     }
-    if (M == 1) ldad = (K + 7) / 8 * 8;
+    if (rows == 1) ldad = (cols + 7) / 8 * 8;
     MxStreamArgs a{format, dtype, (int)M, (int)N, (int)K, Ad, ldad, nullptr, B, ldb, Bs, C, ldc,
-                   alpha, beta, ep, st.sms, st.fault_injection};
-    ce = launch_mx_stream(a, ctx);
+                   alpha, beta, ep, st.sms, st.fault_injection, tA, transB};
+    ce = cudaErrorNotSupported;
+    if (stream) ce = launch_mx_stream(a, ctx);
+    else if (wgrad) ce = launch_mx_wgrad(a, ctx);
     if (ce != cudaErrorNotSupported) return api_done(GEMM_PATH_MX_STREAM, ctx, ce);
-  }
-  if (M <= WGRAD_ROWS && transA && !transB && dtype != GEMM_F32 && format == GEMM_MX_INT8) {
-    // a low-rank adapter's gradient: the checkpoint streamed once
-    Scratch ws;
-    const void* Ad = A;
-    int64_t ldad = lda;
-    cudaError_t ce = cudaSuccess;
-    if (((uintptr_t)A % 16) != 0 || lda % 8 != 0) {
-      ldad = (M + 7) / 8 * 8;
-      ce = ws.get((size_t)(K * ldad * 2), stream);
-      if (ce == cudaSuccess)
-        ce = launch_repack_16((int)K, (int)M, A, lda, ws.ptr, ldad, ctx);
-      Ad = ws.ptr;
-      if (ce != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, ce);
-    }
-    MxStreamArgs a{format, dtype, (int)M, (int)N, (int)K, Ad, ldad, nullptr, B, ldb, Bs, C, ldc,
-                   alpha, beta, ep, st.sms, st.fault_injection};
-    ce = launch_mx_wgrad(a, ctx);
-    if (ce != cudaErrorNotSupported) return api_done(GEMM_PATH_MX_STREAM, ctx, ce);
+    if (converted) ce = launch_mx_mixed(a, ctx);
+    if (ce != cudaErrorNotSupported) return api_done(GEMM_PATH_MX_CONVERT, ctx, ce);
   }
   // B expanded to the other operand's type in scratch, then that type's product
   const int64_t ldw = (bc + 7) / 8 * 8;
   Scratch ws;
-  cudaError_t ce = ws.get((size_t)(br * ldw * e), stream);
+  cudaError_t ce = ws.get((size_t)(br * ldw * e), stream_);
   if (ce != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, ce);
   MxDequantArgs d{format, dtype, (int)br, (int)bc, B, ldb, Bs, ws.ptr, ldw, st.sms};
   ce = launch_mx_dequantize(d, ctx);
   rc = api_done(GEMM_PATH_NONE, ctx, ce);
   if (rc != GEMM_OK) return rc;
-  rc = api_gemm(transA, transB, M, N, K, dtype, alpha, beta, A, lda, ws.ptr, ldw, C, ldc, stream,
+  rc = api_gemm(transA, transB, M, N, K, dtype, alpha, beta, A, lda, ws.ptr, ldw, C, ldc, stream_,
                 ep);
   if (rc == GEMM_OK) api_add_launches(ctx.launches);
   return rc;

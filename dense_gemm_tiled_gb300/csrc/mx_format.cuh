@@ -207,28 +207,19 @@ __device__ __forceinline__ void mx_encode16(const float (&x)[16], uint32_t byte,
 template <int FMT>
 __device__ __forceinline__ void mx_decode16(const MxCodes<FMT>& c, float scale, float (&x)[16]) {
   if constexpr (FMT == MX_INT8) {
-    // code + 128 as the low byte of 2^23 is an fp32 number: (2^23 + 128 + code)
-    // s - (2^23 + 128) s in one FMA is code * s.  (A scale above 2^103 would
-    // overflow the second product; from there on it multiplies the code.)
-    constexpr float BASE = 8388736.f;
-    const bool big = !(scale < 1.0e31f);
-    const float s = big ? 1.f : scale;
-    const f32x2 s2 = pair(s), off2 = pair(-BASE * s);
+    // code + 128 as the low byte of 2^23 is an fp32 number; less 2^23 + 128 it is
+    // the code
+    const f32x2 base2 = pair(-8388736.f), s2 = pair(scale);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = c.w[i] ^ 0x80808080u;
 #pragma unroll
       for (int j = 0; j < 4; j += 2)
-        unpair(fma2(pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + j)),
-                         __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7541 + j))),
-                    s2, off2),
+        unpair(mul2(add2(pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + j)),
+                              __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7541 + j))),
+                         base2),
+                    s2),
                x[4 * i + j], x[4 * i + j + 1]);
-    }
-    if (__any_sync(__activemask(), big)) {
-      // (the others of the warp multiply by 1)
-      scale = big ? scale : 1.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] *= scale;
     }
   } else {
 #pragma unroll

@@ -370,7 +370,9 @@ typedef enum {
     GEMM_PATH_PER_ENTRY = 8,   /* strided batch run entry by entry (unaligned operands) */
     GEMM_PATH_MX = 9,          /* microscaled storage: quantise, dequantise, act backward */
     GEMM_PATH_MX_TC = 10,      /* product of 4-bit operands: block-scaled tcgen05 kernel */
-    GEMM_PATH_MX_STREAM = 11   /* few rows times a stored right operand, read once */
+    GEMM_PATH_MX_STREAM = 11,  /* few rows times a stored right operand, read once */
+    GEMM_PATH_MX_CONVERT = 12  /* 16-bit rows times a stored right operand, converted inside
+                                  the tcgen05 kernel */
 } gemm_path_t;
 
 int gemm_last_path(void);

@@ -432,3 +432,30 @@ def test_activation_at_the_ends(g, dtype):
     g.mx_act_backward(dY, Q, dX)
     d = f64(dX)[0]
     assert d[2] == np.inf and d[3] == -np.inf and np.isnan(d[4]) and np.isfinite(d[[0, 1, 5]]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt,variant,M,N,K", [
+    ("fp4", "nt", 700, 600, 2100), ("fp4_e4m3", "nt", 513, 1000, 777), ("fp4", "nn", 300, 900, 1300),
+    ("fp4_e4m3", "nn", 130, 515, 2050), ("int8", "tn", 900, 700, 1000), ("int8", "tn", 66, 4000, 130),
+    ("fp4_e4m3", "nn", 1, 3000, 500), ("fp4", "nt", 33, 8000, 96)])
+def test_converted_product(g, dtype, fmt, variant, M, N, K):
+    """The kernel that converts the stored operand: several tiles both ways,
+    ragged, more stages than its ring; the same twice."""
+    tA, tB = variant[0] == "t", variant[1] == "t"
+    r = np.random.default_rng(500 + M)
+    A = matrix(K if tA else M, M if tA else K, dtype, 71)
+    B, b = stored(g, (r.standard_normal((N, K) if tB else (K, N)) * 0.05).astype(np.float32), fmt)
+    a = f64(A)
+    a, b = (a.T if tA else a), (b.T if tB else b)
+    C = torch.full((M, N), float("nan"), dtype=DT[dtype], device="cuda")
+    g.gemm_mx(A, B, C, transA=tA, transB=tB)
+    assert g.last_path() == "mx_convert"
+    check_product(C, a, b, dtype)
+    C1 = torch.full_like(C, float("nan"))
+    g.gemm_mx(A, B, C1, transA=tA, transB=tB)
+    assert torch.equal(C, C1)
+    bias, C0 = matrix(1, N, dtype, 7)[0], matrix(M, N, dtype, 8, offset=1, pitch=N + 3)
+    c0 = f64(C0)
+    g.gemm_mx(A, B, C0, transA=tA, transB=tB, alpha=0.5, beta=-1.0, bias=bias, act="gelu")
+    check_product(C0, a, b, dtype, 0.5, -1.0, c0, f64(bias), "gelu")
