@@ -387,40 +387,31 @@ def mx_empty(rows, cols, fmt, device="cuda") -> Mx:
               fmt, rows, cols)
 
 
-def _plain_code(t, what):
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError("matrices are 2-D")
-    if not t.is_cuda:
-        raise ValueError(f"{what} takes CUDA tensors")
-    return code
-
-
-def _handle(stream, t):
-    return (stream.cuda_stream if stream is not None else _current_stream(t.get_device())) or None
-
-
 def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     """Stores mult * op(X) in Q (an Mx) and, with Y, writes Y = act(op(X)) in the
     same pass: the forward pass of an activation whose input is checkpointed.
     X is [rows, cols] (or [cols, rows] with transX) float32, float16 or bfloat16;
     Y has X's dtype and shape and may be X.  Returns Q."""
-    dtype = _plain_code(X, "mx_quantize()")
+    dt, sx = X.dtype, X.shape
+    dtype = _DTYPES.get(dt)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {dt}")
     want = (Q.cols, Q.rows) if transX else (Q.rows, Q.cols)
-    if tuple(X.shape) != want:
-        raise ValueError(f"X is {tuple(X.shape)}, expected {want}")
+    if sx != want:
+        raise ValueError(f"X is {tuple(sx)}, expected {want}")
+    if not X.is_cuda:
+        raise ValueError("mx_quantize() takes CUDA tensors")
+    yp, ldy = None, 0
     if Y is not None:
-        if Y.dtype != X.dtype or Y.shape != X.shape or not Y.is_cuda:
+        if Y.dtype != dt or Y.shape != sx or not Y.is_cuda:
             raise ValueError("Y has X's dtype and shape, on a CUDA device")
+        yp, ldy = Y.data_ptr() or None, _ld_of(sx, Y.stride())
     elif act != "none":
         raise ValueError("act needs Y")
-    rc = _lib.gemm_mx_quantize(
-        Q.format, int(transX), Q.rows, Q.cols, dtype, float(mult), X.data_ptr() or None, _ld(X),
-        ACTS[act], (Y.data_ptr() or None) if Y is not None else None,
-        _ld(Y) if Y is not None else 0, Q.ptr, Q.pitch,
-        Q.sptr, _handle(stream, X))
+    s = (stream.cuda_stream if stream is not None else _current_stream(X.get_device())) or None
+    rc = _lib.gemm_mx_quantize(Q.format, 1 if transX else 0, Q.rows, Q.cols, dtype, mult,
+                               X.data_ptr() or None, _ld_of(sx, X.stride()), ACTS[act], yp, ldy,
+                               Q.ptr, Q.pitch, Q.sptr, s)
     if rc != OK:
         raise GemmError(rc)
     return Q
@@ -428,12 +419,17 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
 
 def mx_dequantize(Q, Y, stream=None):
     """Y = the values of Q, in Y's dtype.  Returns Y."""
-    dtype = _plain_code(Y, "mx_dequantize()")
-    if tuple(Y.shape) != (Q.rows, Q.cols):
-        raise ValueError(f"Y is {tuple(Y.shape)}, expected {(Q.rows, Q.cols)}")
-    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, Q.ptr, Q.pitch,
-                                 Q.sptr, dtype, Y.data_ptr() or None, _ld(Y),
-                                 _handle(stream, Y))
+    dtype = _DTYPES.get(Y.dtype)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {Y.dtype}")
+    sy = Y.shape
+    if sy != (Q.rows, Q.cols):
+        raise ValueError(f"Y is {tuple(sy)}, expected {(Q.rows, Q.cols)}")
+    if not Y.is_cuda:
+        raise ValueError("mx_dequantize() takes CUDA tensors")
+    s = (stream.cuda_stream if stream is not None else _current_stream(Y.get_device())) or None
+    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, Q.ptr, Q.pitch, Q.sptr, dtype,
+                                 Y.data_ptr() or None, _ld_of(sy, Y.stride()), s)
     if rc != OK:
         raise GemmError(rc)
     return Y
@@ -443,20 +439,25 @@ def mx_act_backward(dY, Q, dX, act="gelu", dbias=None, stream=None):
     """dX = dY * act'(x) with x read from its 8-bit checkpoint Q ('int8'), and
     dbias[j] = sum_i dX[i, j] (a contiguous float32 tensor of cols elements, or
     None).  dX may be dY.  Returns dX."""
-    dtype = _plain_code(dY, "mx_act_backward()")
+    dt, sy = dY.dtype, dY.shape
+    dtype = _DTYPES.get(dt)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {dt}")
     if Q.fmt != "int8":
         raise TypeError("the checkpoint is an 'int8' Mx")
-    if dX.dtype != dY.dtype or not dX.is_cuda or tuple(dX.shape) != (Q.rows, Q.cols) or \
-            tuple(dY.shape) != (Q.rows, Q.cols):
+    if dX.dtype != dt or sy != (Q.rows, Q.cols) or dX.shape != sy or \
+            not (dY.is_cuda and dX.is_cuda):
         raise ValueError(f"dY and dX: {(Q.rows, Q.cols)} CUDA tensors of one dtype")
-    if dbias is not None and (not dbias.is_cuda or dbias.numel() != Q.cols or
-                              dbias.element_size() != 4 or not dbias.is_floating_point() or
-                              not dbias.is_contiguous()):
-        raise ValueError("dbias: a contiguous float32 CUDA tensor of cols elements")
-    rc = _lib.gemm_mx_act_backward(
-        Q.rows, Q.cols, dtype, ACTS[act], dY.data_ptr() or None, _ld(dY),
-        Q.ptr, Q.pitch, Q.sptr, dX.data_ptr() or None,
-        _ld(dX), (dbias.data_ptr() or None) if dbias is not None else None, _handle(stream, dY))
+    bp = None
+    if dbias is not None:
+        if not dbias.is_cuda or dbias.numel() != Q.cols or _DTYPES.get(dbias.dtype) != F32 or \
+                not dbias.is_contiguous():
+            raise ValueError("dbias: a contiguous float32 CUDA tensor of cols elements")
+        bp = dbias.data_ptr() or None
+    s = (stream.cuda_stream if stream is not None else _current_stream(dY.get_device())) or None
+    rc = _lib.gemm_mx_act_backward(Q.rows, Q.cols, dtype, ACTS[act], dY.data_ptr() or None,
+                                   _ld_of(sy, dY.stride()), Q.ptr, Q.pitch, Q.sptr,
+                                   dX.data_ptr() or None, _ld_of(sy, dX.stride()), bp, s)
     if rc != OK:
         raise GemmError(rc)
     return dX

@@ -115,6 +115,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// One thread of a warp whose 32 threads all take the same path.  The loops that
+// issue TMA copies and MMAs keep their whole warp together and let one thread
+// issue: addresses and descriptors then live in uniform registers, where a
+// branch on a lane number has each operand moved there before every instruction
+// (a 4-bit product of 8192^3: 301 us with the branch, 195 us without).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Waits until the mbarrier phase with parity `parity` has completed.  Returns
 // false (after flagging) on timeout or when another role of the block has
 // already aborted.

@@ -304,12 +304,11 @@ struct MxStreamArgs {
   int transA = 0, transB = 1;  // (launch_mx_mixed)
 };
 // The converted product: A of type `out`, 16-byte aligned rows, op(A) op(B).
-// pair: 256 x 256 tiles on block pairs; otherwise 128 columns x mt rows, K in
-// `splits` slices.  cudaErrorNotSupported (nothing launched) for the variants
-// that have no kernel (int8 but tn; transA otherwise).
+// cudaErrorNotSupported (nothing launched) for the variants that have no kernel
+// (int8 but tn; transA otherwise), and where expanding B is the better plan.
 struct MixedPlan {
-  bool pair = false;
-  int mt = 128, splits = 1;
+  int mt = 128, splits = 1;  // rows of C a tile covers, slices of K
+  bool convert = true;       // false: expanding the operand is estimated to be faster
 };
 MixedPlan mixed_plan(int M, int N, int K, int num_sms);
 cudaError_t launch_mx_mixed(const MxStreamArgs& a, LaunchCtx& ctx);
@@ -319,7 +318,7 @@ cudaError_t launch_mx_mixed_bf16(const MxStreamArgs& a, LaunchCtx& ctx);
 // not take the problem
 cudaError_t launch_mx_stream(const MxStreamArgs& a, LaunchCtx& ctx);
 // C[M,N] = A^T B, A [K,M] of type `out` (fp16 or bf16, 16-byte aligned rows), M
-// up to 64, B [K,N] stored in 8 bits (As unused)
+// up to 32, B [K,N] stored in 8 bits (As unused)
 cudaError_t launch_mx_wgrad(const MxStreamArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, LaunchCtx& ctx);

@@ -71,17 +71,6 @@ struct MxTcParams {
   int stages_k;        // K stages of a tile
 };
 
-// One thread of a warp whose 32 threads all take the same path: the issuing
-// loops keep the whole warp together, so that addresses and descriptors live in
-// uniform registers.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 // Shared-memory descriptors as (low word, constant high word): the low word
 // holds the address >> 4, so a step along K or a ring stage is an addition.
 //   codes: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart
@@ -216,9 +205,15 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tmA);
-      tma_prefetch_desc(&tmB);
+    {
+      const bool leader = elect_one();
+      if (leader) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSA);
+        tma_prefetch_desc(&tmSB);
+      }
+      __syncwarp();
       int stage = 0;
       uint32_t phase = 0;
       uint32_t pending = 0, pend_phase = 0;
@@ -227,7 +222,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         int m0, n0, bz;
         tile_origin<PAIR, BN>(p, t, rank, m0, n0, bz);
         for (int kb = 0; kb < mp.stages_k; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, wc));
+          if (!ok) break;
           const bool skip = first && p.fault_injection == 1;
           first = false;
           if (!skip) {
@@ -238,7 +234,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
             // scale tiles past a row's end, and rows past the last range, read
             // as zero
             const int t0 = kb * TPS, ra = m0 >> 7, rb = n0 >> 7;
-            if constexpr (PAIR) {
+            if (!leader) {
+            } else if constexpr (PAIR) {
               const uint32_t bar = mapa_shared(full_bar(stage), 0u);
               if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), STAGE_TX);
               tma_load_3d_pair(sa, &tmA, kb * 128, m0, 0, bar);
@@ -262,6 +259,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
           } else {
             pending &= ~(1u << stage);
           }
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }

@@ -19,7 +19,7 @@ namespace {
 constexpr int64_t LIM = (int64_t)1 << 31;
 
 // Rows up to which a product streams its 4-bit right operand.
-constexpr int64_t WGRAD_ROWS = 64;  // (columns of A, in the tn product)
+constexpr int64_t WGRAD_ROWS = 32;  // (columns of A, in the tn product)
 constexpr int64_t STREAM_ROWS = 32, STREAM_ROWS_4 = 32;
 
 inline bool known_format(int f) { return f >= GEMM_MX_FP4 && f <= GEMM_MX_INT8; }

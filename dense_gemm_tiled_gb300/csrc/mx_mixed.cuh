@@ -11,28 +11,33 @@
 // The tensor core's 16-bit kinds take both operands in A's type, so the codes
 // become that type in shared memory.  The stored operand is the MMA's 128-row
 // side: a block converts 128 of its rows (or columns) once for up to 128 rows of
-// A (256 with a pair), and the accumulator is C transposed: lanes are columns of
-// C, so a warp's stores cover 32 of them in a row.
+// A, and the accumulator is C transposed: lanes are columns of C, so a warp's
+// stores cover 32 of them in a row.
 //   warp 0        producer: TMA of A's tile (128-byte swizzle), the codes and
-//                 their scale tiles, into one ring of stages of 64 k
+//                 their scale tiles, into a ring of stages of 64 k
 //   warp 1        tensor memory, MMA issue
 //   warps 2-5     epilogue
-//   warps 6-13    converters: 32 codes a thread and stage, written in the
-//                 swizzled K-major (nt) or MN-major (nn, tn) operand layout
-// Two forms:
-//   pairs   256 columns x 256 rows of C, 2-SM MMAs (each block converts its own
-//           128 columns and loads half of A's rows), persistent, two
-//           accumulators: large products, bound by the MMAs and L2's rate
-//   single  128 columns x 32, 64 or 128 rows, K split over a cluster whose blocks
-//           join their fp32 sums through distributed shared memory in rank order:
-//           small and skinny products, bound by the codes' bytes or latency
+//   warps 6-15    converters: codes to 16-bit values in the swizzled K-major (nt)
+//                 or MN-major (nn, tn) operand layout, in a ring of tiles of its
+//                 own.  Five groups of two warps take the stages in turn, each
+//                 with a tile of its own
+// What bounds it is the chain of a stage: convert, fence to the tensor core's
+// proxy, barrier, MMA, commit, barrier, about 2 us, of which five overlap: 0.4 us
+// a stage (0.19 without conversion and MMAs).  Eight tiles for the five groups,
+// with fewer stages of loads, measured the same to 20 % slower, all warps on each
+// stage the same.
+// One tile of C a cluster, K split over its blocks, which join their fp32 sums
+// through distributed shared memory in rank order.  For up to a few hundred rows
+// of A, where expanding the stored operand into scratch for the 16-bit kernels
+// would move 4.5 times its bytes.  (For large products that expansion costs a few
+// per cent and the 16-bit kernel's pairs of blocks feed the MMAs better: a form
+// of this kernel on pairs reached 0.97 PFLOP/s at 4096^3 against 1.59.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "hgemm_tcgen05.cuh"
@@ -42,12 +47,15 @@ namespace gb300 {
 namespace {
 
 constexpr int MM_K = 64;          // k of a stage: a 128-byte row of 16-bit values
-constexpr int MM_CONV = 8;        // converter warps
+constexpr int MM_CONV = 10;       // converter warps, in groups of
+constexpr int MM_GROUP = 2;       // two: a group converts every fifth stage
+constexpr int MM_GROUPS = MM_CONV / MM_GROUP;
 constexpr int MM_EPI = 4;
 constexpr int MM_THREADS = 32 * (2 + MM_EPI + MM_CONV);
 constexpr int MM_W_BYTES = 128 * 128;
 constexpr int MM_S_BYTES = 1024;  // up to two scale tiles
-constexpr int MM_MAX_STAGES = 6;
+constexpr int MM_MAX_STAGES = 12;
+constexpr int MM_TILES = MM_GROUPS;   // converted tiles
 constexpr int MM_FIXED = 1024 + 512;
 
 template <int FMT>
@@ -59,12 +67,12 @@ __host__ __device__ constexpr int mm_scale_tiles() { return W_MN && FMT == MX_FP
 
 struct MixedParams {
   int M, N, K;
-  int mt;              // rows of C a tile covers (pairs: 256)
+  int mt;              // rows of C a tile covers
   int x_bytes;         // A's tile in a block's stage
-  int ring;            // stages
+  int ring;            // stages of loads
   int steps;           // k stages in all
   int per;             // of a block (its slice)
-  int tiles_m, tiles_n, tiles;
+  int tiles_m;
   void* C;
   int64_t ldc;
   float alpha, beta;
@@ -73,24 +81,6 @@ struct MixedParams {
   uint64_t timeout_ns;
   int fault_injection;
 };
-
-// acquire at cluster scope: arrivals may come from the pair's other block, with
-// shared memory it wrote
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const WaitCtl& w) {
-  if (!mbar_wait(bar, parity, w)) return false;
-  return mbar_try_wait_cluster(bar, parity);  // (the phase is complete: returns at once)
-}
 
 // 32 codes of one row -> 16 words of T values.  `codes`: 16 bytes of e2m1 pairs
 // or 32 signed bytes; b0, b1 the scale bytes of its first and second 16 (equal
@@ -164,222 +154,171 @@ __device__ __forceinline__ void convert32(const uint32_t (&codes)[FMT == MX_INT8
 }
 
 // W_MN: the codes are stored [K, N]; X_MN: A is stored [K, M]
-template <typename T, int FMT, bool W_MN, bool X_MN, bool PAIR>
+template <typename T, int FMT, bool W_MN, bool X_MN>
 __global__ void __launch_bounds__(MM_THREADS, 1)
     mx_mixed_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmS, const MixedParams p) {
   constexpr int CODE_BYTES = mm_code_bytes<FMT>();
   constexpr int STILES = mm_scale_tiles<FMT, W_MN>();
-  const int stage_bytes = MM_W_BYTES + p.x_bytes + CODE_BYTES + MM_S_BYTES;
-  const int rank = PAIR ? (int)cluster_ctarank() : 0;       // block of a pair
-  const int slice = PAIR ? 0 : (int)blockIdx.x;             // block of a split cluster
-  const int splits = PAIR ? 1 : (int)gridDim.x;
-  const int worker = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.y;
-  const int workers = PAIR ? (int)(gridDim.x >> 1) : p.tiles;  // (single: one tile a cluster)
+  const int stage_bytes = p.x_bytes + CODE_BYTES + MM_S_BYTES;
+  const int slice = (int)blockIdx.x, splits = (int)gridDim.x;  // a cluster is a row of the grid
   const int k_lo = slice * p.per, k_hi = min(p.steps, k_lo + p.per);
   const int nk = k_hi - k_lo;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(base_ptr + p.ring * stage_bytes);
+  uint64_t* const bars =
+      reinterpret_cast<uint64_t*>(base_ptr + MM_TILES * MM_W_BYTES + p.ring * stage_bytes);
   const uint32_t bar0 = smem_u32(bars);
-  // this block's codes and scales landed; A's tile landed (pairs: both blocks',
-  // on the even block); codes converted (pairs: both blocks', there too); the
-  // MMAs that read the stage finished
+  // codes and scales landed; A's tile landed; the MMAs that read the stage
+  // finished; codes converted; the MMAs that read the converted tile finished
   auto code_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
   auto x_bar = [&](int s) { return bar0 + 8u * (uint32_t)(MM_MAX_STAGES + s); };
-  auto conv_bar = [&](int s) { return bar0 + 8u * (uint32_t)(2 * MM_MAX_STAGES + s); };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(3 * MM_MAX_STAGES + s); };
-  auto accf_bar = [&](int b) { return bar0 + 8u * (uint32_t)(4 * MM_MAX_STAGES + b); };
-  auto acce_bar = [&](int b) { return bar0 + 8u * (uint32_t)(4 * MM_MAX_STAGES + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (uint32_t)(4 * MM_MAX_STAGES + 4);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * MM_MAX_STAGES + 5);
+  auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(2 * MM_MAX_STAGES + s); };
+  constexpr int B1 = 3 * MM_MAX_STAGES;
+  auto conv_bar = [&](int w) { return bar0 + 8u * (uint32_t)(B1 + w); };
+  auto free_bar = [&](int w) { return bar0 + 8u * (uint32_t)(B1 + MM_TILES + w); };
+  constexpr int B2 = B1 + 2 * MM_TILES;
+  const uint32_t acc_bar = bar0 + 8u * (uint32_t)B2;
+  const uint32_t drain_bar = bar0 + 8u * (uint32_t)(B2 + 1);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + B2 + 2);
   volatile uint32_t* const abort_flag = tmem_slot + 1;
-  static_assert(8 * (4 * MM_MAX_STAGES + 6) <= 512, "barrier area");
-  auto w_at = [&](int s) { return base + (uint32_t)(s * stage_bytes); };
-  auto x_at = [&](int s) { return w_at(s) + (uint32_t)MM_W_BYTES; };
+  static_assert(8 * (B2 + 3) <= 512, "barrier area");
+  auto w_at = [&](int w) { return base + (uint32_t)(w * MM_W_BYTES); };
+  auto x_at = [&](int s) {
+    return base + (uint32_t)(MM_TILES * MM_W_BYTES) + (uint32_t)(s * stage_bytes);
+  };
   auto c_at = [&](int s) { return x_at(s) + (uint32_t)p.x_bytes; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t tmem_cols = PAIR ? 512u : (uint32_t)p.mt;
+  const uint32_t tmem_cols = (uint32_t)p.mt;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ring; ++s) {
       mbar_init(code_bar(s), 1);
       mbar_init(x_bar(s), 1);
-      mbar_init(conv_bar(s), (PAIR ? 2 : 1) * MM_CONV);
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), (PAIR ? 2 : 1) * 32 * MM_EPI);
+    for (int w = 0; w < MM_TILES; ++w) {
+      mbar_init(conv_bar(w), MM_GROUP);
+      mbar_init(free_bar(w), 1);
     }
+    mbar_init(acc_bar, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
   if (warp == 1) {
-    if constexpr (PAIR) {
-      tmem_alloc_pair(smem_u32(tmem_slot), tmem_cols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(tmem_slot), tmem_cols);
-      tmem_relinquish();
-    }
+    tmem_alloc(smem_u32(tmem_slot), tmem_cols);
+    tmem_relinquish();
   }
   tc_fence_before();
-  if constexpr (PAIR) cluster_sync();
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
   pdl_trigger();
   const WaitCtl wc{p.status, abort_flag, p.timeout_ns};
 
-  // tile t: columns n0 of this block, rows m0 (row tiles innermost: the blocks
-  // that run together read few columns' codes and all of A)
-  auto origin = [&](int t, int& n0, int& m0) {
-    const int tn = t / p.tiles_m;
-    n0 = (PAIR ? 2 * tn + rank : tn) * 128;
-    m0 = (t - tn * p.tiles_m) * p.mt;
-  };
+  // the cluster's tile: columns n0, rows m0 (row tiles innermost: the blocks that
+  // run together read few columns' codes and all of A)
+  const int n0 = (int)blockIdx.y / p.tiles_m * 128, m0 = (int)blockIdx.y % p.tiles_m * p.mt;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tmX);
-      tma_prefetch_desc(&tmW);
-      tma_prefetch_desc(&tmS);
+    {
+      const bool leader = elect_one();
+      if (leader) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmS);
+      }
+      __syncwarp();
       int stage = 0;
       uint32_t phase = 0, pending = 0, pend_phase = 0;
-      bool ok = true, first = true;
-      for (int t = worker; ok && t < p.tiles; t += workers) {
-        int n0, m0;
-        origin(t, n0, m0);
-        for (int k = k_lo; k < k_hi; ++k) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) { ok = false; break; }
-          const bool skip = first && p.fault_injection == 1;
-          first = false;
-          if (skip) {
-            pending &= ~(1u << stage);
-          } else {
-            const uint32_t x = x_at(stage), c = c_at(stage), s = c + (uint32_t)CODE_BYTES;
-            const uint32_t cb = code_bar(stage);
-            mbar_arrive_expect_tx(cb, (uint32_t)(CODE_BYTES + STILES * 512));
-            if constexpr (W_MN) {
-              tma_load_3d(c, &tmW, FMT == MX_INT8 ? n0 : n0 / 2, k * MM_K, 0, cb);
-              tma_load_3d(s, &tmS, 0, (n0 >> 7) * STILES, (k * MM_K) >> 7, cb);
-            } else {
-              tma_load_3d(c, &tmW, FMT == MX_INT8 ? k * MM_K : k * MM_K / 2, n0, 0, cb);
-              tma_load_3d(s, &tmS, 0, k * MM_K / (4 * mx_block(FMT)), n0 >> 7, cb);
-            }
-            const int mx = m0 + (PAIR ? rank * 128 : 0);
-            if constexpr (PAIR) {
-              const uint32_t xb = mapa_shared(x_bar(stage), 0u);
-              if (rank == 0) mbar_arrive_expect_tx(x_bar(stage), 2u * (uint32_t)p.x_bytes);
-              if constexpr (X_MN) {
-                tma_load_3d_pair(x, &tmX, mx, k * MM_K, 0, xb);
-                tma_load_3d_pair(x + 8192u, &tmX, mx + 64, k * MM_K, 0, xb);
-              } else {
-                tma_load_3d_pair(x, &tmX, k * MM_K, mx, 0, xb);
-              }
-            } else {
-              const uint32_t xb = x_bar(stage);
-              mbar_arrive_expect_tx(xb, (uint32_t)p.x_bytes);
-              if constexpr (X_MN) {
-                for (int h = 0; h < p.x_bytes / 8192; ++h)
-                  tma_load_3d(x + (uint32_t)(h * 8192), &tmX, mx + 64 * h, k * MM_K, 0, xb);
-              } else {
-                tma_load_3d(x, &tmX, k * MM_K, mx, 0, xb);
-              }
-            }
-            pending |= 1u << stage;
-            pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
-          }
-          if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+      for (int k = k_lo; k < k_hi; ++k) {
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, wc))) break;
+        const bool skip = p.fault_injection == 1 && k == k_lo;
+        if (!skip) {
+          pending |= 1u << stage;
+          pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
         }
+        if (!skip && leader) {
+          const uint32_t x = x_at(stage), c = c_at(stage), s = c + (uint32_t)CODE_BYTES;
+          const uint32_t cb = code_bar(stage), xb = x_bar(stage);
+          mbar_arrive_expect_tx(cb, (uint32_t)(CODE_BYTES + STILES * 512));
+          if constexpr (W_MN) {
+            tma_load_3d(c, &tmW, FMT == MX_INT8 ? n0 : n0 / 2, k * MM_K, 0, cb);
+            tma_load_3d(s, &tmS, 0, (n0 >> 7) * STILES, (k * MM_K) >> 7, cb);
+          } else {
+            tma_load_3d(c, &tmW, FMT == MX_INT8 ? k * MM_K : k * MM_K / 2, n0, 0, cb);
+            tma_load_3d(s, &tmS, 0, k * MM_K / (4 * mx_block(FMT)), n0 >> 7, cb);
+          }
+          mbar_arrive_expect_tx(xb, (uint32_t)p.x_bytes);
+          if constexpr (X_MN) {
+            for (int h = 0; h < p.x_bytes / 8192; ++h)
+              tma_load_3d(x + (uint32_t)(h * 8192), &tmX, m0 + 64 * h, k * MM_K, 0, xb);
+          } else {
+            tma_load_3d(x, &tmX, k * MM_K, m0, 0, xb);
+          }
+        }
+        __syncwarp();
+        if (++stage == p.ring) { stage = 0; phase ^= 1u; }
       }
       // every load issued lands before shared memory is released
       for (int s = 0; s < p.ring; ++s)
         if (pending & (1u << s)) {
           mbar_wait_drain(code_bar(s), (pend_phase >> s) & 1u, p.timeout_ns);
-          if (rank == 0) mbar_wait_drain(x_bar(s), (pend_phase >> s) & 1u, p.timeout_ns);
+          mbar_wait_drain(x_bar(s), (pend_phase >> s) & 1u, p.timeout_ns);
         }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // (the warp stays converged; see mx4_tcgen05.cu on uniform operands)
-    if (rank == 0) {
-      uint32_t lead;
-      asm volatile(
-          "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(lead));
-      const bool leader = lead != 0;
-      // D fp32, A and B of T, majors, N = mt, M = 128 or 256
-      const uint32_t idesc = (1u << 4) | (Elem<T>::FMT << 7) | (Elem<T>::FMT << 10) |
-                             ((W_MN ? 1u : 0u) << 15) | ((X_MN ? 1u : 0u) << 16) |
-                             ((uint32_t)(p.mt >> 3) << 17) | ((PAIR ? 16u : 8u) << 24);
-      int stage = 0;
-      uint32_t phase = 0;
-      int it = 0;
-      bool ok = true;
-      for (int t = worker; ok && t < p.tiles; t += workers, ++it) {
-        const int buf = it & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(acce_bar(buf), ((uint32_t)(it >> 1) & 1u) ^ 1u, wc));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(PAIR ? buf * 256 : 0);
-        for (int k = 0; k < nk; ++k) {
-          ok = __all_sync(0xffffffffu, mbar_wait(x_bar(stage), phase, wc) &&
-                                           mbar_wait_cluster(conv_bar(stage), phase, wc));
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            const uint32_t w = w_at(stage), x = x_at(stage);
-#pragma unroll
-            for (int kk = 0; kk < MM_K / 16; ++kk) {
-              const uint64_t ad = W_MN ? make_sdesc(w + (uint32_t)kk * 2048u, 8192u, 1024u)
-                                       : make_sdesc(w + (uint32_t)kk * 32u, 16u, 1024u);
-              const uint64_t bd = X_MN ? make_sdesc(x + (uint32_t)kk * 2048u, 8192u, 1024u)
-                                       : make_sdesc(x + (uint32_t)kk * 32u, 16u, 1024u);
-              const uint32_t acc = (k | kk) != 0 ? 1u : 0u;
-              if constexpr (PAIR) tc_mma_f16_pair(d, ad, bd, idesc, acc);
-              else tc_mma_f16(d, ad, bd, idesc, acc);
-            }
-            if constexpr (PAIR) tc_commit_pair_mc(empty_bar(stage), (uint16_t)3u);
-            else tc_commit(empty_bar(stage));
-          }
-          __syncwarp();
-          if (++stage == p.ring) { stage = 0; phase ^= 1u; }
-        }
-        if (!ok) break;
-        if (leader) {
-          if constexpr (PAIR) tc_commit_pair_mc(accf_bar(buf), (uint16_t)3u);
-          else tc_commit(accf_bar(buf));
-        }
-        __syncwarp();
-      }
+    const bool leader = elect_one();
+    // D fp32, A and B of T, majors, N = mt, M = 128
+    const uint32_t idesc = (1u << 4) | (Elem<T>::FMT << 7) | (Elem<T>::FMT << 10) |
+                           ((W_MN ? 1u : 0u) << 15) | ((X_MN ? 1u : 0u) << 16) |
+                           ((uint32_t)(p.mt >> 3) << 17) | (8u << 24);
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, wphase = 0;
+    bool ok = true;
+    for (int k = 0; k < nk; ++k) {
+      ok = __all_sync(0xffffffffu, mbar_wait(x_bar(stage), phase, wc) &&
+                                       mbar_wait(conv_bar(slot), wphase, wc));
+      if (!ok) break;
+      tc_fence_after();
       if (leader) {
-        if constexpr (PAIR) tc_commit_pair_mc(drain_bar, (uint16_t)1u);
-        else tc_commit(drain_bar);
-        mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
+        const uint32_t w = w_at(slot), x = x_at(stage);
+#pragma unroll
+        for (int kk = 0; kk < MM_K / 16; ++kk) {
+          const uint64_t ad = W_MN ? make_sdesc(w + (uint32_t)kk * 2048u, 8192u, 1024u)
+                                   : make_sdesc(w + (uint32_t)kk * 32u, 16u, 1024u);
+          const uint64_t bd = X_MN ? make_sdesc(x + (uint32_t)kk * 2048u, 8192u, 1024u)
+                                   : make_sdesc(x + (uint32_t)kk * 32u, 16u, 1024u);
+          tc_mma_f16(tmem_base, ad, bd, idesc, (k | kk) != 0 ? 1u : 0u);
+        }
+        tc_commit(free_bar(slot));
+        tc_commit(empty_bar(stage));
       }
       __syncwarp();
+      if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+      if (++slot == MM_TILES) { slot = 0; wphase ^= 1u; }
     }
+    if (leader) {
+      if (ok) tc_commit(acc_bar);
+      tc_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
+    }
+    __syncwarp();
   } else if (warp < 2 + MM_EPI) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    int it = 0;
-    for (int t = worker; t < p.tiles; t += workers, ++it) {
-      int n0, m0;
-      origin(t, n0, m0);
-      const int buf = it & 1;
-      bool got = false;
-      if (lane == 0) got = mbar_wait(accf_bar(buf), (uint32_t)(it >> 1) & 1u, wc);
-      got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
-      if (!got) break;
+    bool got = false;
+    if (lane == 0) got = mbar_wait(acc_bar, 0u, wc);
+    got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+    if (got) {
       tc_fence_after();
-      const uint32_t row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(PAIR ? buf * 256 : 0);
+      const uint32_t row = tmem_base + ((uint32_t)(q * 32) << 16);
       const int n = n0 + 32 * q + lane;  // this lane's column of C
       const int chunks = min(p.mt, p.M - m0 + 31) / 32;
       T* const col = static_cast<T*>(p.C) + n;
@@ -392,7 +331,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         tmem_ld_32x32b_x32(row + (uint32_t)(c * 32), r);
         tmem_ld_wait();
         if (splits > 1) {
-          // fp32 sums [row of C][column], in the ring: every stage was consumed
+          // fp32 sums [row of C][column], over the converted tiles: the MMAs are done
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(
@@ -415,76 +354,95 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
           }
         }
       }
-      tc_fence_before();
-      if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(acce_bar(buf), 0u));
-      else mbar_arrive(acce_bar(buf));
     }
   } else {
     // ------------------------------------------------------------ converters
-    const int ct = threadIdx.x - 32 * (2 + MM_EPI);  // 0 .. 255
-    // stored [N, K]: row ct / 2, 32 codes of K from 32 (ct & 1);
-    // stored [K, N]: k row (ct % 128) / 2, 32 columns from 32 seg
-    const int r = W_MN ? (ct & 127) >> 1 : ct >> 1;
-    const int seg = W_MN ? 2 * (ct >> 7) + (ct & 1) : (ct & 1);
+    // A thread of a group of 64 takes four runs of 32 codes of a stage:
+    //   stored [N, K]: rows r, r + 32, r + 64, r + 96, 32 codes of K from 32 seg
+    //   stored [K, N]: k rows r, r + 32, 32 columns from 32 seg and 32 (seg + 2)
+    const int ct = (threadIdx.x - 32 * (2 + MM_EPI)) & (32 * MM_GROUP - 1);
+    const int group = (warp - 2 - MM_EPI) / MM_GROUP;
+    const int r = ct >> 1, seg = ct & 1;
     constexpr int B32 = FMT == MX_INT8 ? 32 : 16;  // bytes of 32 codes
-    const uint32_t from = (uint32_t)(r * (W_MN ? 4 : 2) * B32 + seg * B32);
-    const uint32_t to = W_MN ? (uint32_t)((seg >> 1) * 8192 + r * 128) : (uint32_t)(r * 128);
-    const int chunk0 = W_MN ? 4 * (seg & 1) : 4 * seg;
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int t = worker; ok && t < p.tiles; t += workers) {
-      for (int k = k_lo; k < k_hi; ++k) {
-        ok = false;
-        if (lane == 0) ok = mbar_wait(code_bar(stage), phase, wc);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        const uint32_t c = c_at(stage), s = c + (uint32_t)CODE_BYTES;
-        uint32_t codes[FMT == MX_INT8 ? 8 : 4];
+    constexpr int ROW = (W_MN ? 4 : 2) * B32;      // of a row of codes
+    const uint32_t from = (uint32_t)(r * ROW + seg * B32);
+    const uint32_t to = (uint32_t)(r * 128);
+    int stage = 0, turn = 0;
+    uint32_t phase = 0, wphase = 1;
+    for (int k = k_lo; k < k_hi; ++k) {
+      const int st = stage;
+      const uint32_t ph = phase;
+      if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+      const bool mine = turn == group;
+      if (++turn == MM_GROUPS) turn = 0;
+      if (!mine) continue;
+      // (the tile first: with the MMAs of the stage before this group's done, the
+      // codes of that stage and of all before it have landed, so that the load
+      // barrier is at most one phase behind, the ring having at least as many
+      // stages as there are groups)
+      bool ok = false;
+      if (lane == 0) ok = mbar_wait(free_bar(group), wphase, wc) && mbar_wait(code_bar(st), ph, wc);
+      wphase ^= 1u;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      const uint32_t c = c_at(st), s = c + (uint32_t)CODE_BYTES;
+      uint32_t codes[4][FMT == MX_INT8 ? 8 : 4];
 #pragma unroll
-        for (int i = 0; i < B32 / 16; ++i)
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at = c + from +
+                            (uint32_t)(W_MN ? (i & 1) * 32 * ROW + (i >> 1) * 2 * B32 : i * 32 * ROW);
+#pragma unroll
+        for (int h = 0; h < B32 / 16; ++h)
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(codes[4 * i]), "=r"(codes[4 * i + 1]), "=r"(codes[4 * i + 2]),
-                         "=r"(codes[4 * i + 3])
-                       : "r"(c + from + (uint32_t)(16 * i)));
-        // the block of this thread's codes (two of 16), and the row, in the tiles
-        const int tr = W_MN ? ((k * MM_K) & 127) + r : r;
+                       : "=r"(codes[i][4 * h]), "=r"(codes[i][4 * h + 1]),
+                         "=r"(codes[i][4 * h + 2]), "=r"(codes[i][4 * h + 3])
+                       : "r"(at + (uint32_t)(16 * h)));
+      }
+      // the runs' scale words: rows 32 apart are neighbours in a scale tile
+      uint32_t word[4];
+      if constexpr (W_MN) {
+        const uint32_t at = s + (uint32_t)(r * 16 + ((k * MM_K) & 127) / 32 * 4);
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(word[0]), "=r"(word[1]) : "r"(at));
+        word[2] = word[0];
+        word[3] = word[1];
+        if constexpr (STILES == 2)
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(word[2]), "=r"(word[3])
+                       : "r"(at + 512u));
+      } else {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
+                     : "r"(s + (uint32_t)(r * 16)));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // the run's block (the first of two 16-wide ones) within its word
         const int blk = FMT == MX_FP4_E4M3 ? 2 * seg
-                        : W_MN             ? seg
+                        : W_MN             ? seg + 2 * (i >> 1)
                                            : ((k * MM_K) >> 5 & 3) + seg;
-        uint32_t word;
-        asm volatile("ld.shared.b32 %0, [%1];"
-                     : "=r"(word)
-                     : "r"(s + (uint32_t)((blk >> 2) * 512 + (tr & 31) * 16 + (tr >> 5) * 4)));
-        const uint32_t b0 = (word >> (8 * (blk & 3))) & 255u;
-        const uint32_t b1 = FMT == MX_FP4_E4M3 ? (word >> (8 * (blk & 3) + 8)) & 255u : b0;
+        const uint32_t b0 = (word[i] >> (8 * blk)) & 255u;
+        const uint32_t b1 = FMT == MX_FP4_E4M3 ? (word[i] >> (8 * blk + 8)) & 255u : b0;
         uint32_t out[16];
-        convert32<T, FMT>(codes, b0, b1, out);
-        const uint32_t w = w_at(stage) + to;
+        convert32<T, FMT>(codes[i], b0, b1, out);
+        const uint32_t w = w_at(group) + to +
+                           (uint32_t)(W_MN ? (i >> 1) * 8192 + (i & 1) * 32 * 128 : i * 32 * 128);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           w + (uint32_t)(((chunk0 + j) ^ (r & 7)) * 16)),
+                           w + (uint32_t)(((4 * seg + j) ^ (r & 7)) * 16)),
                        "r"(out[4 * j]), "r"(out[4 * j + 1]), "r"(out[4 * j + 2]),
                        "r"(out[4 * j + 3])
                        : "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(conv_bar(stage), 0u));
-          else mbar_arrive(conv_bar(stage));
-        }
-        if (++stage == p.ring) { stage = 0; phase ^= 1u; }
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(conv_bar(group));
     }
   }
 
   tc_fence_before();
-  // a pair leaves together; a split cluster joins its sums
   cluster_sync();
-  if (!PAIR && splits > 1) {
-    int n0, m0;
-    origin(worker, n0, m0);
+  if (splits > 1) {  // join the slices' sums
     const int q_lo = slice * 32 / splits, q_cnt = (slice + 1) * 32 / splits - q_lo;
     const int mc = min(p.mt, p.M - m0);
     for (int i = threadIdx.x; i < q_cnt * mc; i += MM_THREADS) {
@@ -506,40 +464,38 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, tmem_cols);
-    else tmem_dealloc(tmem_base, tmem_cols);
+    tmem_dealloc(tmem_base, tmem_cols);
   }
 }
 
 // ---------------------------------------------------------------- host side
-template <typename T, int FMT, bool W_MN, bool X_MN, bool PAIR>
-cudaError_t launch_mixed_form(const MxStreamArgs& a, int mt, int want_splits, LaunchCtx& ctx) {
-  auto kern = mx_mixed_kernel<T, FMT, W_MN, X_MN, PAIR>;
+template <typename T, int FMT, bool W_MN, bool X_MN>
+cudaError_t launch_mixed_v(const MxStreamArgs& a, LaunchCtx& ctx) {
+  auto kern = mx_mixed_kernel<T, FMT, W_MN, X_MN>;
   constexpr int CODE_BYTES = mm_code_bytes<FMT>();
+  const MixedPlan pl = mixed_plan(a.M, a.N, a.K, a.num_sms);
+  if (!pl.convert) return cudaErrorNotSupported;
   MixedParams p;
   p.M = a.M; p.N = a.N; p.K = a.K;
-  p.mt = mt;
-  const int x_rows = PAIR ? 128 : mt;
-  p.x_bytes = X_MN ? (x_rows + 63) / 64 * 8192 : x_rows * 128;
-  const int stage = MM_W_BYTES + p.x_bytes + CODE_BYTES + MM_S_BYTES;
-  p.ring = (SMEM_LIMIT - MM_FIXED) / stage;
+  p.mt = pl.mt;
+  p.x_bytes = X_MN ? (pl.mt + 63) / 64 * 8192 : pl.mt * 128;
+  const int stage = p.x_bytes + CODE_BYTES + MM_S_BYTES;
+  p.ring = (SMEM_LIMIT - MM_FIXED - MM_TILES * MM_W_BYTES) / stage;
   if (p.ring > MM_MAX_STAGES) p.ring = MM_MAX_STAGES;
+  if (p.ring < MM_GROUPS) return cudaErrorNotSupported;  // (never: five at 128 rows)
   p.steps = (a.K + MM_K - 1) / MM_K;
-  p.per = (p.steps + want_splits - 1) / want_splits;
+  p.per = (p.steps + pl.splits - 1) / pl.splits;
   const int splits = (p.steps + p.per - 1) / p.per;
-  const int bn = PAIR ? 256 : 128;
-  p.tiles_n = (int)(((int64_t)a.N + bn - 1) / bn);
-  p.tiles_m = (int)(((int64_t)a.M + mt - 1) / mt);
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  if (tiles > (PAIR ? (1 << 30) : 65535)) return cudaErrorNotSupported;
-  p.tiles = (int)tiles;
+  p.tiles_m = (int)(((int64_t)a.M + pl.mt - 1) / pl.mt);
+  const int64_t tiles = (int64_t)p.tiles_m * (((int64_t)a.N + 127) / 128);
+  if (tiles > 65535) return cudaErrorNotSupported;
   p.C = a.C; p.ldc = a.ldc;
   p.alpha = a.alpha; p.beta = a.beta;
   p.ep = a.ep;
   p.status = ctx.status;
   p.timeout_ns = ctx.timeout_ns;
   p.fault_injection = a.fault_injection;
-  const size_t smem = (size_t)p.ring * stage + MM_FIXED;
+  const size_t smem = (size_t)MM_TILES * MM_W_BYTES + (size_t)p.ring * stage + MM_FIXED;
   static const cudaError_t attr =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
   if (attr != cudaSuccess) return attr;
@@ -551,39 +507,17 @@ cudaError_t launch_mixed_form(const MxStreamArgs& a, int mt, int want_splits, La
   const int64_t stiles = mx_scale_tiles(FMT, (int)wc);
   const int row_codes = W_MN ? 128 : MM_K;  // codes of a box row
   bool ok = X_MN ? make_map(&mX, Elem<T>::TMA, a.A, a.K, a.M, a.lda, 64, MM_K)
-                 : make_map(&mX, Elem<T>::TMA, a.A, a.M, a.K, a.lda, MM_K, x_rows);
+                 : make_map(&mX, Elem<T>::TMA, a.A, a.M, a.K, a.lda, MM_K, pl.mt);
   ok = ok && make_map(&mW, U8, a.B, wr, wbytes, a.ldb, FMT == MX_INT8 ? row_codes : row_codes / 2,
                       W_MN ? MM_K : 128, NONE, 1, 0, 1);
   ok = ok && make_map(&mS, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.Bs, stiles, 128, 128, 128,
                       mm_scale_tiles<FMT, W_MN>(), NONE, (wr + 127) / 128, stiles * 128, 4);
   if (!ok) return cudaErrorNotSupported;
-  cudaError_t e;
-  if (PAIR) {
-    static std::atomic<int> pairs{0};
-    int have = pairs.load(std::memory_order_relaxed);
-    if (have == 0) {
-      have = resident_clusters((const void*)kern, 2, MM_THREADS, smem);
-      if (have <= 0) have = a.num_sms / 2;
-      pairs.store(have, std::memory_order_relaxed);
-    }
-    const int workers = have < p.tiles ? have : p.tiles;
-    ctx.grid = 2 * workers;
-    e = launch_kernel(kern, dim3((unsigned)ctx.grid), dim3(MM_THREADS), smem, ctx.stream, 2, mX, mW,
-                      mS, p);
-  } else {
-    ctx.grid = splits * p.tiles;
-    e = launch_kernel(kern, dim3((unsigned)splits, (unsigned)p.tiles), dim3(MM_THREADS), smem,
-                      ctx.stream, splits, mX, mW, mS, p);
-  }
+  ctx.grid = (int)(splits * tiles);
+  const cudaError_t e = launch_kernel(kern, dim3((unsigned)splits, (unsigned)tiles),
+                                      dim3(MM_THREADS), smem, ctx.stream, splits, mX, mW, mS, p);
   if (e == cudaSuccess) ctx.launches++;
   return e;
-}
-
-template <typename T, int FMT, bool W_MN, bool X_MN>
-cudaError_t launch_mixed_v(const MxStreamArgs& a, LaunchCtx& ctx) {
-  const MixedPlan pl = mixed_plan(a.M, a.N, a.K, a.num_sms);
-  return pl.pair ? launch_mixed_form<T, FMT, W_MN, X_MN, true>(a, 256, 1, ctx)
-                 : launch_mixed_form<T, FMT, W_MN, X_MN, false>(a, pl.mt, pl.splits, ctx);
 }
 
 template <typename T>

@@ -5,37 +5,35 @@
 
 namespace gb300 {
 
-// Form of a converted product: the one with the least estimated time, in units
-// of a stage's loads: rounds of tiles x (stages of a block + what a tile costs
-// beside them).
+// Rows of C a tile covers, and as many slices of K as leave every cluster
+// resident (an SM a block; at most 6: clusters of 8 leave too many SMs of a GPC
+// over, 33 x 2048 x 2048 14.0 us with 8, 7.8 with 6, 8.0 with 4); and whether that is estimated to take less time than expanding the operand
+// and multiplying with the 16-bit kernel: rounds of blocks x stages x 0.4 us
+// against the operand's bytes (read, written, read: 5 a value) and the products
+// at 1.5 PFLOP/s.  Measured, us, converted against expanded, fp4 (nt but where
+// said):  33 x 2048 x 2048 8.0 / 16.1;  64 x 8192 x 8192 33 / 61;  128 x 8192 x
+// 8192 32 / 61;  256 x 8192 x 8192 56 / 73;  nn 1 x 8192 x 8192 28 / 64;  nn 512 x
+// 2048 x 5632 24 / 25;  512 x 5632 x 2048 34 / 20;  1000 x 3000 x 777 24 / 15;
+// 4096^3 205 / 86.
 MixedPlan mixed_plan(int M, int N, int K, int num_sms) {
   static const int forced = [] {
     const char* e = getenv("GEMM_GB300_MX_MIXED");
     return e ? atoi(e) : -1;
   }();
   const int64_t steps = ((int64_t)K + 63) / 64;
-  const int64_t n128 = ((int64_t)N + 127) / 128;
   MixedPlan pl;
   pl.mt = M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  // single: as many slices of K as leave every cluster resident (an SM a block;
-  // clusters of up to 8 leave some SMs of a GPC over)
-  const int64_t tiles = n128 * (((int64_t)M + pl.mt - 1) / pl.mt);
-  int64_t s = tiles > 0 ? (int64_t)num_sms * 7 / 8 / tiles : 1;
-  if (s > 8) s = 8;
-  if (s > steps) s = steps;
-  if (s < 1) s = 1;
+  const int64_t tiles = ((int64_t)N + 127) / 128 * (((int64_t)M + pl.mt - 1) / pl.mt);
+  int64_t s = forced > 0 ? forced : (int64_t)num_sms * 7 / 8 / (tiles > 0 ? tiles : 1);
+  s = forced > 0 ? (s < 8 ? s : 8) : s < 6 ? s : 6;
+  s = s < steps ? s : steps;
+  s = s > 1 ? s : 1;
   pl.splits = (int)s;
-  const int64_t rounds1 = (tiles * s + num_sms - 1) / num_sms;
-  const double t1 = (double)rounds1 * ((double)((steps + s - 1) / s) + (s > 1 ? 14 : 10));
-  const int64_t pairs = ((N + 255) / 256) * (int64_t)(((int64_t)M + 255) / 256);
-  const int64_t rounds2 = (pairs + num_sms / 2 - 1) / (num_sms / 2);
-  const double t2 = (double)rounds2 * (double)steps * 1.05 + 20;
-  pl.pair = M > 128 && t2 < t1;
-  if (forced == 0) pl.pair = true;
-  if (forced > 0) {
-    pl.pair = false;
-    pl.splits = forced < 8 ? forced : 8;
-  }
+  const int64_t rounds = (tiles * s + num_sms - 1) / num_sms;
+  const double convert = 6 + 0.4 * (double)rounds * (double)((steps + s - 1) / s);
+  const double nk = (double)N * K;
+  const double expand = 8 + 5 * nk / 6.8e6 + 2 * nk * M / 1.5e9;
+  pl.convert = forced == 0 ? false : forced > 0 || convert < expand;
   return pl;
 }
 

@@ -175,32 +175,35 @@ __global__ void __launch_bounds__(ST_THREADS)
 
   if (warp == WARPS) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    {
+      const bool leader = elect_one();
       int stage = 0;
       uint32_t phase = 0, pending = 0, pend_phase = 0;
       for (int k = k_lo; k < k_hi; ++k) {
-        if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) break;
-        if (p.fault_injection == 1 && k == k_lo) {
-          if (++stage == p.ring) { stage = 0; phase ^= 1u; }
-          continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, wc))) break;
+        const bool skip = p.fault_injection == 1 && k == k_lo;
+        if (!skip) {
+          pending |= 1u << stage;
+          pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
         }
-        const uint32_t w = base + (uint32_t)(stage * C_::STAGE), x = w + C_::W_BYTES;
-        const uint32_t s = x + C_::X_BYTES, xs = s + C_::S_BYTES;
-        const uint32_t bar = full_bar(stage);
-        mbar_arrive_expect_tx(bar, (uint32_t)C_::STAGE);
-        tma_load_3d(w, &tmW, k * 128, n0, 0, bar);
-        tma_load_3d(s, &tmS, 0, k * TPS, n0 >> 7, bar);
-        if constexpr (XT == X_FP4) {
-          tma_load_3d(x, &tmX, k * 128, m0, 0, bar);
-          tma_load_3d(xs, &tmXS, 0, k * TPS, m0 >> 7, bar);
-        } else {
-          // 32 columns a box: [group][row][64 bytes]
+        if (!skip && leader) {
+          const uint32_t w = base + (uint32_t)(stage * C_::STAGE), x = w + C_::W_BYTES;
+          const uint32_t s = x + C_::X_BYTES, xs = s + C_::S_BYTES;
+          const uint32_t bar = full_bar(stage);
+          mbar_arrive_expect_tx(bar, (uint32_t)C_::STAGE);
+          tma_load_3d(w, &tmW, k * 128, n0, 0, bar);
+          tma_load_3d(s, &tmS, 0, k * TPS, n0 >> 7, bar);
+          if constexpr (XT == X_FP4) {
+            tma_load_3d(x, &tmX, k * 128, m0, 0, bar);
+            tma_load_3d(xs, &tmXS, 0, k * TPS, m0 >> 7, bar);
+          } else {
+            // 32 columns a box: [group][row][64 bytes]
 #pragma unroll
-          for (int b = 0; b < KSTEP / 32; ++b)
-            tma_load_3d(x + (uint32_t)(b * 8 * NT * 64), &tmX, k * KSTEP + 32 * b, m0, 0, bar);
+            for (int b = 0; b < KSTEP / 32; ++b)
+              tma_load_3d(x + (uint32_t)(b * 8 * NT * 64), &tmX, k * KSTEP + 32 * b, m0, 0, bar);
+          }
         }
-        pending |= 1u << stage;
-        pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
+        __syncwarp();
         if (++stage == p.ring) { stage = 0; phase ^= 1u; }
       }
       // every load issued lands before the block's shared memory is released

@@ -2,7 +2,7 @@
 //
 //   C[m, n] = act(alpha * sum_t A[t, m] s[t, n/32] q[t, n] + beta * C + bias[n]),
 //
-// A [T, M] fp16 or bf16 with M up to 64 columns, q the checkpoint of the
+// A [T, M] fp16 or bf16 with M up to 32 columns, q the checkpoint of the
 // layer's input, [T, N] (the tn product of "Metal GEMM Kernels for LoRA Training
 // on Apple Silicon", section 5, with its right operand stored in 8 bits).
 // Bound by the bytes of the checkpoint, each read once.
@@ -187,23 +187,26 @@ __global__ void __launch_bounds__(WG_THREADS)
 
   if (warp == WG_WARPS) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    {
+      const bool leader = elect_one();
       int stage = 0;
       uint32_t phase = 0, pending = 0, pend_phase = 0;
       for (int k = k_lo; k < k_hi; ++k) {
-        if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) break;
-        if (p.fault_injection == 1 && k == k_lo) {
-          if (++stage == p.ring) { stage = 0; phase ^= 1u; }
-          continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, wc))) break;
+        const bool skip = p.fault_injection == 1 && k == k_lo;
+        if (!skip) {
+          pending |= 1u << stage;
+          pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
         }
-        const uint32_t q = base + (uint32_t)(stage * C_::STAGE), a = q + C_::Q_BYTES;
-        const uint32_t bar = full_bar(stage);
-        mbar_arrive_expect_tx(bar, C_::TX);
-        tma_load_3d(q, &tmQ, n0, k * TSTEP, 0, bar);
-        tma_load_3d(a, &tmA, 0, k * TSTEP, 0, bar);
-        tma_load_3d(a + C_::A_BYTES, &tmS, 0, (int)blockIdx.y, (k * TSTEP) >> 7, bar);
-        pending |= 1u << stage;
-        pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
+        if (!skip && leader) {
+          const uint32_t q = base + (uint32_t)(stage * C_::STAGE), a = q + C_::Q_BYTES;
+          const uint32_t bar = full_bar(stage);
+          mbar_arrive_expect_tx(bar, C_::TX);
+          tma_load_3d(q, &tmQ, n0, k * TSTEP, 0, bar);
+          tma_load_3d(a, &tmA, 0, k * TSTEP, 0, bar);
+          tma_load_3d(a + C_::A_BYTES, &tmS, 0, (int)blockIdx.y, (k * TSTEP) >> 7, bar);
+        }
+        __syncwarp();
         if (++stage == p.ring) { stage = 0; phase ^= 1u; }
       }
       for (int s = 0; s < p.ring; ++s)
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(WG_THREADS)
       const int t = (lane & 7) + ((lane >> 4) << 3);
       const int ch = 2 * i + ((lane >> 3) & 1);  // 16-byte chunk of A's row
       // (the swizzle of a row of 32 MT bytes)
-      const int sw = MT == 4 ? (t & 7) : MT == 2 ? ((t >> 1) & 3) : ((t >> 2) & 1);
+      const int sw = MT == 2 ? ((t >> 1) & 3) : ((t >> 2) & 1);
       at_a[i] = (uint32_t)(C_::Q_BYTES + (t + part * 32) * 32 * MT + ((ch ^ sw) * 16));
     }
     int stage = 0;
@@ -354,9 +357,7 @@ cudaError_t launch_wgrad(const MxStreamArgs& a, LaunchCtx& ctx) {
   p.fault_injection = a.fault_injection;
   const int64_t tiles = mx_scale_tiles(MX_INT8, a.N);
   CUtensorMap mQ, mS, mA;
-  const CUtensorMapSwizzle sw = MT == 4   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : MT == 2 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                          : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUtensorMapSwizzle sw = MT == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
   const CUtensorMapDataType ty = std::is_same<T, __half>::value
                                      ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -376,8 +377,7 @@ cudaError_t launch_wgrad(const MxStreamArgs& a, LaunchCtx& ctx) {
 template <typename T>
 cudaError_t launch_wgrad_t(const MxStreamArgs& a, LaunchCtx& ctx) {
   if (a.M <= 16) return launch_wgrad<T, 1>(a, ctx);
-  if (a.M <= 32) return launch_wgrad<T, 2>(a, ctx);
-  return launch_wgrad<T, 4>(a, ctx);
+  return launch_wgrad<T, 2>(a, ctx);
 }
 
 }  // namespace

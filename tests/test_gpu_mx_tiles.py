@@ -24,8 +24,9 @@ def test_forced_tile(lib_path, gpu, tile):
 
 @pytest.mark.parametrize("form", [0, 1, 2, 5, 8])
 def test_forced_converted_form(lib_path, gpu, form):
-    """The converted product (GEMM_GB300_MX_MIXED): 0 block pairs, otherwise
-    single blocks with K in that many slices."""
+    """Products with a 16-bit operand (GEMM_GB300_MX_MIXED): 0 the stored operand
+    always expanded, otherwise always converted where there is such a kernel,
+    with K in that many slices."""
     env = dict(os.environ, GEMM_GB300_MX_MIXED=str(form))
     r = subprocess.run([sys.executable, "-m", "pytest", os.path.join(HERE, "test_gpu_mx.py"), "-q",
                         "-x", "-m", "gpu", "-k", "mixed or converted"], env=env,
