@@ -40,10 +40,12 @@ constexpr int ROWS = 128;          // rows of B a block takes
 constexpr int KSTEP = 256;         // codes of K a stage holds
 constexpr int WARPS = 8;            // 16 rows of B each
 constexpr int ST_THREADS = 32 * (WARPS + 1);
-constexpr int MAX_RING = 3;
+// Two stages a block: small blocks, several an SM, keep more loads in flight than
+// deeper rings (32 x 8192 x 8192 fp4 29.6 us with three, 22.5 with two; 8 rows
+// 15.2 / 14.6)
+constexpr int RING = 2;
 constexpr int SUM_PITCH = ROWS + 4;  // (a quad's four columns in different banks)
 constexpr int MAX_SPLIT = 8;       // blocks of a cluster (the portable limit)
-constexpr int SMEM_MAX = 227 * 1024;
 
 // A's type: fp16, bf16, or codes of B's format
 enum { X_F16 = 1, X_BF16 = 2, X_FP4 = 3 };
@@ -58,8 +60,6 @@ struct SCfg {
   static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES + XS_BYTES;
   static constexpr int SUMS = SUM_PITCH * 8 * NT * 4;
   static constexpr int smem(int ring) { return ring * STAGE + SUMS + 1024 + 256; }
-  static constexpr int RING_MAX = (SMEM_MAX - SUMS - 1280) / STAGE;
-  static constexpr int RING = RING_MAX < MAX_RING ? RING_MAX : MAX_RING;
 };
 
 struct SParams {
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(ST_THREADS)
   uint64_t* const bars = reinterpret_cast<uint64_t*>(base_ptr + p.ring * C_::STAGE + C_::SUMS);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(MAX_RING + s); };
-  volatile uint32_t* const abort_flag = reinterpret_cast<uint32_t*>(bars + 2 * MAX_RING);
+  auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(RING + s); };
+  volatile uint32_t* const abort_flag = reinterpret_cast<uint32_t*>(bars + 2 * RING);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster is a row of the grid
@@ -349,7 +349,7 @@ cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
   using C_ = SCfg<FMT, XT, NT>;
   auto kern = mx_stream_kernel<FMT, XT, NT>;
   static const cudaError_t attr = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::smem(C_::RING));
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::smem(RING));
   if (attr != cudaSuccess) return attr;
   SParams p;
   p.M = a.M; p.N = a.N; p.K = a.K;
@@ -364,21 +364,24 @@ cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
   p.per = p.stages;
   for (int s = MAX_SPLIT; s > 1; --s) {
     const int per = (p.stages + s - 1) / s, n = (p.stages + per - 1) / per;
-    const int ring = per < C_::RING ? per : C_::RING;
+    const int ring = per < RING ? per : RING;
     // (queried once for each cluster and ring size)
-    static std::atomic<int> slots[MAX_SPLIT + 1][MAX_RING + 1];
+    static std::atomic<int> slots[MAX_SPLIT + 1][RING + 1];
     int have = slots[n][ring].load(std::memory_order_relaxed);
     if (have == 0) {
       have = 1 + resident_clusters((const void*)kern, n, ST_THREADS, (size_t)C_::smem(ring));
       slots[n][ring].store(have, std::memory_order_relaxed);
     }
+    // (blocks of one stage only where blocks of two would leave SMs without one: 1 x
+    // 5632 x 2048 6.3 us in 352 blocks, 5.3 in 176)
+    if (per == 1 && rb * mg * ((p.stages + 1) / 2) >= a.num_sms) continue;
     if (rb * mg < have) {
       splits = n;
       p.per = per;
       break;
     }
   }
-  p.ring = p.per < C_::RING ? p.per : C_::RING;
+  p.ring = p.per < RING ? p.per : RING;
   p.C = a.C; p.ldc = a.ldc; p.out = a.out;
   p.alpha = a.alpha; p.beta = a.beta;
   p.ep = a.ep;
