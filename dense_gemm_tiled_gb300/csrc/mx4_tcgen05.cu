@@ -19,6 +19,10 @@
 //              tensor memory (tcgen05.cp: 32 rows x 16 bytes onto 32 lanes x 4
 //              columns, repeated to all four lane quarters) and issues the MMAs
 //   warps 2..  epilogue
+// Measured: 8192^3 fp4 to bf16 170 us (6.5 PFLOP/s) on pairs of 256 x 256, tensor
+// pipe 75 % of SM-active cycles; the MMAs and scale copies without loads take 144.
+// Two 128 x 128 or 256 x 128 tiles' accumulators fit beside the scales, one of 256
+// x 256: its epilogue empties it into registers first, about 1 us a tile.
 // The storage's scale tile is that copy's source as it lies in memory.  Each
 // ring stage has scale columns of its own in tensor memory: a stage is refilled
 // only after the MMAs that read it completed, so its columns are free then too.

@@ -5,7 +5,9 @@
 // A [T, M] fp16 or bf16 with M up to 32 columns, q the checkpoint of the
 // layer's input, [T, N] (the tn product of "Metal GEMM Kernels for LoRA Training
 // on Apple Silicon", section 5, with its right operand stored in 8 bits).
-// Bound by the bytes of the checkpoint, each read once.
+// Bound by the bytes of the checkpoint, each read once: 32 x 8192 x 8192 fp16 takes
+// 25.8 us, 2.7 TB/s, where 70 MB at HBM's rate would be 10.4; what is left is the
+// instructions that turn codes into operands.
 //
 // A block takes 128 columns of the checkpoint and a slice of T; a cluster's
 // blocks share the columns and split T.  A producer warp brings 64 rows of q (128-
@@ -15,6 +17,11 @@
 // of four rows and interleaves them with byte permutes, so one pass makes the
 // operands of four 8-column tiles (column 4g + j of the quarter in tile j).  A
 // comes through ldmatrix.trans.
+//   Every row has a scale of its own, so a pair of rows needs both scales side by
+// side: one more warp makes these once a stage (32 row pairs x 4 blocks) for all
+// the others, which otherwise spent a third of their instructions on them (28.3
+// -> 25.8 us at the size below; two blocks of ten warps an SM: three, at 64
+// registers a thread, 31.3; the loading warp making them as well, 36).
 //   A code becomes fp16 by putting its byte into 1024's fraction (1024 + q + 128,
 // exact); one FMA by the scale takes 1152 times the scale away, exactly while
 // the scale is a power of two between 2^-14 and 2.  Other scales, and bf16, go
@@ -39,7 +46,7 @@ namespace {
 constexpr int COLS = 128;   // columns of the checkpoint a block takes
 constexpr int TSTEP = 64;   // rows of it a stage holds
 constexpr int WG_WARPS = 8;
-constexpr int WG_THREADS = 32 * (WG_WARPS + 1);
+constexpr int WG_THREADS = 32 * (WG_WARPS + 2);  // and a producer, and the scales' warp
 constexpr int WG_RING = 4;
 constexpr int WG_PITCH = COLS + 4;  // of the sums (a row's start moves by 16 bytes of a bank row)
 constexpr int WG_SPLIT = 8;
@@ -48,9 +55,11 @@ template <int MT>
 struct GCfg {
   static constexpr int Q_BYTES = TSTEP * 128;
   static constexpr int A_BYTES = TSTEP * 32 * MT;
-  static constexpr int S_BYTES = 1024;  // one 512-byte tile, its slot a swizzle period
-  static constexpr int STAGE = Q_BYTES + A_BYTES + S_BYTES;
-  static constexpr uint32_t TX = Q_BYTES + A_BYTES + 512;
+  static constexpr int S_BYTES = 512;       // one scale tile
+  static constexpr int P_BYTES = 128 * 8;   // and the row pairs' scales made from it
+  static constexpr int PAD = 512;           // (a stage is whole swizzle periods)
+  static constexpr int STAGE = Q_BYTES + A_BYTES + S_BYTES + P_BYTES + PAD;
+  static constexpr uint32_t TX = Q_BYTES + A_BYTES + S_BYTES;
   static constexpr int SUMS = 16 * MT * WG_PITCH * 4;
   static constexpr int smem(int ring) { return ring * STAGE + SUMS + 1024 + 256; }
 };
@@ -98,6 +107,11 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (std::is_same<T, __half>::value) {
@@ -109,19 +123,35 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// Pairs (row 0, row 1) of four columns' values as 16-bit operands: a, b the two
-// rows' codes (each offset by 128), s0, s1 their scale bytes.
+// What a pair of rows' scale bytes become for code_pairs: two words.
+//   fp16, both between 2^-14 and 2 (activations below 254; they and 1152 times
+//   them are normal fp16 numbers): the scales as a half2, then -1152 times them
+//   otherwise: the scales in fp32, the first one's sign (scales are positive)
+//   telling the fp16 form so
 template <typename T>
-__device__ __forceinline__ void code_pairs(uint32_t a, uint32_t b, uint32_t s0, uint32_t s1,
-                                           uint32_t (&out)[4]) {
+__device__ __forceinline__ uint2 pair_scales(uint32_t s0, uint32_t s1) {
   if constexpr (std::is_same<T, __half>::value) {
     const uint32_t t = s0 | (s1 << 16);
-    // both scales between 2^-14 and 2 (activations below 254): they and 1152
-    // times them are normal fp16 numbers
     if (((t - 0x00710071u) & 0xFFF0FFF0u) == 0u) {
       const uint32_t sbits = (t - 0x00700070u) << 10;
-      const __half2 s = *reinterpret_cast<const __half2*>(&sbits);
-      const __half2 off = __hmul2(s, __float2half2_rn(-1152.f));
+      const __half2 off =
+          __hmul2(*reinterpret_cast<const __half2*>(&sbits), __float2half2_rn(-1152.f));
+      return make_uint2(sbits, *reinterpret_cast<const uint32_t*>(&off));
+    }
+    return make_uint2(__float_as_uint(e8m0_value(s0)) | 0x80000000u, __float_as_uint(e8m0_value(s1)));
+  } else {
+    return make_uint2(__float_as_uint(e8m0_value(s0)), __float_as_uint(e8m0_value(s1)));
+  }
+}
+
+// Pairs (row 0, row 1) of four columns' values as 16-bit operands: a, b the two
+// rows' codes (each offset by 128), sc their pair_scales.
+template <typename T>
+__device__ __forceinline__ void code_pairs(uint32_t a, uint32_t b, uint2 sc, uint32_t (&out)[4]) {
+  if constexpr (std::is_same<T, __half>::value) {
+    if ((int32_t)sc.x >= 0) {
+      const __half2 s = *reinterpret_cast<const __half2*>(&sc.x);
+      const __half2 off = *reinterpret_cast<const __half2*>(&sc.y);
       const uint32_t lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -134,7 +164,7 @@ __device__ __forceinline__ void code_pairs(uint32_t a, uint32_t b, uint32_t s0, 
   }
   // code + 128 in the fraction of 2^23, less 2^23 + 128: the code; times its
   // scale: exact in fp32 and, within its range, in the 16-bit type
-  const float f0 = e8m0_value(s0), f1 = e8m0_value(s1);
+  const float f0 = __uint_as_float(sc.x & 0x7FFFFFFFu), f1 = __uint_as_float(sc.y);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float x = __uint_as_float(__byte_perm(a, 0x4B000000u, 0x7540 + j)) - 8388736.f;
@@ -156,7 +186,8 @@ __global__ void __launch_bounds__(WG_THREADS)
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(WG_RING + s); };
-  volatile uint32_t* const abort_flag = reinterpret_cast<uint32_t*>(bars + 2 * WG_RING);
+  auto scale_bar = [&](int s) { return bar0 + 8u * (uint32_t)(2 * WG_RING + s); };
+  volatile uint32_t* const abort_flag = reinterpret_cast<uint32_t*>(bars + 3 * WG_RING);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = (int)gridDim.x, rank = (int)blockIdx.x;
@@ -166,6 +197,7 @@ __global__ void __launch_bounds__(WG_THREADS)
     for (int s = 0; s < p.ring; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), WG_WARPS);
+      mbar_init(scale_bar(s), 1);
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -213,17 +245,40 @@ __global__ void __launch_bounds__(WG_THREADS)
         if (pending & (1u << s))
           mbar_wait_drain(full_bar(s), (pend_phase >> s) & 1u, p.timeout_ns);
     }
+  } else if (warp > WG_WARPS) {
+    // ------------------------------------------------------------ scales of row pairs
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int k = k_lo; k < k_hi; ++k) {
+      if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, wc))) break;
+      const uint32_t tile =
+          base + (uint32_t)(stage * C_::STAGE + C_::Q_BYTES + C_::A_BYTES);
+      // entry 4 pair + block; rows 2 pair and 2 pair + 1 of the stage, which starts
+      // in the middle of its scale tile every other time
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = 32 * i + lane, t = ((k * TSTEP) & 127) + 2 * (at >> 2);
+        const uint32_t from = tile + (uint32_t)((t & 31) * 16 + (t >> 5) * 4 + (at & 3));
+        const uint2 v = pair_scales<T>(lds8(from), lds8(from + 16u));
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
+                         tile + (uint32_t)(C_::S_BYTES + at * 8)),
+                     "r"(v.x), "r"(v.y)
+                     : "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(scale_bar(stage));
+      if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+    }
   } else {
     // ------------------------------------------------------------ products
     // this lane's places within a stage: rows 2 c + (i & 1) + 8 (i >> 1) of a
     // 16-row step (the swizzle goes by the row's last three bits: the same for
     // every step)
-    uint32_t at_q[2], at_a[MT], at_s[2];
+    uint32_t at_q[2], at_a[MT];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * c + i;
       at_q[i] = (uint32_t)(t * 128 + (((2 * quarter + (g >> 2)) ^ t) * 16) + 4 * (g & 3) + part * 4096);
-      at_s[i] = (uint32_t)(C_::Q_BYTES + C_::A_BYTES + t * 16 + quarter + part * 4);
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -234,32 +289,35 @@ __global__ void __launch_bounds__(WG_THREADS)
       const int sw = MT == 2 ? ((t >> 1) & 3) : ((t >> 2) & 1);
       at_a[i] = (uint32_t)(C_::Q_BYTES + (t + part * 32) * 32 * MT + ((ch ^ sw) * 16));
     }
+    // (row pair 16 part + c of the stage's 32, this quarter's block)
+    const uint32_t at_s = (uint32_t)(C_::Q_BYTES + C_::A_BYTES + C_::S_BYTES +
+                                     ((16 * part + c) * 4 + quarter) * 8);
     int stage = 0;
     uint32_t phase = 0;
     for (int k = k_lo; k < k_hi; ++k) {
       bool ok = false;
-      if (lane == 0) ok = mbar_wait(full_bar(stage), phase, wc);
+      // (the codes' own barrier too: it is the scales' warp that has seen it)
+      if (lane == 0)
+        ok = mbar_wait(scale_bar(stage), phase, wc) && mbar_wait(full_bar(stage), phase, wc);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       const uint32_t q = base + (uint32_t)(stage * C_::STAGE);
-      // (64 rows on: two words on in the scale tile's rows)
-      const uint32_t s_in = q + (uint32_t)(((k * TSTEP) & 127) / 32 * 4);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {  // rows 32 part + 16 kk .. + 15 of the stage
         uint32_t am[MT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
           ldmatrix_x4_trans(q + at_a[i] + (uint32_t)(kk * 16 * 32 * MT), am[i]);
-        uint32_t w[4], sb[4];
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t down = (uint32_t)(kk * 16 + 8 * (i >> 1));
-          w[i] = lds32(q + at_q[i & 1] + down * 128u) ^ 0x80808080u;
-          sb[i] = lds8(s_in + at_s[i & 1] + down * 16u);
-        }
+        for (int i = 0; i < 4; ++i)
+          w[i] = lds32(q + at_q[i & 1] + (uint32_t)(kk * 16 + 8 * (i >> 1)) * 128u) ^ 0x80808080u;
+        // rows 2c, 2c + 1 and 8 further on: pairs 8 kk + c and 4 further on
+        const uint2 s0 = lds64(q + at_s + (uint32_t)(kk * 8 * 32));
+        const uint2 s1 = lds64(q + at_s + (uint32_t)((kk * 8 + 4) * 32));
         uint32_t lo[4], hi[4];
-        code_pairs<T>(w[0], w[1], sb[0], sb[1], lo);
-        code_pairs<T>(w[2], w[3], sb[2], sb[3], hi);
+        code_pairs<T>(w[0], w[1], s0, lo);
+        code_pairs<T>(w[2], w[3], s1, hi);
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
