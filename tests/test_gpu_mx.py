@@ -458,3 +458,53 @@ def test_converted_product(g, dtype, fmt, variant, M, N, K):
     c0 = f64(C0)
     g.gemm_mx(A, B, C0, transA=tA, transB=tB, alpha=0.5, beta=-1.0, bias=bias, act="gelu")
     check_product(C0, a, b, dtype, 0.5, -1.0, c0, f64(bias), "gelu")
+
+
+def far_rows(rows, cols, pitch, dtype, seed):
+    """A matrix whose rows lie `pitch` elements apart in one large allocation."""
+    base = torch.empty((rows - 1) * pitch + cols, dtype=DT[dtype], device="cuda")
+    v = base.as_strided((rows, cols), (pitch, 1))
+    if seed is not None:
+        v.copy_(matrix(rows, cols, dtype, seed))
+    return v
+
+
+def test_offsets_past_32_bits(g):
+    """Rows 2^31 elements (or bytes of codes) apart, and 130 rows 2^25 apart:
+    every byte and element offset passes 32 bits (allocations of 4 to 9 GB)."""
+    P = 1 << 31
+    X = far_rows(3, 100, P, "f16", 1)
+    codes = torch.empty(2 * P + 112, dtype=torch.uint8, device="cuda").as_strided((3, 112), (P, 1))
+    Q = g.Mx(codes, torch.empty(g.mx_scale_bytes("int8", 3, 100), dtype=torch.uint8, device="cuda"),
+             "int8", 3, 100)
+    Y = far_rows(3, 100, P, "f16", None)
+    g.mx_quantize(X, Q, act="gelu", Y=Y)
+    want, st, xq = mx_ref.store(f64(X), "int8")
+    assert np.array_equal(codes.cpu().numpy(), want) and np.array_equal(Q.scales.cpu().numpy(), st)
+    y = mx_ref.gelu(f64(X))
+    assert np.all(np.abs(f64(Y) - y) <= 2.0 ** -20 * (np.abs(f64(X)) + np.abs(y)) + 2.0 ** -10 * np.abs(y) + 2.0 ** -24)
+    g.mx_dequantize(Q, Y)
+    assert torch.equal(Y.cpu(), torch.from_numpy(xq).to(torch.float16))
+    g.mx_act_backward(X, Q, Y, act="relu")
+    assert torch.equal(Y.cpu(), (torch.from_numpy(xq) > 0).half() * X.cpu())
+    del X, Y, codes, Q
+    torch.cuda.empty_cache()
+    P = 1 << 25
+    r = np.random.default_rng(6)
+    (A, a), (B, b) = (stored(g, r.standard_normal((n, 96)).astype(np.float32), "fp4") for n in (130, 104))
+    C = far_rows(130, 104, P, "f16", None)
+    g.gemm_mx(A, B, C)
+    check_product(C, a, b.T, "f16")
+    c0 = f64(C)
+    g.gemm_mx(A, B, C, alpha=0.5, beta=1.0)
+    check_product(C, a, b.T, "f16", 0.5, 1.0, c0)
+    X = far_rows(130, 96, P, "f16", 7)
+    for M in (130, 5):  # expanded or converted, and streamed
+        g.gemm_mx(X[:M], B, C[:M], transB=True)
+        check_product(C[:M].contiguous(), f64(X[:M]), b.T, "f16")
+    Q, q = stored(g, r.standard_normal((130, 200)).astype(np.float32), "int8")
+    W = torch.empty((96, 200), dtype=torch.float16, device="cuda")
+    g.gemm_mx(X, Q, W, transA=True)
+    check_product(W, f64(X).T, q, "f16")
+    g.gemm_mx(X[:, :24], Q, W[:24], transA=True)
+    check_product(W[:24], f64(X[:, :24]).T, q, "f16")
