@@ -328,8 +328,10 @@ int gemm_mx4(int format, int64_t M, int64_t N, int64_t K, int dtype, float alpha
  *     C = act(alpha * op(A) * op(B) + beta * C + bias[j]),
  * A and C of dtype as in gemm(); B stored in `format` as [K, N] (blocks along
  * N) or, with transB, as [N, K] (blocks along K); ldb in BYTES.  The values of
- * B are rounded to dtype before the product (exact but where fp16's range
- * ends).
+ * B are rounded to dtype before the product, which is exact but where fp16's
+ * range ends (with few rows of A a power-of-two scale beyond fp16's range is kept
+ * in fp32 instead).  Takes scratch in stream order where B is expanded for the
+ * other types' kernels, and where rows of A are not 16-byte aligned.
  */
 int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype,
             float alpha, float beta, const void* A, int64_t lda, const void* B, int64_t ldb,

@@ -382,7 +382,7 @@ def test_wgrad_scales_past_fp16(g, dtype):
     check_product(C, f64(A).T, b, dtype)
 
 
-@pytest.mark.parametrize("case", ["mx4", "stream", "wgrad"])
+@pytest.mark.parametrize("case", ["mx4", "stream", "wgrad", "convert"])
 def test_bounded_waits(lib_path, gpu, case):
     """A load that never comes ends as a status, not as a hang (the library's own
     test hook: the producer leaves out its first load)."""
@@ -391,11 +391,13 @@ def test_bounded_waits(lib_path, gpu, case):
     B, _ = stored(g, r.standard_normal((256, 512)).astype(np.float32), "int8" if case == "wgrad" else "fp4")
     M = 200 if case == "mx4" else 8
     A = stored(g, r.standard_normal((M, 512)).astype(np.float32), "fp4")[0] if case == "mx4" else \
-        matrix(*((256, 8) if case == "wgrad" else (8, 512)), "f16", 1)
-    C = torch.empty((M, 512 if case == "wgrad" else 256), dtype=torch.float16, device="cuda")
+        matrix(*{"wgrad": (256, 8), "convert": (8, 256), "stream": (8, 512)}[case], "f16", 1)
+    C = torch.empty((M, 512 if case in ("wgrad", "convert") else 256), dtype=torch.float16,
+                    device="cuda")
     call = lambda: g.gemm_mx(A, B, C, transA=case == "wgrad", transB=case == "stream")  # noqa: E731
     call()
     torch.cuda.synchronize()
+    assert g.last_path() == {"mx4": "mx_tc", "convert": "mx_convert"}.get(case, "mx_stream")
     want = C.clone()
     g.set_wait_timeout_ns(20_000_000)
     g.set_fault_injection(1)
