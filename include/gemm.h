@@ -285,7 +285,11 @@ int64_t gemm_mx_scale_bytes(int format, int64_t rows, int64_t cols);
  * Y: NULL, or act(X) (without mult) is written to it in the same pass, dtype,
  *   [rows, cols]: the forward pass of an activation whose input is kept in 8
  *   bits.  Not with transX (GEMM_ERR_UNSUPPORTED); act without Y is an error.
- *   Y may be X itself with the same pitch.
+ *   Y may be X itself with the same pitch.  GEMM_ACT_GELU is x Phi(x), in fp32
+ *   within a few ulp for every x.  (gemm_ex()'s fused x/2 (1 + erf(x / sqrt 2)) is
+ *   evaluated as that sum, whose error is about 2^-22 |x|: in fp32 the two differ
+ *   by as much, and for x below -4 mostly by gemm_ex()'s.)  GEMM_ACT_RELU is x
+ *   where x > 0, else 0, as gemm_ex()'s: a NaN becomes 0.
  */
 int gemm_mx_quantize(int format, int transX, int64_t rows, int64_t cols, int dtype, float mult,
                      const void* X, int64_t ldx, int act, void* Y, int64_t ldy, void* q,
@@ -300,8 +304,8 @@ int gemm_mx_dequantize(int format, int64_t rows, int64_t cols, const void* q, in
  * gemm_mx_act_backward -- the backward pass of Y = act(X) from X's checkpoint
  * in GEMM_MX_INT8:
  *     dX = dY * act'(x8),   dbias[j] = sum_i dX[i, j]
- * act'(x): GEMM_ACT_NONE 1; GEMM_ACT_RELU 1 where x > 0, else 0;
- * GEMM_ACT_GELU Phi(x) + x phi(x).  dY, dX: dtype, [rows, cols]; dX may be dY
+ * act'(x): GEMM_ACT_NONE 1; GEMM_ACT_RELU 1 where x > 0, else 0 (so also
+ * throughout a block that reads as NaN); GEMM_ACT_GELU Phi(x) + x phi(x).  dY, dX: dtype, [rows, cols]; dX may be dY
  * itself with the same pitch.  dbias: NULL or cols fp32 sums (of the values
  * before their rounding to dtype, in an order that does not change from call to
  * call).  rows == 0 sets dbias to zero.
