@@ -17,6 +17,9 @@ static_assert((int)GEMM_MX_FP4 == (int)MX_FP4 && (int)GEMM_MX_FP4_E4M3 == (int)M
 namespace {
 
 constexpr int64_t LIM = (int64_t)1 << 31;
+// Products' sizes end earlier: the kernels and the copies around them count
+// stages, tiles and a grid's strides (up to 2^17 elements past an end) in 32 bits.
+constexpr int64_t PRODUCT_LIM = LIM - ((int64_t)1 << 18);
 
 // Rows up to which a product streams its 4-bit right operand.
 constexpr int64_t WGRAD_ROWS = 32;  // (columns of A, in the tn product)
@@ -78,7 +81,7 @@ int check_product(int64_t M, int64_t N, int64_t K, int dtype, const void* C, int
                   const void* bias, int act) {
   if (!known_type(dtype) || !known_act(act)) return GEMM_ERR_INVALID_ARG;
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
-  if (M >= LIM || N >= LIM || K >= LIM) return GEMM_ERR_UNSUPPORTED;
+  if (M > PRODUCT_LIM || N > PRODUCT_LIM || K > PRODUCT_LIM) return GEMM_ERR_UNSUPPORTED;
   if (ldc < (N > 1 ? N : 1)) return GEMM_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return GEMM_OK;
   const int64_t e = type_bytes(dtype);

@@ -320,7 +320,8 @@ int gemm_mx_act_backward(int64_t rows, int64_t cols, int dtype, int act, const v
  * A [M, K] and B [N, K] stored in the same 4-bit format (blocks along K), C of
  * dtype; products of codes and scales exact, fp32 accumulation.  lda, ldb in
  * BYTES (see above), ldc in elements; bias and act as gemm_ex().
- * GEMM_ERR_UNSUPPORTED for GEMM_MX_INT8.
+ * GEMM_ERR_UNSUPPORTED for GEMM_MX_INT8, and (as for gemm_mx()) where M, N or K
+ * is above 2^31 - 2^18.
  */
 int gemm_mx4(int format, int64_t M, int64_t N, int64_t K, int dtype, float alpha, float beta,
              const void* A, int64_t lda, const void* As, const void* B, int64_t ldb,
