@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM - 1 - (GENERAL ? 1 : 0)
 __global__ void mx_column_sum_kernel(const float* part, int blocks, int cols, float* out) {
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= cols) return;
   float v = 0.f;
 #pragma unroll 8
@@ -673,7 +673,7 @@ cudaError_t act_backward_t(const MxActBwdArgs& a, LaunchCtx& ctx) {
                                 ctx.stream, 1, p);
   if (e == cudaSuccess) ctx.launches++;
   if (e == cudaSuccess && a.dbias) {
-    e = launch_kernel(mx_column_sum_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(64), 0,
+    e = launch_kernel(mx_column_sum_kernel, dim3((unsigned)(((int64_t)a.cols + 63) / 64)), dim3(64), 0,
                       ctx.stream, 1, (const float*)a.part, (int)grid.y, a.cols, a.dbias);
     if (e == cudaSuccess) ctx.launches++;
   }
