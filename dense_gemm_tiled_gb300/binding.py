@@ -226,10 +226,13 @@ def _ld(t) -> int:
 
 
 _DTYPES = {}
+_get_raw_stream = None  # device index -> raw handle of its current stream, where torch has it
 
 
-def _dtype_codes():
+def _torch_tables():
+    global _get_raw_stream
     import torch
+    _get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _DTYPES.update({torch.float32: F32, torch.float16: F16_F32ACC, torch.bfloat16: BF16_F32ACC})
 
 
@@ -253,10 +256,9 @@ ACTS = {"none": 0, "relu": 1, "gelu": 2}
 
 def _current_stream(device_index: int) -> int:
     """Raw handle of the current CUDA stream of a device."""
+    if _get_raw_stream is not None:
+        return _get_raw_stream(device_index)
     import torch
-    get_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if get_raw is not None:
-        return get_raw(device_index)
     return torch.cuda.current_stream(device_index).cuda_stream
 
 
@@ -349,13 +351,34 @@ class Mx:
     """A matrix [rows, cols] in microscaled storage: `codes`, a 2-D uint8 CUDA
     tensor of `rows` rows (row pitch a multiple of 16 bytes, at least
     mx_row_bytes), and `scales`, a contiguous uint8 CUDA tensor of at least
-    mx_scale_bytes elements.  fmt: 'fp4', 'fp4_e4m3' or 'int8'."""
-    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "pitch", "ptr", "sptr")
+    mx_scale_bytes elements.  fmt: 'fp4', 'fp4_e4m3' or 'int8'.
+
+    The tensors are read on each call, as gemm() reads its operands: storage that
+    was replaced (`.data`, `set_()`, a new tensor in `codes`) is used from then
+    on, and refused if it does not hold the matrix."""
+    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "_seen", "_operand")
 
     def __init__(self, codes, scales, fmt, rows, cols):
         code = MX_FORMATS.get(fmt)
         if code is None:
             raise ValueError(f"unknown format {fmt!r}")
+        self.codes, self.scales, self.fmt, self.format = codes, scales, fmt, code
+        self.rows, self.cols = rows, cols
+        self._check((codes.data_ptr(), scales.data_ptr(), codes.nbytes, codes.stride(), scales.nbytes))
+
+    def operand(self):
+        """(address of the codes, their row pitch, address of the scales), of the
+        tensors as they are now; checked again whenever one of them lies elsewhere
+        or has another size or pitch."""
+        codes, scales = self.codes, self.scales
+        seen = (codes.data_ptr(), scales.data_ptr(), codes.nbytes, codes.stride(), scales.nbytes)
+        if seen != self._seen:
+            self._check(seen)
+        return self._operand
+
+    def _check(self, seen):
+        codes, scales, rows, cols, code = self.codes, self.scales, self.rows, self.cols, self.format
+        self._seen = None
         if not (codes.is_cuda and scales.is_cuda):
             raise ValueError("stored operands are CUDA tensors")
         if codes.itemsize != 1 or scales.itemsize != 1:
@@ -363,18 +386,18 @@ class Mx:
         # (mx_row_bytes and mx_scale_bytes, without a call into the library)
         need = ((cols if code == 2 else (cols + 1) >> 1) + 15) & -16
         blocks = (cols + 15) >> 4 if code == 1 else (cols + 31) >> 5
-        shape, stride = codes.shape, codes.stride()
+        codes_at, scales_at, _, stride, scale_bytes = seen
+        shape = codes.shape
         if len(shape) != 2 or shape[0] != rows or shape[1] < need or \
                 (shape[1] > 1 and stride[1] != 1):
             raise ValueError(f"codes: {rows} rows of at least {need} bytes, contiguous within a row")
-        if scales.numel() < ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512 or \
+        if scale_bytes < ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512 or \
                 not scales.is_contiguous():
             raise ValueError("scales: a contiguous tensor of mx_scale_bytes(fmt, rows, cols) bytes")
-        self.codes, self.scales, self.fmt, self.format = codes, scales, fmt, code
-        self.rows, self.cols = rows, cols
         # (a single row's pitch is not used: any valid one)
-        self.pitch = stride[0] if rows > 1 else max(need, 16)
-        self.ptr, self.sptr = codes.data_ptr() or None, scales.data_ptr() or None
+        self._operand = (codes_at or None, stride[0] if rows > 1 else max(need, 16),
+                         scales_at or None)
+        self._seen = seen
 
 
 def mx_empty(rows, cols, fmt, device="cuda") -> Mx:
@@ -411,7 +434,7 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     s = (stream.cuda_stream if stream is not None else _current_stream(X.get_device())) or None
     rc = _lib.gemm_mx_quantize(Q.format, 1 if transX else 0, Q.rows, Q.cols, dtype, mult,
                                X.data_ptr() or None, _ld_of(sx, X.stride()), ACTS[act], yp, ldy,
-                               Q.ptr, Q.pitch, Q.sptr, s)
+                               *Q.operand(), s)
     if rc != OK:
         raise GemmError(rc)
     return Q
@@ -428,7 +451,7 @@ def mx_dequantize(Q, Y, stream=None):
     if not Y.is_cuda:
         raise ValueError("mx_dequantize() takes CUDA tensors")
     s = (stream.cuda_stream if stream is not None else _current_stream(Y.get_device())) or None
-    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, Q.ptr, Q.pitch, Q.sptr, dtype,
+    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, *Q.operand(), dtype,
                                  Y.data_ptr() or None, _ld_of(sy, Y.stride()), s)
     if rc != OK:
         raise GemmError(rc)
@@ -456,7 +479,7 @@ def mx_act_backward(dY, Q, dX, act="gelu", dbias=None, stream=None):
         bp = dbias.data_ptr() or None
     s = (stream.cuda_stream if stream is not None else _current_stream(dY.get_device())) or None
     rc = _lib.gemm_mx_act_backward(Q.rows, Q.cols, dtype, ACTS[act], dY.data_ptr() or None,
-                                   _ld_of(sy, dY.stride()), Q.ptr, Q.pitch, Q.sptr,
+                                   _ld_of(sy, dY.stride()), *Q.operand(),
                                    dX.data_ptr() or None, _ld_of(sy, dX.stride()), bp, s)
     if rc != OK:
         raise GemmError(rc)
@@ -499,9 +522,8 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
             raise ValueError(f"inner dimensions differ: {K} vs {B.cols}")
         if A.rows != M or B.rows != N:
             raise ValueError(f"C is {(M, N)}, expected {(A.rows, B.rows)}")
-        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, alpha, beta, A.ptr, A.pitch, A.sptr, B.ptr,
-                           B.pitch, B.sptr, C.data_ptr() or None, _ld_of(sc, C.stride()), bp,
-                           ACTS[act], s)
+        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, alpha, beta, *A.operand(), *B.operand(),
+                           C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
     else:
         if A.dtype != dt:
             raise TypeError("A and C must share a dtype")
@@ -517,8 +539,8 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
         if Ma != M or Nb != N:
             raise ValueError(f"C is {(M, N)}, expected {(Ma, Nb)}")
         rc = _lib.gemm_mx(B.format, 1 if transA else 0, 1 if transB else 0, M, N, K, dtype, alpha,
-                          beta, A.data_ptr() or None, _ld_of(sa, A.stride()), B.ptr, B.pitch,
-                          B.sptr, C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
+                          beta, A.data_ptr() or None, _ld_of(sa, A.stride()), *B.operand(),
+                          C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
     if rc != OK:
         raise GemmError(rc)
     return C
@@ -550,6 +572,6 @@ def check_device_status(stream=None) -> int:
 
 
 try:
-    _dtype_codes()
+    _torch_tables()
 except ImportError:  # pragma: no cover - torch is needed only by the tensor wrappers
     pass
