@@ -356,7 +356,8 @@ class Mx:
     The tensors are read on each call, as gemm() reads its operands: storage that
     was replaced (`.data`, `set_()`, a new tensor in `codes`) is used from then
     on, and refused if it does not hold the matrix."""
-    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "_seen", "_operand")
+    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "_seen", "_operand",
+                 "device")
 
     def __init__(self, codes, scales, fmt, rows, cols):
         code = MX_FORMATS.get(fmt)
@@ -379,8 +380,9 @@ class Mx:
     def _check(self, seen):
         codes, scales, rows, cols, code = self.codes, self.scales, self.rows, self.cols, self.format
         self._seen = None
-        if not (codes.is_cuda and scales.is_cuda):
-            raise ValueError("stored operands are CUDA tensors")
+        device = codes.get_device()
+        if device < 0 or scales.get_device() != device:
+            raise ValueError("codes and scales are CUDA tensors of one device")
         if codes.itemsize != 1 or scales.itemsize != 1:
             raise TypeError("codes and scales are bytes")
         # (mx_row_bytes and mx_scale_bytes, without a call into the library)
@@ -397,7 +399,7 @@ class Mx:
         # (a single row's pitch is not used: any valid one)
         self._operand = (codes_at or None, stride[0] if rows > 1 else max(need, 16),
                          scales_at or None)
-        self._seen = seen
+        self._seen, self.device = seen, device
 
 
 def mx_empty(rows, cols, fmt, device="cuda") -> Mx:
@@ -422,19 +424,20 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     want = (Q.cols, Q.rows) if transX else (Q.rows, Q.cols)
     if sx != want:
         raise ValueError(f"X is {tuple(sx)}, expected {want}")
-    if not X.is_cuda:
-        raise ValueError("mx_quantize() takes CUDA tensors")
+    dev, stored = X.get_device(), Q.operand()
+    if dev < 0 or Q.device != dev:
+        raise ValueError("mx_quantize() takes CUDA tensors of one device")
     yp, ldy = None, 0
     if Y is not None:
-        if Y.dtype != dt or Y.shape != sx or not Y.is_cuda:
-            raise ValueError("Y has X's dtype and shape, on a CUDA device")
+        if Y.dtype != dt or Y.shape != sx or Y.get_device() != dev:
+            raise ValueError("Y has X's dtype, shape and device")
         yp, ldy = Y.data_ptr() or None, _ld_of(sx, Y.stride())
     elif act != "none":
         raise ValueError("act needs Y")
-    s = (stream.cuda_stream if stream is not None else _current_stream(X.get_device())) or None
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
     rc = _lib.gemm_mx_quantize(Q.format, 1 if transX else 0, Q.rows, Q.cols, dtype, mult,
                                X.data_ptr() or None, _ld_of(sx, X.stride()), ACTS[act], yp, ldy,
-                               *Q.operand(), s)
+                               *stored, s)
     if rc != OK:
         raise GemmError(rc)
     return Q
@@ -448,10 +451,11 @@ def mx_dequantize(Q, Y, stream=None):
     sy = Y.shape
     if sy != (Q.rows, Q.cols):
         raise ValueError(f"Y is {tuple(sy)}, expected {(Q.rows, Q.cols)}")
-    if not Y.is_cuda:
-        raise ValueError("mx_dequantize() takes CUDA tensors")
-    s = (stream.cuda_stream if stream is not None else _current_stream(Y.get_device())) or None
-    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, *Q.operand(), dtype,
+    dev, stored = Y.get_device(), Q.operand()
+    if dev < 0 or Q.device != dev:
+        raise ValueError("mx_dequantize() takes CUDA tensors of one device")
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
+    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, *stored, dtype,
                                  Y.data_ptr() or None, _ld_of(sy, Y.stride()), s)
     if rc != OK:
         raise GemmError(rc)
@@ -468,18 +472,20 @@ def mx_act_backward(dY, Q, dX, act="gelu", dbias=None, stream=None):
         raise TypeError(f"unsupported dtype {dt}")
     if Q.fmt != "int8":
         raise TypeError("the checkpoint is an 'int8' Mx")
-    if dX.dtype != dt or sy != (Q.rows, Q.cols) or dX.shape != sy or \
-            not (dY.is_cuda and dX.is_cuda):
+    if dX.dtype != dt or sy != (Q.rows, Q.cols) or dX.shape != sy:
         raise ValueError(f"dY and dX: {(Q.rows, Q.cols)} CUDA tensors of one dtype")
+    dev, stored = dY.get_device(), Q.operand()
+    if dev < 0 or Q.device != dev or dX.get_device() != dev:
+        raise ValueError("mx_act_backward() takes CUDA tensors of one device")
     bp = None
     if dbias is not None:
-        if not dbias.is_cuda or dbias.numel() != Q.cols or _DTYPES.get(dbias.dtype) != F32 or \
+        if dbias.get_device() != dev or dbias.numel() != Q.cols or _DTYPES.get(dbias.dtype) != F32 or \
                 not dbias.is_contiguous():
             raise ValueError("dbias: a contiguous float32 CUDA tensor of cols elements")
         bp = dbias.data_ptr() or None
-    s = (stream.cuda_stream if stream is not None else _current_stream(dY.get_device())) or None
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
     rc = _lib.gemm_mx_act_backward(Q.rows, Q.cols, dtype, ACTS[act], dY.data_ptr() or None,
-                                   _ld_of(sy, dY.stride()), *Q.operand(),
+                                   _ld_of(sy, dY.stride()), *stored,
                                    dX.data_ptr() or None, _ld_of(sy, dX.stride()), bp, s)
     if rc != OK:
         raise GemmError(rc)
@@ -500,7 +506,8 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
     dtype = _DTYPES.get(dt)
     if dtype is None:
         raise TypeError(f"unsupported dtype {dt}")
-    if not C.is_cuda:
+    dev = C.get_device()
+    if dev < 0:
         raise ValueError("gemm_mx() takes CUDA tensors")
     sc = C.shape
     if len(sc) != 2:
@@ -508,10 +515,11 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
     M, N = sc
     bp = None
     if bias is not None:
-        if not bias.is_cuda or bias.dtype != dt or bias.numel() != N or not bias.is_contiguous():
+        if bias.get_device() != dev or bias.dtype != dt or bias.numel() != N or not bias.is_contiguous():
             raise ValueError("bias: a contiguous CUDA tensor of N elements of C's dtype")
         bp = bias.data_ptr() or None
-    s = (stream.cuda_stream if stream is not None else _current_stream(C.get_device())) or None
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
+    stored = B.operand()
     if isinstance(A, Mx):
         if transA or transB:
             raise ValueError("two stored operands are both stored along K")
@@ -522,7 +530,10 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
             raise ValueError(f"inner dimensions differ: {K} vs {B.cols}")
         if A.rows != M or B.rows != N:
             raise ValueError(f"C is {(M, N)}, expected {(A.rows, B.rows)}")
-        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, alpha, beta, *A.operand(), *B.operand(),
+        a = A.operand()
+        if A.device != dev or B.device != dev:
+            raise ValueError("A, B and C are on one device")
+        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, alpha, beta, *a, *stored,
                            C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
     else:
         if A.dtype != dt:
@@ -530,8 +541,8 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
         sa = A.shape
         if len(sa) != 2:
             raise ValueError("matrices are 2-D")
-        if not A.is_cuda:
-            raise ValueError("gemm_mx() takes CUDA tensors")
+        if A.get_device() != dev or B.device != dev:
+            raise ValueError("A, B and C are CUDA tensors of one device")
         Ma, K = (sa[1], sa[0]) if transA else sa
         Kb, Nb = (B.cols, B.rows) if transB else (B.rows, B.cols)
         if K != Kb:
@@ -539,7 +550,7 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
         if Ma != M or Nb != N:
             raise ValueError(f"C is {(M, N)}, expected {(Ma, Nb)}")
         rc = _lib.gemm_mx(B.format, 1 if transA else 0, 1 if transB else 0, M, N, K, dtype, alpha,
-                          beta, A.data_ptr() or None, _ld_of(sa, A.stride()), *B.operand(),
+                          beta, A.data_ptr() or None, _ld_of(sa, A.stride()), *stored,
                           C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
     if rc != OK:
         raise GemmError(rc)

@@ -125,3 +125,36 @@ def test_replaced_storage_that_does_not_fit_is_refused(b, name, what):
     with pytest.raises(TypeError if what == "type" else ValueError):
         call()
     assert len(b.calls) == done
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_operands_of_two_devices_are_refused(b, name):
+    for dev in (0, 1):
+        call = every_call(b, mx(b, 130, 70, "int8", dev), mx(b, 40, 96, "fp4", dev),
+                          mx(b, 7, 96, "fp4", dev), dev)[name]
+        call()
+        done = len(b.calls)
+        call = every_call(b, mx(b, 130, 70, "int8", dev), mx(b, 40, 96, "fp4", dev),
+                          mx(b, 7, 96, "fp4", dev), 1 - dev)[name]
+        with pytest.raises(ValueError):
+            call()
+        assert len(b.calls) == done
+
+
+def test_every_tensor_is_on_the_device(b):
+    t = lambda *s, dev=0, dt=torch.float16: Fake(torch.zeros(s, dtype=dt), dev)  # noqa: E731
+    Q, B = mx(b, 130, 70, "int8"), mx(b, 40, 96, "fp4")
+    bad = [
+        lambda: b.mx_quantize(t(130, 70), Q, act="relu", Y=t(130, 70, dev=1)),
+        lambda: b.mx_act_backward(t(130, 70), Q, t(130, 70, dev=1)),
+        lambda: b.mx_act_backward(t(130, 70), Q, t(130, 70),
+                                  dbias=t(70, dev=1, dt=torch.float32)),
+        lambda: b.gemm_mx(t(5, 96, dev=1), B, t(5, 40), transB=True),
+        lambda: b.gemm_mx(t(5, 96), B, t(5, 40), transB=True, bias=t(40, dev=1)),
+        lambda: b.gemm_mx(mx(b, 5, 96, "fp4", 1), B, t(5, 40)),
+        lambda: b.Mx(Q.codes, Fake(Q.scales.t, 1), "int8", 130, 70),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    assert not b.calls
