@@ -364,7 +364,7 @@ class Mx:
         if code is None:
             raise ValueError(f"unknown format {fmt!r}")
         self.codes, self.scales, self.fmt, self.format = codes, scales, fmt, code
-        self.rows, self.cols = rows, cols
+        self.rows, self.cols = int(rows), int(cols)
         self._check((codes.data_ptr(), scales.data_ptr(), codes.nbytes, codes.stride(), scales.nbytes))
 
     def operand(self):
@@ -402,6 +402,11 @@ class Mx:
         self._seen, self.device = seen, device
 
 
+def _stored(Q, name):
+    if not isinstance(Q, Mx):
+        raise TypeError(f"{name} is a stored operand (an Mx), not a {type(Q).__name__}")
+
+
 def mx_empty(rows, cols, fmt, device="cuda") -> Mx:
     """Room for a stored matrix."""
     import torch
@@ -421,6 +426,7 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     dtype = _DTYPES.get(dt)
     if dtype is None:
         raise TypeError(f"unsupported dtype {dt}")
+    _stored(Q, "Q")
     want = (Q.cols, Q.rows) if transX else (Q.rows, Q.cols)
     if sx != want:
         raise ValueError(f"X is {tuple(sx)}, expected {want}")
@@ -435,7 +441,7 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     elif act != "none":
         raise ValueError("act needs Y")
     s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
-    rc = _lib.gemm_mx_quantize(Q.format, 1 if transX else 0, Q.rows, Q.cols, dtype, mult,
+    rc = _lib.gemm_mx_quantize(Q.format, 1 if transX else 0, Q.rows, Q.cols, dtype, float(mult),
                                X.data_ptr() or None, _ld_of(sx, X.stride()), ACTS[act], yp, ldy,
                                *stored, s)
     if rc != OK:
@@ -448,6 +454,7 @@ def mx_dequantize(Q, Y, stream=None):
     dtype = _DTYPES.get(Y.dtype)
     if dtype is None:
         raise TypeError(f"unsupported dtype {Y.dtype}")
+    _stored(Q, "Q")
     sy = Y.shape
     if sy != (Q.rows, Q.cols):
         raise ValueError(f"Y is {tuple(sy)}, expected {(Q.rows, Q.cols)}")
@@ -470,6 +477,7 @@ def mx_act_backward(dY, Q, dX, act="gelu", dbias=None, stream=None):
     dtype = _DTYPES.get(dt)
     if dtype is None:
         raise TypeError(f"unsupported dtype {dt}")
+    _stored(Q, "Q")
     if Q.fmt != "int8":
         raise TypeError("the checkpoint is an 'int8' Mx")
     if dX.dtype != dt or sy != (Q.rows, Q.cols) or dX.shape != sy:
@@ -519,6 +527,7 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
             raise ValueError("bias: a contiguous CUDA tensor of N elements of C's dtype")
         bp = bias.data_ptr() or None
     s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
+    _stored(B, "B")
     stored = B.operand()
     if isinstance(A, Mx):
         if transA or transB:
@@ -533,7 +542,7 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
         a = A.operand()
         if A.device != dev or B.device != dev:
             raise ValueError("A, B and C are on one device")
-        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, alpha, beta, *a, *stored,
+        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, float(alpha), float(beta), *a, *stored,
                            C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
     else:
         if A.dtype != dt:
@@ -549,8 +558,8 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
             raise ValueError(f"inner dimensions differ: {K} vs {Kb}")
         if Ma != M or Nb != N:
             raise ValueError(f"C is {(M, N)}, expected {(Ma, Nb)}")
-        rc = _lib.gemm_mx(B.format, 1 if transA else 0, 1 if transB else 0, M, N, K, dtype, alpha,
-                          beta, A.data_ptr() or None, _ld_of(sa, A.stride()), *stored,
+        rc = _lib.gemm_mx(B.format, 1 if transA else 0, 1 if transB else 0, M, N, K, dtype, float(alpha),
+                          float(beta), A.data_ptr() or None, _ld_of(sa, A.stride()), *stored,
                           C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
     if rc != OK:
         raise GemmError(rc)

@@ -158,3 +158,32 @@ def test_every_tensor_is_on_the_device(b):
         with pytest.raises(ValueError):
             call()
     assert not b.calls
+
+
+def test_scalars_that_gemm_takes(b):
+    """alpha, beta and mult as Python numbers, numpy scalars and 0-d tensors;
+    sizes as numpy integers."""
+    import numpy as np
+    t = lambda *s: Fake(torch.zeros(s, dtype=torch.float16))  # noqa: E731
+    Q, B, A = mx(b, np.int64(130), np.int32(70), "int8"), mx(b, 40, 96, "fp4"), mx(b, 7, 96, "fp4")
+    assert type(Q.rows) is int and type(Q.cols) is int
+    for half in (0.5, np.float32(0.5), np.float64(0.5), torch.tensor(0.5)):
+        b.mx_quantize(t(130, 70), Q, mult=half)
+        b.gemm_mx(t(5, 96), B, t(5, 40), transB=True, alpha=half, beta=half)
+        b.gemm_mx(A, B, t(7, 40), alpha=half, beta=half)
+        for (name, args), n in zip(b.calls[-3:], (1, 2, 2)):
+            given = [v for v in args if type(v) is float]
+            assert given == [0.5] * n, name
+    assert all(type(v) in (int, float, type(None)) for _, args in b.calls for v in args)
+
+
+def test_plain_tensors_in_a_stored_operands_place(b):
+    t = lambda *s: Fake(torch.zeros(s, dtype=torch.float16))  # noqa: E731
+    B = mx(b, 40, 96, "fp4")
+    for call in (lambda: b.gemm_mx(t(5, 96), t(96, 40), t(5, 40)),
+                 lambda: b.gemm_mx(B, t(96, 40), t(40, 40)),
+                 lambda: b.mx_quantize(t(4, 8), t(4, 8)), lambda: b.mx_dequantize(t(4, 8), t(4, 8)),
+                 lambda: b.mx_act_backward(t(4, 8), t(4, 8), t(4, 8))):
+        with pytest.raises(TypeError, match="stored operand"):
+            call()
+    assert not b.calls
