@@ -149,23 +149,25 @@ __device__ __forceinline__ void mx_encode16(const float (&x)[16], uint32_t byte,
     // an FMA (P. Markstein, "Computation of elementary functions on the IBM RISC
     // System/6000 processor", 1990).  |x| is at most a few times 6 s, or 448 is
     // s, so nothing overflows; where the residual is inexact (x below 2^-100) y
-    // is far below every code.
+    // is far below every code.  Computed negated, and the codes' signs turned
+    // back: a residual of 0 times -r is -0, to which a zero quotient of either
+    // sign adds without losing its own.
     float y[16];
     const float s = e4m3_value(byte);
     if (byte == 0u) {  // every code 0, with its element's sign
 #pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = copysignf(0.f, x[i]);
+      for (int i = 0; i < 16; ++i) y[i] = copysignf(0.f, -x[i]);
     } else {
       const float r = __frcp_rn(s);
-      const f32x2 r2 = pair(r), s2 = pair(-s);
+      const f32x2 r2 = pair(-r), s2 = pair(s);
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
         const f32x2 v = pair(x[i], x[i + 1]), y0 = mul2(v, r2);
         unpair(fma2(fma2(y0, s2, v), r2, y0), y[i], y[i + 1]);
       }
     }
-    c.w[0] = e2m1_word(y);
-    c.w[1] = e2m1_word(y + 8);
+    c.w[0] = e2m1_word(y) ^ 0x88888888u;
+    c.w[1] = e2m1_word(y + 8) ^ 0x88888888u;
     if (byte == 0x7Fu) c.w[0] = c.w[1] = 0u;
   } else {
     // times 2^(127 - byte), a normal number for every byte up to 253: exact

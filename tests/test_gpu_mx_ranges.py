@@ -1,0 +1,56 @@
+"""Stored operands at the ends of their ranges: signs of zeros, padding after a negative factor,
+scales far from 1 whose products are ordinary numbers, 16-bit values that overflow
+before their scale is applied, and scales that are no fp16 numbers."""
+import numpy as np
+import pytest
+import torch
+
+import mx_ref
+from helpers import to_np
+from oracle import compare
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(autouse=True)
+def _lib(lib_path, gpu):
+    yield
+
+
+@pytest.fixture
+def g():
+    from dense_gemm_tiled_gb300 import binding
+    return binding
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def stored(g, x64, fmt):
+    codes, st, v = mx_ref.store(x64, fmt)
+    return g.Mx(torch.from_numpy(codes).cuda(), torch.from_numpy(st).cuda(), fmt, *x64.shape), v
+
+
+def check(C, a, bT, dtype):
+    res = compare.check(to_np(C), a @ bT, np.abs(a) @ np.abs(bT), dtype)
+    assert res["ok"], res
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp4_e4m3"])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("trans", [False, True])
+def test_zeros_keep_their_sign(g, fmt, dtype, trans):
+    """In blocks of zeros alone and beside other values; a value too small for a
+    code is a zero of its sign as well."""
+    gen = torch.Generator().manual_seed(4)
+    x = torch.randn((40, 200), generator=gen)
+    x[:, ::3], x[:, ::6], x[:, 1::7], x[7, :70] = 0.0, -0.0, -2.0 ** -9, -0.0
+    x = x.to(DT[dtype])
+    Q = g.mx_empty(40, 200, fmt)
+    g.mx_quantize((x.t() if trans else x).contiguous().cuda(), Q, transX=trans)
+    codes, st, _ = mx_ref.store(x.double().numpy(), fmt)
+    assert np.array_equal(Q.scales.cpu().numpy(), st)
+    assert np.array_equal(Q.codes.cpu().numpy(), codes)
