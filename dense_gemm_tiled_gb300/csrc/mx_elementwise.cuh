@@ -220,6 +220,11 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(GENERAL))
         m = scale_bits(m, p.mult);
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] *= p.mult;
+        if (n < 16) {  // (absent columns stay 0: the code of -1 * 0 is another)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i >= n) x[i] = 0.f;
+        }
       }
       if (mx_block(FMT) == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       uint32_t byte = mx_scale_byte<FMT>(__uint_as_float(m));
@@ -294,6 +299,13 @@ __global__ void __launch_bounds__(TT_THREADS) mx_quantize_t_kernel(const QuantPa
         if (MULT) {
           lo[i] *= p.mult;
           hi[i] *= p.mult;
+        }
+      }
+      if (MULT && nc < 32) {  // (absent columns stay 0: the code of -1 * 0 is another)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (i >= nc) lo[i] = 0.f;
+          if (16 + i >= nc) hi[i] = 0.f;
         }
       }
       uint32_t ml = max_abs_bits(lo), mh = max_abs_bits(hi);

@@ -54,3 +54,23 @@ def test_zeros_keep_their_sign(g, fmt, dtype, trans):
     codes, st, _ = mx_ref.store(x.double().numpy(), fmt)
     assert np.array_equal(Q.scales.cpu().numpy(), st)
     assert np.array_equal(Q.codes.cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("fmt", list(mx_ref.BLOCK))
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("trans", [False, True])
+def test_padding_after_a_negative_factor(g, fmt, dtype, trans):
+    """Codes past a row's last column are zero bytes whatever mult's sign; zeros
+    inside it keep theirs (-1 * 0 is -0)."""
+    for rows, cols in [(1, 1), (3, 17), (130, 77), (33, 259), (70, 129)]:
+        gen = torch.Generator().manual_seed(cols)
+        x = torch.randn((rows, cols), generator=gen).to(DT[dtype])
+        x[:, ::5] = 0.0
+        x[:, ::10] = -0.0
+        Q = g.mx_empty(rows, cols, fmt)
+        Q.codes.fill_(0xA5)
+        X = (x.t() if trans else x).contiguous().cuda()
+        g.mx_quantize(X, Q, transX=trans, mult=-1.0)
+        codes, st, _ = mx_ref.store(x.double().numpy(), fmt, -1.0)
+        assert np.array_equal(Q.scales.cpu().numpy(), st)
+        assert np.array_equal(Q.codes.cpu().numpy(), codes), (rows, cols)
