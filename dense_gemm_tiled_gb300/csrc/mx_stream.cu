@@ -31,6 +31,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -238,84 +239,116 @@ __global__ void __launch_bounds__(ST_THREADS)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           sw[t][i] = lds32(s + s_at + (uint32_t)(t * 512 + i * 128));
+      // Two power-of-two scales: A's first, then B's.  A sum of code products, a
+      // multiple of 1/4 below 2^11, times a scale below 2^113 is exact and within
+      // fp32; where A has a greater one, the lesser of each two scales comes first
+      // (2^120 and 2^-120 would leave fp32 on their way to 1).
+      bool far = false;
+      if constexpr (FMT == MX_FP4 && XT == X_FP4) {
+        uint32_t top = 0;  // (bytes of 0xF0 and more)
 #pragma unroll
-      for (int b = 0; b < KSTEP / 32; ++b) {
-        // B's codes: rows g and g + 8, eight a lane
-        uint32_t wa[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t v = lds32(w + w_at + (uint32_t)(i * 1024) + (uint32_t)((b ^ g) * 16));
-          e2m1_halves(v, wa[i]);
-          if constexpr (FMT == MX_FP4_E4M3) {
-            const int blk = 2 * b + (c >> 1);  // of the stage's 16
-            const __half2 sc = e4m3_half2((sw[b / 2][i] >> (8 * (blk & 3))) & 255u);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) wa[i][j] = half2_mul(wa[i][j], sc);
-          }
-          if constexpr (XT == X_BF16) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) wa[i][j] = half2_to_bf162(wa[i][j]);
-          }
+        for (int i = lane; i < 8 * NT * TPS; i += 32) {
+          const int row = (m0 & 127) + i % (8 * NT);
+          const uint32_t word =
+              lds32(xs + (uint32_t)(i / (8 * NT) * 512 + (row & 31) * 16 + (row >> 5) * 4));
+          top |= word & (word >> 1) & (word >> 2) & (word >> 3) & 0x10101010u;
         }
-        const uint32_t a0[4] = {wa[0][0], wa[1][0], wa[0][1], wa[1][1]};
-        const uint32_t a1[4] = {wa[0][2], wa[1][2], wa[0][3], wa[1][3]};
-        float sc[2];
-        if constexpr (FMT == MX_FP4) {
+        far = __any_sync(0xffffffffu, top != 0u);
+      }
+      const auto products = [&](auto far_scales) {
+        [[maybe_unused]] constexpr bool FAR = decltype(far_scales)::value;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) sc[i] = e8m0_value((sw[b / 4][i] >> (8 * (b & 3))) & 255u);
-        }
+        for (int b = 0; b < KSTEP / 32; ++b) {
+          // B's codes: rows g and g + 8, eight a lane
+          uint32_t wa[2][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint32_t xb[4];
-          if constexpr (XT == X_FP4) {
-            const int r = 8 * j + g;
-            e2m1_halves(lds32(x + (uint32_t)(r * 128 + ((b ^ g) * 16) + 4 * c)), xb);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t v = lds32(w + w_at + (uint32_t)(i * 1024) + (uint32_t)((b ^ g) * 16));
+            e2m1_halves(v, wa[i]);
             if constexpr (FMT == MX_FP4_E4M3) {
-              const int blk = 2 * b + (c >> 1), row = (m0 & 127) + r;
-              const uint32_t word = lds32(xs + (uint32_t)((blk >> 2) * 512 + (row & 31) * 16 +
-                                                          (row >> 5) * 4));
-              const __half2 xsc = e4m3_half2((word >> (8 * (blk & 3))) & 255u);
+              const int blk = 2 * b + (c >> 1);  // of the stage's 16
+              const __half2 sc = e4m3_half2((sw[b / 2][i] >> (8 * (blk & 3))) & 255u);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) xb[e] = half2_mul(xb[e], xsc);
+              for (int j = 0; j < 4; ++j) wa[i][j] = half2_mul(wa[i][j], sc);
             }
-          } else {
-            const uint4 v = lds128(x + (uint32_t)((b * 8 * NT + 8 * j + g) * 64 + 16 * c));
-            xb[0] = v.x; xb[1] = v.y; xb[2] = v.z; xb[3] = v.w;
-          }
-          if constexpr (FMT == MX_FP4) {
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (XT == X_BF16) {
-              mma_bf16(part, a0, xb[0], xb[1]);
-              mma_bf16(part, a1, xb[2], xb[3]);
-            } else {
-              mma_f16(part, a0, xb[0], xb[1]);
-              mma_f16(part, a1, xb[2], xb[3]);
-            }
-            if constexpr (XT == X_FP4) {
-              // the scales of A's rows 2c and 2c + 1 of this tile
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int row = (m0 & 127) + 8 * j + 2 * c + e;
-                const uint32_t word =
-                    lds32(xs + (uint32_t)((b >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4));
-                const float xsc = e8m0_value((word >> (8 * (b & 3))) & 255u);
-                part[e] *= xsc;
-                part[2 + e] *= xsc;
+              for (int j = 0; j < 4; ++j) wa[i][j] = half2_to_bf162(wa[i][j]);
+            }
+          }
+          const uint32_t a0[4] = {wa[0][0], wa[1][0], wa[0][1], wa[1][1]};
+          const uint32_t a1[4] = {wa[0][2], wa[1][2], wa[0][3], wa[1][3]};
+          [[maybe_unused]] float sc[2];
+          if constexpr (FMT == MX_FP4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sc[i] = e8m0_value((sw[b / 4][i] >> (8 * (b & 3))) & 255u);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint32_t xb[4];
+            if constexpr (XT == X_FP4) {
+              const int r = 8 * j + g;
+              e2m1_halves(lds32(x + (uint32_t)(r * 128 + ((b ^ g) * 16) + 4 * c)), xb);
+              if constexpr (FMT == MX_FP4_E4M3) {
+                const int blk = 2 * b + (c >> 1), row = (m0 & 127) + r;
+                const uint32_t word = lds32(xs + (uint32_t)((blk >> 2) * 512 + (row & 31) * 16 +
+                                                            (row >> 5) * 4));
+                const __half2 xsc = e4m3_half2((word >> (8 * (blk & 3))) & 255u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) xb[e] = half2_mul(xb[e], xsc);
+              }
+            } else {
+              const uint4 v = lds128(x + (uint32_t)((b * 8 * NT + 8 * j + g) * 64 + 16 * c));
+              xb[0] = v.x; xb[1] = v.y; xb[2] = v.z; xb[3] = v.w;
+            }
+            if constexpr (FMT == MX_FP4) {
+              float part[4] = {0.f, 0.f, 0.f, 0.f};
+              if constexpr (XT == X_BF16) {
+                mma_bf16(part, a0, xb[0], xb[1]);
+                mma_bf16(part, a1, xb[2], xb[3]);
+              } else {
+                mma_f16(part, a0, xb[0], xb[1]);
+                mma_f16(part, a1, xb[2], xb[3]);
+              }
+              if constexpr (XT == X_FP4) {
+                // the scales of A's rows 2c and 2c + 1 of this tile
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int row = (m0 & 127) + 8 * j + 2 * c + e;
+                  const uint32_t word =
+                      lds32(xs + (uint32_t)((b >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4));
+                  const uint32_t xb8 = (word >> (8 * (b & 3))) & 255u;
+                  if constexpr (!FAR) {
+                    const float xsc = e8m0_value(xb8);
+                    part[e] *= xsc;
+                    part[2 + e] *= xsc;
+                  } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {  // (255, NaN, is the greater)
+                      const uint32_t wb8 = (sw[b / 4][i] >> (8 * (b & 3))) & 255u;
+                      part[2 * i + e] *= e8m0_value(min(xb8, wb8));
+                      part[2 * i + e] *= e8m0_value(max(xb8, wb8));
+                    }
+                  }
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[j][e] = __fmaf_rn(part[e], FAR ? 1.f : sc[e >> 1], acc[j][e]);
+            } else {
+              if constexpr (XT == X_BF16) {
+                mma_bf16(acc[j], a0, xb[0], xb[1]);
+                mma_bf16(acc[j], a1, xb[2], xb[3]);
+              } else {
+                mma_f16(acc[j], a0, xb[0], xb[1]);
+                mma_f16(acc[j], a1, xb[2], xb[3]);
               }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = __fmaf_rn(part[e], sc[e >> 1], acc[j][e]);
-          } else {
-            if constexpr (XT == X_BF16) {
-              mma_bf16(acc[j], a0, xb[0], xb[1]);
-              mma_bf16(acc[j], a1, xb[2], xb[3]);
-            } else {
-              mma_f16(acc[j], a0, xb[0], xb[1]);
-              mma_f16(acc[j], a1, xb[2], xb[3]);
-            }
           }
         }
-      }
+      };
+      if (far) products(std::true_type{});
+      else products(std::false_type{});
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(stage));
       if (++stage == p.ring) { stage = 0; phase ^= 1u; }

@@ -74,3 +74,31 @@ def test_padding_after_a_negative_factor(g, fmt, dtype, trans):
         codes, st, _ = mx_ref.store(x.double().numpy(), fmt, -1.0)
         assert np.array_equal(Q.scales.cpu().numpy(), st)
         assert np.array_equal(Q.codes.cpu().numpy(), codes), (rows, cols)
+
+
+@pytest.mark.parametrize("shift", [124, -124, 125, -125])
+def test_opposite_scales_of_two_stored_operands(g, shift):
+    """Values about 2^124 and 2^-124 (2^125 and its inverse: scaled codes below 2^-126): every product of a
+    block is an ordinary number, in whatever order the scales are applied."""
+    for M, N, K in [(1, 40, 64), (7, 130, 700), (32, 200, 300)]:
+        r = np.random.default_rng(M)
+        A, a = stored(g, (r.standard_normal((M, K)) * 2.0 ** shift).astype(np.float32), "fp4")
+        B, b = stored(g, (r.standard_normal((N, K)) * 2.0 ** -shift).astype(np.float32), "fp4")
+        C = torch.empty((M, N), device="cuda")
+        g.gemm_mx(A, B, C)
+        assert g.last_path() == "mx_stream"
+        check(C, a, b.T, "f32")
+
+
+def test_opposite_scales_keep_nan(g):
+    r = np.random.default_rng(1)
+    x = (r.standard_normal((5, 96)) * 2.0 ** 124).astype(np.float32)
+    w = (r.standard_normal((40, 96)) * 2.0 ** -124).astype(np.float32)
+    x[1, 40], w[3, 0], w[7] = np.nan, np.inf, 0.0
+    (A, a), (B, b) = stored(g, x, "fp4"), stored(g, w, "fp4")
+    C = torch.empty((5, 40), device="cuda")
+    g.gemm_mx(A, B, C)
+    want = np.zeros((5, 40), dtype=bool)
+    want[1], want[:, 3] = True, True
+    assert np.array_equal(torch.isnan(C).cpu().numpy(), want)
+    assert torch.equal(C[[0, 2, 3, 4], 7].cpu(), torch.zeros(4))
