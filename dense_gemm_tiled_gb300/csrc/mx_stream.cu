@@ -13,9 +13,11 @@
 // K order within a 32-code group is the loads': lane c of a quad holds codes 8c
 // .. 8c + 7 (one word) and the same eight columns of A (one 16-byte load).
 //   Power-of-two scales are applied to the fp32 sums of a 32-code group, which
-// are exact products of codes and A; e4m3 scales to the codes, in fp16 (a 4-bit
-// significand times a 2-bit one: exact), since a group spans two of their blocks.
-// bf16 products take the codes as bf16 (exact too).
+// are exact products of codes and A, where A is fp16 or stored.  Other scales go
+// to the codes: e4m3 ones in fp16 (a 4-bit significand times a 2-bit one: exact),
+// since a group spans two of their blocks; powers of two, for a bf16 A, as bf16
+// (exact: it has fp32's exponents), since a sum of bf16 values times unscaled codes
+// may leave fp32 where the product does not.
 //   The slices' fp32 sums are joined through distributed shared memory in rank
 // order, so a result does not depend on timing.
 //   tcgen05 would use 8 to 32 of its 128 rows here and take 16-bit operands from
@@ -107,6 +109,16 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t h, __half2 s) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h), s);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t bf162_mul(uint32_t h, __nv_bfloat162 s) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&h), s);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// a power-of-two scale twice as bf16, which has fp32's exponents: 2^-127 is a
+// subnormal, 255 NaN
+__device__ __forceinline__ __nv_bfloat162 e8m0_bf162(uint32_t byte) {
+  const uint32_t v = (byte == 255u ? 0x7FC0u : byte == 0u ? 0x0040u : byte << 7) * 0x10001u;
+  return *reinterpret_cast<const __nv_bfloat162*>(&v);
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -144,6 +156,8 @@ __global__ void __launch_bounds__(ST_THREADS)
                      const __grid_constant__ CUtensorMap tmXS, const SParams p) {
   using C_ = SCfg<FMT, XT, NT>;
   constexpr int TPS = C_::TPS;
+  // power-of-two scales multiply the sums of a 32-code group (others the codes)
+  constexpr bool SUMS_SCALED = FMT == MX_FP4 && XT != X_BF16;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - smem_u32(smem_raw));
@@ -274,12 +288,17 @@ __global__ void __launch_bounds__(ST_THREADS)
             if constexpr (XT == X_BF16) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) wa[i][j] = half2_to_bf162(wa[i][j]);
+              if constexpr (FMT == MX_FP4) {
+                const __nv_bfloat162 sc = e8m0_bf162((sw[b / 4][i] >> (8 * (b & 3))) & 255u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) wa[i][j] = bf162_mul(wa[i][j], sc);
+              }
             }
           }
           const uint32_t a0[4] = {wa[0][0], wa[1][0], wa[0][1], wa[1][1]};
           const uint32_t a1[4] = {wa[0][2], wa[1][2], wa[0][3], wa[1][3]};
           [[maybe_unused]] float sc[2];
-          if constexpr (FMT == MX_FP4) {
+          if constexpr (SUMS_SCALED) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) sc[i] = e8m0_value((sw[b / 4][i] >> (8 * (b & 3))) & 255u);
           }
@@ -301,15 +320,10 @@ __global__ void __launch_bounds__(ST_THREADS)
               const uint4 v = lds128(x + (uint32_t)((b * 8 * NT + 8 * j + g) * 64 + 16 * c));
               xb[0] = v.x; xb[1] = v.y; xb[2] = v.z; xb[3] = v.w;
             }
-            if constexpr (FMT == MX_FP4) {
+            if constexpr (SUMS_SCALED) {
               float part[4] = {0.f, 0.f, 0.f, 0.f};
-              if constexpr (XT == X_BF16) {
-                mma_bf16(part, a0, xb[0], xb[1]);
-                mma_bf16(part, a1, xb[2], xb[3]);
-              } else {
-                mma_f16(part, a0, xb[0], xb[1]);
-                mma_f16(part, a1, xb[2], xb[3]);
-              }
+              mma_f16(part, a0, xb[0], xb[1]);
+              mma_f16(part, a1, xb[2], xb[3]);
               if constexpr (XT == X_FP4) {
                 // the scales of A's rows 2c and 2c + 1 of this tile
 #pragma unroll

@@ -102,3 +102,17 @@ def test_opposite_scales_keep_nan(g):
     want[1], want[:, 3] = True, True
     assert np.array_equal(torch.isnan(C).cpu().numpy(), want)
     assert torch.equal(C[[0, 2, 3, 4], 7].cpu(), torch.zeros(4))
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp4_e4m3"])
+def test_large_bf16_rows_times_small_weights(g, fmt):
+    """bf16 rows of 2^126: a sum of unscaled codes would leave fp32 while the
+    products with the weights do not; the same for every number of rows."""
+    r = np.random.default_rng(2)
+    B, b = stored(g, (r.standard_normal((70, 320)) * 2.0 ** -5).astype(np.float32), fmt)
+    for M in (1, 9, 32, 40):
+        x = torch.from_numpy(r.uniform(0.5, 1.0, (M, 320)) * 2.0 ** 122).to(torch.bfloat16).cuda()
+        x[:, ::7] *= 16.0
+        C = torch.empty((M, 70), dtype=torch.bfloat16, device="cuda")
+        g.gemm_mx(x, B, C, transB=True)
+        check(C, f64(x), b.T, "bf16")
