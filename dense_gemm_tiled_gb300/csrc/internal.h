@@ -304,13 +304,16 @@ struct MxStreamArgs {
   int transA = 0, transB = 1;  // (launch_mx_mixed)
 };
 // The converted product: A of type `out`, 16-byte aligned rows, op(A) op(B).
-// cudaErrorNotSupported (nothing launched) for the variants that have no kernel
-// (int8 but tn; transA otherwise), and where expanding B is the better plan.
 struct MixedPlan {
   int mt = 128, splits = 1;  // rows of C a tile covers, slices of K
   bool convert = true;       // false: expanding the operand is estimated to be faster
 };
 MixedPlan mixed_plan(int M, int N, int K, int num_sms);
+// Whether there is such a kernel (fp4 nt and nn, int8 tn), its grid holds the
+// problem and the plan is to convert.  To be asked before launch_mx_mixed().
+bool mx_mixed_takes(int format, int transA, int transB, int M, int N, int K, int num_sms);
+// cudaErrorNotSupported (nothing launched) where a tensor map does not take the
+// problem
 cudaError_t launch_mx_mixed(const MxStreamArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_mixed_f16(const MxStreamArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx_mixed_bf16(const MxStreamArgs& a, LaunchCtx& ctx);

@@ -280,14 +280,15 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
                     launch_scale(dtype, (int)M, (int)N, C, ldc, beta, ctx, ep));
   // 16-bit A: kernels that read B as it is stored.  A's rows go through the
   // tensor-memory-access unit: rows off 16-byte alignment (and a single row
-  // stored as a column) are copied into scratch first.
+  // stored as a column) are copied into scratch first, once the kernel is settled.
   const bool column = transA && M == 1;  // op(A) is one row
   const bool fp4 = format != GEMM_MX_INT8;
   const int tA = column && fp4 ? 0 : transA;
   const bool stream = fp4 && transB && !tA && M <= STREAM_ROWS;
   const bool wgrad = !fp4 && tA && !transB && M <= WGRAD_ROWS;
-  const bool converted = fp4 ? !tA : (tA && !transB);
-  if (dtype != GEMM_F32 && (stream || wgrad || converted)) {
+  if (dtype != GEMM_F32 &&
+      (stream || wgrad ||
+       mx_mixed_takes(format, tA, transB, (int)M, (int)N, (int)K, st.sms))) {
     Scratch ws;
     const void* Ad = A;
     int64_t ldad = lda;
@@ -307,12 +308,13 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
     if (rows == 1) ldad = (cols + 7) / 8 * 8;
     MxStreamArgs a{format, dtype, (int)M, (int)N, (int)K, Ad, ldad, nullptr, B, ldb, Bs, C, ldc,
                    alpha, beta, ep, st.sms, st.fault_injection, tA, transB};
-    ce = cudaErrorNotSupported;
-    if (stream) ce = launch_mx_stream(a, ctx);
-    else if (wgrad) ce = launch_mx_wgrad(a, ctx);
-    if (ce != cudaErrorNotSupported) return api_done(GEMM_PATH_MX_STREAM, ctx, ce);
-    if (converted) ce = launch_mx_mixed(a, ctx);
-    if (ce != cudaErrorNotSupported) return api_done(GEMM_PATH_MX_CONVERT, ctx, ce);
+    ce = stream  ? launch_mx_stream(a, ctx)
+         : wgrad ? launch_mx_wgrad(a, ctx)
+                 : launch_mx_mixed(a, ctx);
+    // (not supported: more columns than the grid holds, or a pitch past a tensor
+    // map's)
+    if (ce != cudaErrorNotSupported)
+      return api_done(stream || wgrad ? GEMM_PATH_MX_STREAM : GEMM_PATH_MX_CONVERT, ctx, ce);
   }
   // B expanded to the other operand's type in scratch, then that type's product
   const int64_t ldw = (bc + 7) / 8 * 8;

@@ -474,7 +474,6 @@ cudaError_t launch_mixed_v(const MxStreamArgs& a, LaunchCtx& ctx) {
   auto kern = mx_mixed_kernel<T, FMT, W_MN, X_MN>;
   constexpr int CODE_BYTES = mm_code_bytes<FMT>();
   const MixedPlan pl = mixed_plan(a.M, a.N, a.K, a.num_sms);
-  if (!pl.convert) return cudaErrorNotSupported;
   MixedParams p;
   p.M = a.M; p.N = a.N; p.K = a.K;
   p.mt = pl.mt;
@@ -488,7 +487,6 @@ cudaError_t launch_mixed_v(const MxStreamArgs& a, LaunchCtx& ctx) {
   const int splits = (p.steps + p.per - 1) / p.per;
   p.tiles_m = (int)(((int64_t)a.M + pl.mt - 1) / pl.mt);
   const int64_t tiles = (int64_t)p.tiles_m * (((int64_t)a.N + 127) / 128);
-  if (tiles > 65535) return cudaErrorNotSupported;
   p.C = a.C; p.ldc = a.ldc;
   p.alpha = a.alpha; p.beta = a.beta;
   p.ep = a.ep;
@@ -522,11 +520,8 @@ cudaError_t launch_mixed_v(const MxStreamArgs& a, LaunchCtx& ctx) {
 
 template <typename T>
 cudaError_t launch_mixed_t(const MxStreamArgs& a, LaunchCtx& ctx) {
+  if (a.format == MX_INT8) return launch_mixed_v<T, MX_INT8, true, true>(a, ctx);
   const bool fp4 = a.format == MX_FP4;
-  if (a.format == MX_INT8)
-    return a.transA && !a.transB ? launch_mixed_v<T, MX_INT8, true, true>(a, ctx)
-                                 : cudaErrorNotSupported;
-  if (a.transA) return cudaErrorNotSupported;
   if (a.transB)
     return fp4 ? launch_mixed_v<T, MX_FP4, false, false>(a, ctx)
                : launch_mixed_v<T, MX_FP4_E4M3, false, false>(a, ctx);

@@ -37,6 +37,13 @@ MixedPlan mixed_plan(int M, int N, int K, int num_sms) {
   return pl;
 }
 
+bool mx_mixed_takes(int format, int transA, int transB, int M, int N, int K, int num_sms) {
+  if (format == MX_INT8 ? !(transA && !transB) : transA != 0) return false;
+  const MixedPlan pl = mixed_plan(M, N, K, num_sms);
+  const int64_t tiles = ((int64_t)M + pl.mt - 1) / pl.mt * (((int64_t)N + 127) / 128);
+  return pl.convert && tiles <= 65535;
+}
+
 cudaError_t launch_mx_mixed_f16(const MxStreamArgs& a, LaunchCtx& ctx) {
   return launch_mixed_t<__half>(a, ctx);
 }
