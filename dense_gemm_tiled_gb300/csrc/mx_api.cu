@@ -23,7 +23,7 @@ constexpr int64_t PRODUCT_LIM = LIM - ((int64_t)1 << 18);
 
 // Rows up to which a product streams its 4-bit right operand.
 constexpr int64_t WGRAD_ROWS = 32;  // (columns of A, in the tn product)
-constexpr int64_t STREAM_ROWS = 32, STREAM_ROWS_4 = 32;
+constexpr int64_t STREAM_ROWS = 32;  // (what the streaming kernel holds)
 
 inline bool known_format(int f) { return f >= GEMM_MX_FP4 && f <= GEMM_MX_INT8; }
 inline bool known_type(int d) {
@@ -235,7 +235,7 @@ int gemm_mx4(int format, int64_t M, int64_t N, int64_t K, int dtype, float alpha
   if (K == 0)
     return api_done(GEMM_PATH_SCALE, ctx,
                     launch_scale(dtype, (int)M, (int)N, C, ldc, beta, ctx, ep));
-  if (M <= STREAM_ROWS_4) {
+  if (M <= STREAM_ROWS) {
     MxStreamArgs a{format, dtype, (int)M, (int)N, (int)K, A, lda, As, B, ldb, Bs, C, ldc, alpha,
                    beta, ep, st.sms, st.fault_injection};
     const cudaError_t ce = launch_mx_stream(a, ctx);

@@ -481,7 +481,9 @@ cudaError_t launch_mixed_v(const MxStreamArgs& a, LaunchCtx& ctx) {
   const int stage = p.x_bytes + CODE_BYTES + MM_S_BYTES;
   p.ring = (SMEM_LIMIT - MM_FIXED - MM_TILES * MM_W_BYTES) / stage;
   if (p.ring > MM_MAX_STAGES) p.ring = MM_MAX_STAGES;
-  if (p.ring < MM_GROUPS) return cudaErrorNotSupported;  // (never: five at 128 rows)
+  static_assert((SMEM_LIMIT - MM_FIXED - MM_TILES * MM_W_BYTES) /
+                        (128 * 128 + CODE_BYTES + MM_S_BYTES) >= MM_GROUPS,
+                "a ring of as many stages as there are groups, at the most rows");
   p.steps = (a.K + MM_K - 1) / MM_K;
   p.per = (p.steps + pl.splits - 1) / pl.splits;
   const int splits = (p.steps + p.per - 1) / p.per;

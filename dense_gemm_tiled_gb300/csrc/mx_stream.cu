@@ -171,7 +171,6 @@ __global__ void __launch_bounds__(ST_THREADS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = (int)gridDim.x, rank = (int)blockIdx.x;  // a cluster is a row of the grid
   const int n0 = (int)blockIdx.y * ROWS;
-  const int m0 = (int)blockIdx.z * 8 * NT;
   const int k_lo = rank * p.per, k_hi = min(p.stages, k_lo + p.per);
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ring; ++s) {
@@ -213,13 +212,13 @@ __global__ void __launch_bounds__(ST_THREADS)
           tma_load_3d(w, &tmW, k * 128, n0, 0, bar);
           tma_load_3d(s, &tmS, 0, k * TPS, n0 >> 7, bar);
           if constexpr (XT == X_FP4) {
-            tma_load_3d(x, &tmX, k * 128, m0, 0, bar);
-            tma_load_3d(xs, &tmXS, 0, k * TPS, m0 >> 7, bar);
+            tma_load_3d(x, &tmX, k * 128, 0, 0, bar);
+            tma_load_3d(xs, &tmXS, 0, k * TPS, 0, bar);
           } else {
             // 32 columns a box: [group][row][64 bytes]
 #pragma unroll
             for (int b = 0; b < KSTEP / 32; ++b)
-              tma_load_3d(x + (uint32_t)(b * 8 * NT * 64), &tmX, k * KSTEP + 32 * b, m0, 0, bar);
+              tma_load_3d(x + (uint32_t)(b * 8 * NT * 64), &tmX, k * KSTEP + 32 * b, 0, 0, bar);
           }
         }
         __syncwarp();
@@ -262,9 +261,8 @@ __global__ void __launch_bounds__(ST_THREADS)
         uint32_t top = 0;  // (bytes of 0xF0 and more)
 #pragma unroll
         for (int i = lane; i < 8 * NT * TPS; i += 32) {
-          const int row = (m0 & 127) + i % (8 * NT);
           const uint32_t word =
-              lds32(xs + (uint32_t)(i / (8 * NT) * 512 + (row & 31) * 16 + (row >> 5) * 4));
+              lds32(xs + (uint32_t)(i / (8 * NT) * 512 + i % (8 * NT) * 16));
           top |= word & (word >> 1) & (word >> 2) & (word >> 3) & 0x10101010u;
         }
         far = __any_sync(0xffffffffu, top != 0u);
@@ -309,9 +307,8 @@ __global__ void __launch_bounds__(ST_THREADS)
               const int r = 8 * j + g;
               e2m1_halves(lds32(x + (uint32_t)(r * 128 + ((b ^ g) * 16) + 4 * c)), xb);
               if constexpr (FMT == MX_FP4_E4M3) {
-                const int blk = 2 * b + (c >> 1), row = (m0 & 127) + r;
-                const uint32_t word = lds32(xs + (uint32_t)((blk >> 2) * 512 + (row & 31) * 16 +
-                                                            (row >> 5) * 4));
+                const int blk = 2 * b + (c >> 1);
+                const uint32_t word = lds32(xs + (uint32_t)((blk >> 2) * 512 + r * 16));
                 const __half2 xsc = e4m3_half2((word >> (8 * (blk & 3))) & 255u);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) xb[e] = half2_mul(xb[e], xsc);
@@ -328,9 +325,8 @@ __global__ void __launch_bounds__(ST_THREADS)
                 // the scales of A's rows 2c and 2c + 1 of this tile
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const int row = (m0 & 127) + 8 * j + 2 * c + e;
                   const uint32_t word =
-                      lds32(xs + (uint32_t)((b >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4));
+                      lds32(xs + (uint32_t)((b >> 2) * 512 + (8 * j + 2 * c + e) * 16));
                   const uint32_t xb8 = (word >> (8 * (b & 3))) & 255u;
                   if constexpr (!FAR) {
                     const float xsc = e8m0_value(xb8);
@@ -382,14 +378,13 @@ __global__ void __launch_bounds__(ST_THREADS)
   cluster_sync();
   // (a block finishes its share of the 128 columns, four a thread)
   const int q_lo = rank * (ROWS / 4) / splits, q_cnt = (rank + 1) * (ROWS / 4) / splits - q_lo;
-  const int mc = min(8 * NT, p.M - m0);
-  for (int i = threadIdx.x; i < q_cnt * mc; i += ST_THREADS) {
+  for (int i = threadIdx.x; i < q_cnt * p.M; i += ST_THREADS) {
     const int m = i / q_cnt, n = 4 * (q_lo + i % q_cnt);
     if (n0 + n >= p.N) continue;
     const float4 v = cluster_sum4(sums + (uint32_t)((m * SUM_PITCH + n) * 4), splits);
-    if (p.out == 0) finish4<float>(p, m0 + m, n0 + n, v);
-    else if (p.out == 1) finish4<__half>(p, m0 + m, n0 + n, v);
-    else finish4<__nv_bfloat16>(p, m0 + m, n0 + n, v);
+    if (p.out == 0) finish4<float>(p, m, n0 + n, v);
+    else if (p.out == 1) finish4<__half>(p, m, n0 + n, v);
+    else finish4<__nv_bfloat16>(p, m, n0 + n, v);
   }
   cluster_sync();  // no block leaves while another reads its sums
 }
@@ -406,8 +401,7 @@ cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
   p.M = a.M; p.N = a.N; p.K = a.K;
   p.stages = (a.K + KSTEP - 1) / KSTEP;
   const int64_t rb = ((int64_t)a.N + ROWS - 1) / ROWS;
-  const int64_t mg = ((int64_t)a.M + 8 * NT - 1) / (8 * NT);
-  if (rb > 65535 || mg > 65535) return cudaErrorNotSupported;
+  if (rb > 65535) return cudaErrorNotSupported;
   // The most slices of K whose clusters are all resident at once (a slice's
   // stages, up to the ring, are its block's loads in flight); one where no split
   // is.
@@ -425,8 +419,8 @@ cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
     }
     // (blocks of one stage only where blocks of two would leave SMs without one: 1 x
     // 5632 x 2048 6.3 us in 352 blocks, 5.3 in 176)
-    if (per == 1 && rb * mg * ((p.stages + 1) / 2) >= a.num_sms) continue;
-    if (rb * mg < have) {
+    if (per == 1 && rb * ((p.stages + 1) / 2) >= a.num_sms) continue;
+    if (rb < have) {
       splits = n;
       p.per = per;
       break;
@@ -457,9 +451,9 @@ cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
     ok = ok && make_map(&mX, XT == X_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                         a.A, a.M, a.K, a.lda, 32, 8 * NT, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return cudaErrorNotSupported;
-  ctx.grid = (int)(splits * rb * mg);
+  ctx.grid = (int)(splits * rb);
   const cudaError_t e =
-      launch_kernel(kern, dim3((unsigned)splits, (unsigned)rb, (unsigned)mg), dim3(ST_THREADS),
+      launch_kernel(kern, dim3((unsigned)splits, (unsigned)rb), dim3(ST_THREADS),
                     (size_t)C_::smem(p.ring), ctx.stream, splits, mW, mS, mX, mXS, p);
   if (e == cudaSuccess) ctx.launches++;
   return e;
@@ -469,6 +463,7 @@ template <int FMT, int XT>
 cudaError_t launch_stream_nt(const MxStreamArgs& a, LaunchCtx& ctx) {
   if (a.M <= 8) return launch_stream<FMT, XT, 1>(a, ctx);
   if (a.M <= 16) return launch_stream<FMT, XT, 2>(a, ctx);
+  // (M is at most 32)
   return launch_stream<FMT, XT, 4>(a, ctx);
 }
 template <int FMT>
