@@ -29,19 +29,19 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "per_device.h"
 
 namespace gb300 {
 namespace {
 
 int sm_count() {
-  static int sms = 0;
-  if (sms == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (sms <= 0) sms = 1;
-  }
-  return sms;
+  static CountPerDevice sms;
+  const int dev = call_device();
+  const int n = sms.get(dev, [dev] {
+    int q = 0;
+    return cudaDeviceGetAttribute(&q, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? q : -1;
+  });
+  return n > 0 ? n : 1;
 }
 
 int grid_for(int64_t work_items, int threads) {

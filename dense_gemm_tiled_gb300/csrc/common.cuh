@@ -474,15 +474,17 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Clusters of `cluster_x` blocks resident at once.  A cluster lives within a
-// GPC, so these are fewer than the SMs' room for its blocks.
-inline int resident_clusters(const void* kern, int cluster_x, int threads, size_t smem) {
+// Clusters of `cluster_x` blocks resident at once on the current device.  A
+// cluster lives within a GPC, so these are fewer than the SMs' room for its
+// blocks.  -1 where the query fails.
+inline int resident_clusters(const void* kern, int cluster_x, int threads, size_t smem,
+                             dim3 grid = dim3(0)) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cluster_x;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)cluster_x, 1024);
+  cfg.gridDim = grid.x ? grid : dim3((unsigned)cluster_x, 1024);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
@@ -490,7 +492,7 @@ inline int resident_clusters(const void* kern, int cluster_x, int threads, size_
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
     cudaGetLastError();
-    n = 0;
+    n = -1;
   }
   return n;
 }

@@ -23,6 +23,7 @@
 
 #include "../../include/gemm.h"
 #include "internal.h"
+#include "per_device.h"
 
 using namespace gb300;
 
@@ -41,13 +42,13 @@ namespace {
 
 __device__ unsigned int g_status_word;  // per device: bits of STATUS_*
 
-constexpr int MAX_DEVICES = 64;
 std::mutex g_mu;
 unsigned int* g_status_ptr[MAX_DEVICES];
 int g_num_sms[MAX_DEVICES];
 std::atomic<int64_t> g_total_launches{0};
 std::atomic<int64_t> g_timeout_ns{2000000000LL};
 std::atomic<int> g_fault_injection{0};
+thread_local int tl_device = 0;  // of the call in progress (call_device)
 thread_local int tl_last_path = GEMM_PATH_NONE;
 thread_local int tl_last_launches = 0;
 thread_local int tl_last_grid = 0;
@@ -93,6 +94,7 @@ int device_state(int* dev_out, unsigned int** status, int* sms) {
     g_num_sms[dev] = n > 0 ? n : 1;
     g_status_ptr[dev] = static_cast<unsigned int*>(p);
   }
+  tl_device = dev;
   *dev_out = dev;
   *status = g_status_ptr[dev];
   *sms = g_num_sms[dev];
@@ -964,6 +966,7 @@ int run_batched(int transA, int transB, int64_t M64, int64_t N64, int64_t K64, i
 }  // namespace
 
 namespace gb300 {
+int call_device() { return tl_device; }
 int api_state(ApiState* out) {
   const int rc = device_state(&out->dev, &out->status, &out->sms);
   out->timeout_ns = (uint64_t)g_timeout_ns.load();

@@ -54,6 +54,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "tensor_map.h"
 
 namespace gb300 {
@@ -1216,42 +1217,31 @@ __global__ void __launch_bounds__(256) hgemm_sk_reduce(const HParams p) {
 // ---------------------------------------------------------------- host side
 // How many two-block clusters of the pair kernel can be resident at once
 // (fewer than SMs / 2 when the SMs of a GPC do not all pair up).  Queried once
-// per kernel configuration.
+// per kernel configuration and device.
 template <typename T, int BN, bool A_MN, bool B_MN, int MODE>
 int pair_slots(int num_sms) {
-  static int n = 0;
-  if (n == 0) {
+  static CountPerDevice slots;
+  const int n = slots.get(call_device(), [num_sms] {
     using C_ = Cfg<BN, B_MN, MODE>;
     auto kern = hgemm_tc_kernel<T, BN, A_MN, B_MN, MODE>;
-    int q = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C_::SMEM_BYTES) == cudaSuccess) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(2 * (num_sms / 2));
-      cfg.blockDim = dim3(THREADS);
-      cfg.dynamicSmemBytes = C_::SMEM_BYTES;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&q, kern, &cfg) != cudaSuccess) q = 0;
-    }
-    n = q > 0 ? q : num_sms / 2;
-  }
-  return n;
+                             C_::SMEM_BYTES) != cudaSuccess)
+      return -1;
+    return resident_clusters((const void*)kern, 2, THREADS, C_::SMEM_BYTES, dim3(2 * (num_sms / 2)));
+  });
+  return n > 0 ? n : num_sms / 2;
 }
 
-// cudaFuncSetAttribute for the kernel's shared memory, once per
-// configuration (a driver call per GEMM otherwise).
+// cudaFuncSetAttribute for the kernel's shared memory, once per configuration
+// and device (a driver call per GEMM otherwise).
 template <typename T, int BN, bool A_MN, bool B_MN, int MODE>
 cudaError_t kernel_attributes() {
-  static const cudaError_t e = cudaFuncSetAttribute(
-      hgemm_tc_kernel<T, BN, A_MN, B_MN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      Cfg<BN, B_MN, MODE>::SMEM_BYTES);
-  return e;
+  static OncePerDevice set;
+  return set.run(call_device(), cudaSuccess, [] {
+    return cudaFuncSetAttribute(hgemm_tc_kernel<T, BN, A_MN, B_MN, MODE>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Cfg<BN, B_MN, MODE>::SMEM_BYTES);
+  });
 }
 
 template <typename T, int BN, bool A_MN, bool B_MN, int MODE>

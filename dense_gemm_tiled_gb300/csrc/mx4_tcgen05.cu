@@ -471,35 +471,26 @@ bool scale_map(CUtensorMap* m, const void* s, int64_t rows, int64_t tiles, int b
 }
 
 // Blocks (or pairs) resident at once: an SM each (pairs: as many as the GPU's
-// clusters of two allow, queried once).
+// clusters of two allow, queried once a device).
 template <typename T, int FMT, int BN, bool PAIR>
 int mx4_slots(int num_sms) {
   if (!PAIR) return num_sms;
-  static const int slots = [num_sms] {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2 * (num_sms / 2));
-    cfg.blockDim = dim3(MX_THREADS);
-    cfg.dynamicSmemBytes = MxCfg<FMT, BN, PAIR>::SMEM_BYTES;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, mx4_tc_kernel<T, FMT, BN, PAIR>, &cfg) != cudaSuccess)
-      n = 0;
-    return n > 0 ? n : num_sms / 2;
-  }();
-  return slots;
+  static CountPerDevice slots;
+  const int n = slots.get(call_device(), [num_sms] {
+    return resident_clusters((const void*)mx4_tc_kernel<T, FMT, BN, PAIR>, 2, MX_THREADS,
+                             MxCfg<FMT, BN, PAIR>::SMEM_BYTES, dim3(2 * (num_sms / 2)));
+  });
+  return n > 0 ? n : num_sms / 2;
 }
 
 template <typename T, int FMT, int BN, bool PAIR>
 cudaError_t launch_mx4_cfg(const Mx4Args& a, LaunchCtx& ctx) {
   using C_ = MxCfg<FMT, BN, PAIR>;
   auto kern = mx4_tc_kernel<T, FMT, BN, PAIR>;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::SMEM_BYTES);
+  static OncePerDevice set;
+  const cudaError_t attr = set.run(call_device(), cudaSuccess, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::SMEM_BYTES);
+  });
   if (attr != cudaSuccess) return attr;
   MxTcParams mp;
   memset(&mp, 0, sizeof(mp));

@@ -496,8 +496,10 @@ cudaError_t launch_mixed_v(const MxStreamArgs& a, LaunchCtx& ctx) {
   p.timeout_ns = ctx.timeout_ns;
   p.fault_injection = a.fault_injection;
   const size_t smem = (size_t)MM_TILES * MM_W_BYTES + (size_t)p.ring * stage + MM_FIXED;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
+  static OncePerDevice set;
+  const cudaError_t attr = set.run(call_device(), cudaSuccess, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
+  });
   if (attr != cudaSuccess) return attr;
   CUtensorMap mX, mW, mS;
   const CUtensorMapDataType U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;

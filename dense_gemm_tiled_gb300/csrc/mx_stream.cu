@@ -32,12 +32,12 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
 #include "mx_format.cuh"
+#include "per_device.h"
 #include "tensor_map.h"
 
 namespace gb300 {
@@ -394,8 +394,10 @@ template <int FMT, int XT, int NT>
 cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
   using C_ = SCfg<FMT, XT, NT>;
   auto kern = mx_stream_kernel<FMT, XT, NT>;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::smem(RING));
+  static OncePerDevice set;
+  const cudaError_t attr = set.run(call_device(), cudaSuccess, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::smem(RING));
+  });
   if (attr != cudaSuccess) return attr;
   SParams p;
   p.M = a.M; p.N = a.N; p.K = a.K;
@@ -410,17 +412,15 @@ cudaError_t launch_stream(const MxStreamArgs& a, LaunchCtx& ctx) {
   for (int s = MAX_SPLIT; s > 1; --s) {
     const int per = (p.stages + s - 1) / s, n = (p.stages + per - 1) / per;
     const int ring = per < RING ? per : RING;
-    // (queried once for each cluster and ring size)
-    static std::atomic<int> slots[MAX_SPLIT + 1][RING + 1];
-    int have = slots[n][ring].load(std::memory_order_relaxed);
-    if (have == 0) {
-      have = 1 + resident_clusters((const void*)kern, n, ST_THREADS, (size_t)C_::smem(ring));
-      slots[n][ring].store(have, std::memory_order_relaxed);
-    }
+    // (queried once for each cluster and ring size, and device)
+    static CountPerDevice slots[MAX_SPLIT + 1][RING + 1];
+    const int have = slots[n][ring].get(call_device(), [kern, n, ring] {
+      return resident_clusters((const void*)kern, n, ST_THREADS, (size_t)C_::smem(ring));
+    });
     // (blocks of one stage only where blocks of two would leave SMs without one: 1 x
     // 5632 x 2048 6.3 us in 352 blocks, 5.3 in 176)
     if (per == 1 && rb * ((p.stages + 1) / 2) >= a.num_sms) continue;
-    if (rb < have) {
+    if (rb <= have) {
       splits = n;
       p.per = per;
       break;

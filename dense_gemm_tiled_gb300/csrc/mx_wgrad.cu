@@ -32,12 +32,12 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
 #include "mx_format.cuh"
+#include "per_device.h"
 #include "tensor_map.h"
 
 namespace gb300 {
@@ -379,8 +379,10 @@ template <typename T, int MT>
 cudaError_t launch_wgrad(const MxStreamArgs& a, LaunchCtx& ctx) {
   using C_ = GCfg<MT>;
   auto kern = mx_wgrad_kernel<T, MT>;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::smem(WG_RING));
+  static OncePerDevice set;
+  const cudaError_t attr = set.run(call_device(), cudaSuccess, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::smem(WG_RING));
+  });
   if (attr != cudaSuccess) return attr;
   GParams p;
   p.M = a.M; p.N = a.N; p.K = a.K;
@@ -388,19 +390,17 @@ cudaError_t launch_wgrad(const MxStreamArgs& a, LaunchCtx& ctx) {
   const int64_t cb = ((int64_t)a.N + COLS - 1) / COLS;
   if (cb > 65535) return cudaErrorNotSupported;
   // the most slices of T whose clusters are all resident at once (queried once
-  // for each cluster and ring size)
+  // for each cluster and ring size, and device)
   int splits = 1;
   p.per = p.stages;
   for (int s = WG_SPLIT; s > 1; --s) {
     const int per = (p.stages + s - 1) / s, n = (p.stages + per - 1) / per;
     const int ring = per < WG_RING ? per : WG_RING;
-    static std::atomic<int> slots[WG_SPLIT + 1][WG_RING + 1];
-    int have = slots[n][ring].load(std::memory_order_relaxed);
-    if (have == 0) {
-      have = 1 + resident_clusters((const void*)kern, n, WG_THREADS, (size_t)C_::smem(ring));
-      slots[n][ring].store(have, std::memory_order_relaxed);
-    }
-    if (cb < have) {
+    static CountPerDevice slots[WG_SPLIT + 1][WG_RING + 1];
+    const int have = slots[n][ring].get(call_device(), [kern, n, ring] {
+      return resident_clusters((const void*)kern, n, WG_THREADS, (size_t)C_::smem(ring));
+    });
+    if (cb <= have) {
       splits = n;
       p.per = per;
       break;
