@@ -264,11 +264,13 @@ def _current_stream(device_index: int) -> int:
 
 def _ld_of(shape, stride) -> int:
     """_ld from a 2-D shape and stride already fetched."""
-    if shape[1] > 1 and stride[1] != 1:
+    rows, cols = shape
+    ld, step = stride
+    if step != 1 and cols > 1:
         raise ValueError("rows must be contiguous (stride(1) == 1)")
-    if shape[0] <= 1:
-        return max(stride[0], shape[1], 1)
-    return stride[0]
+    if rows <= 1:
+        return max(ld, cols, 1)
+    return ld
 
 
 def gemm(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=None, bias=None,
@@ -353,33 +355,18 @@ class Mx:
     mx_row_bytes), and `scales`, a contiguous uint8 CUDA tensor of at least
     mx_scale_bytes elements.  fmt: 'fp4', 'fp4_e4m3' or 'int8'.
 
-    The tensors are read on each call, as gemm() reads its operands: storage that
-    was replaced (`.data`, `set_()`, a new tensor in `codes`) is used from then
-    on, and refused if it does not hold the matrix."""
-    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "_seen", "_operand",
-                 "device")
+    The tensors' addresses are read on each call, as gemm() reads its operands':
+    storage that was replaced (`.data`, `set_()`, a new tensor in `codes`) is used
+    from then on, and refused if it does not hold the matrix."""
+    __slots__ = ("codes", "scales", "fmt", "format", "rows", "cols", "device", "_seen",
+                 "_operand")
 
     def __init__(self, codes, scales, fmt, rows, cols):
         code = MX_FORMATS.get(fmt)
         if code is None:
             raise ValueError(f"unknown format {fmt!r}")
-        self.codes, self.scales, self.fmt, self.format = codes, scales, fmt, code
-        self.rows, self.cols = int(rows), int(cols)
-        self._check((codes.data_ptr(), scales.data_ptr(), codes.nbytes, codes.stride(), scales.nbytes))
-
-    def operand(self):
-        """(address of the codes, their row pitch, address of the scales), of the
-        tensors as they are now; checked again whenever one of them lies elsewhere
-        or has another size or pitch."""
-        codes, scales = self.codes, self.scales
-        seen = (codes.data_ptr(), scales.data_ptr(), codes.nbytes, codes.stride(), scales.nbytes)
-        if seen != self._seen:
-            self._check(seen)
-        return self._operand
-
-    def _check(self, seen):
-        codes, scales, rows, cols, code = self.codes, self.scales, self.rows, self.cols, self.format
-        self._seen = None
+        if type(rows) is not int or type(cols) is not int:
+            rows, cols = int(rows), int(cols)
         device = codes.get_device()
         if device < 0 or scales.get_device() != device:
             raise ValueError("codes and scales are CUDA tensors of one device")
@@ -388,23 +375,34 @@ class Mx:
         # (mx_row_bytes and mx_scale_bytes, without a call into the library)
         need = ((cols if code == 2 else (cols + 1) >> 1) + 15) & -16
         blocks = (cols + 15) >> 4 if code == 1 else (cols + 31) >> 5
-        codes_at, scales_at, _, stride, scale_bytes = seen
-        shape = codes.shape
+        shape, stride = codes.shape, codes.stride()
         if len(shape) != 2 or shape[0] != rows or shape[1] < need or \
                 (shape[1] > 1 and stride[1] != 1):
             raise ValueError(f"codes: {rows} rows of at least {need} bytes, contiguous within a row")
-        if scale_bytes < ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512 or \
-                not scales.is_contiguous():
+        held = scales.nbytes
+        if held < ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512 or not scales.is_contiguous():
             raise ValueError("scales: a contiguous tensor of mx_scale_bytes(fmt, rows, cols) bytes")
+        self.codes, self.scales, self.fmt, self.format = codes, scales, fmt, code
+        self.rows, self.cols, self.device = rows, cols, device
+        at, scales_at = codes.data_ptr(), scales.data_ptr()
+        self._seen = (at, scales_at, rows * shape[1], held)
         # (a single row's pitch is not used: any valid one)
-        self._operand = (codes_at or None, stride[0] if rows > 1 else max(need, 16),
-                         scales_at or None)
-        self._seen, self.device = seen, device
+        self._operand = (at or None, stride[0] if rows > 1 else max(need, 16), scales_at or None)
+
+    def operand(self):
+        """(address of the codes, their row pitch, address of the scales), of the
+        tensors as they are now; checked again whenever one of them lies elsewhere
+        or has another size."""
+        codes, scales = self.codes, self.scales
+        at, scales_at, held, scales_held = self._seen
+        if at != codes.data_ptr() or scales_at != scales.data_ptr() or held != codes.nbytes or \
+                scales_held != scales.nbytes:
+            self.__init__(codes, scales, self.fmt, self.rows, self.cols)
+        return self._operand
 
 
-def _stored(Q, name):
-    if not isinstance(Q, Mx):
-        raise TypeError(f"{name} is a stored operand (an Mx), not a {type(Q).__name__}")
+def _not_stored(Q, name):
+    return TypeError(f"{name} is a stored operand (an Mx), not a {type(Q).__name__}")
 
 
 def mx_empty(rows, cols, fmt, device="cuda") -> Mx:
@@ -426,11 +424,13 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     dtype = _DTYPES.get(dt)
     if dtype is None:
         raise TypeError(f"unsupported dtype {dt}")
-    _stored(Q, "Q")
+    if not isinstance(Q, Mx):
+        raise _not_stored(Q, "Q")
     want = (Q.cols, Q.rows) if transX else (Q.rows, Q.cols)
     if sx != want:
         raise ValueError(f"X is {tuple(sx)}, expected {want}")
-    dev, stored = X.get_device(), Q.operand()
+    dev = X.get_device()
+    q, pitch, scales = Q.operand()
     if dev < 0 or Q.device != dev:
         raise ValueError("mx_quantize() takes CUDA tensors of one device")
     yp, ldy = None, 0
@@ -443,7 +443,7 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
     rc = _lib.gemm_mx_quantize(Q.format, 1 if transX else 0, Q.rows, Q.cols, dtype, float(mult),
                                X.data_ptr() or None, _ld_of(sx, X.stride()), ACTS[act], yp, ldy,
-                               *stored, s)
+                               q, pitch, scales, s)
     if rc != OK:
         raise GemmError(rc)
     return Q
@@ -454,15 +454,17 @@ def mx_dequantize(Q, Y, stream=None):
     dtype = _DTYPES.get(Y.dtype)
     if dtype is None:
         raise TypeError(f"unsupported dtype {Y.dtype}")
-    _stored(Q, "Q")
+    if not isinstance(Q, Mx):
+        raise _not_stored(Q, "Q")
     sy = Y.shape
     if sy != (Q.rows, Q.cols):
         raise ValueError(f"Y is {tuple(sy)}, expected {(Q.rows, Q.cols)}")
-    dev, stored = Y.get_device(), Q.operand()
+    dev = Y.get_device()
+    q, pitch, scales = Q.operand()
     if dev < 0 or Q.device != dev:
         raise ValueError("mx_dequantize() takes CUDA tensors of one device")
     s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
-    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, *stored, dtype,
+    rc = _lib.gemm_mx_dequantize(Q.format, Q.rows, Q.cols, q, pitch, scales, dtype,
                                  Y.data_ptr() or None, _ld_of(sy, Y.stride()), s)
     if rc != OK:
         raise GemmError(rc)
@@ -477,23 +479,25 @@ def mx_act_backward(dY, Q, dX, act="gelu", dbias=None, stream=None):
     dtype = _DTYPES.get(dt)
     if dtype is None:
         raise TypeError(f"unsupported dtype {dt}")
-    _stored(Q, "Q")
+    if not isinstance(Q, Mx):
+        raise _not_stored(Q, "Q")
     if Q.fmt != "int8":
         raise TypeError("the checkpoint is an 'int8' Mx")
     if dX.dtype != dt or sy != (Q.rows, Q.cols) or dX.shape != sy:
         raise ValueError(f"dY and dX: {(Q.rows, Q.cols)} CUDA tensors of one dtype")
-    dev, stored = dY.get_device(), Q.operand()
+    dev = dY.get_device()
+    q, pitch, scales = Q.operand()
     if dev < 0 or Q.device != dev or dX.get_device() != dev:
         raise ValueError("mx_act_backward() takes CUDA tensors of one device")
     bp = None
     if dbias is not None:
-        if dbias.get_device() != dev or dbias.numel() != Q.cols or _DTYPES.get(dbias.dtype) != F32 or \
-                not dbias.is_contiguous():
+        if dbias.get_device() != dev or dbias.numel() != Q.cols or \
+                _DTYPES.get(dbias.dtype) != F32 or not dbias.is_contiguous():
             raise ValueError("dbias: a contiguous float32 CUDA tensor of cols elements")
         bp = dbias.data_ptr() or None
     s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
     rc = _lib.gemm_mx_act_backward(Q.rows, Q.cols, dtype, ACTS[act], dY.data_ptr() or None,
-                                   _ld_of(sy, dY.stride()), *stored,
+                                   _ld_of(sy, dY.stride()), q, pitch, scales,
                                    dX.data_ptr() or None, _ld_of(sy, dX.stride()), bp, s)
     if rc != OK:
         raise GemmError(rc)
@@ -523,12 +527,14 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
     M, N = sc
     bp = None
     if bias is not None:
-        if bias.get_device() != dev or bias.dtype != dt or bias.numel() != N or not bias.is_contiguous():
+        if bias.get_device() != dev or bias.dtype != dt or bias.numel() != N or \
+                not bias.is_contiguous():
             raise ValueError("bias: a contiguous CUDA tensor of N elements of C's dtype")
         bp = bias.data_ptr() or None
     s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
-    _stored(B, "B")
-    stored = B.operand()
+    if not isinstance(B, Mx):
+        raise _not_stored(B, "B")
+    codes, pitch, scales = B.operand()
     if isinstance(A, Mx):
         if transA or transB:
             raise ValueError("two stored operands are both stored along K")
@@ -539,11 +545,12 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
             raise ValueError(f"inner dimensions differ: {K} vs {B.cols}")
         if A.rows != M or B.rows != N:
             raise ValueError(f"C is {(M, N)}, expected {(A.rows, B.rows)}")
-        a = A.operand()
+        a, lda, a_scales = A.operand()
         if A.device != dev or B.device != dev:
             raise ValueError("A, B and C are on one device")
-        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, float(alpha), float(beta), *a, *stored,
-                           C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
+        rc = _lib.gemm_mx4(A.format, M, N, K, dtype, float(alpha), float(beta), a, lda, a_scales,
+                           codes, pitch, scales, C.data_ptr() or None, _ld_of(sc, C.stride()), bp,
+                           ACTS[act], s)
     else:
         if A.dtype != dt:
             raise TypeError("A and C must share a dtype")
@@ -558,9 +565,10 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
             raise ValueError(f"inner dimensions differ: {K} vs {Kb}")
         if Ma != M or Nb != N:
             raise ValueError(f"C is {(M, N)}, expected {(Ma, Nb)}")
-        rc = _lib.gemm_mx(B.format, 1 if transA else 0, 1 if transB else 0, M, N, K, dtype, float(alpha),
-                          float(beta), A.data_ptr() or None, _ld_of(sa, A.stride()), *stored,
-                          C.data_ptr() or None, _ld_of(sc, C.stride()), bp, ACTS[act], s)
+        rc = _lib.gemm_mx(B.format, 1 if transA else 0, 1 if transB else 0, M, N, K, dtype,
+                          float(alpha), float(beta), A.data_ptr() or None,
+                          _ld_of(sa, A.stride()), codes, pitch, scales, C.data_ptr() or None,
+                          _ld_of(sc, C.stride()), bp, ACTS[act], s)
     if rc != OK:
         raise GemmError(rc)
     return C
