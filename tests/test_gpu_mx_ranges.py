@@ -1,6 +1,7 @@
-"""Stored operands at the ends of their ranges: signs of zeros, padding after a negative factor,
-scales far from 1 whose products are ordinary numbers, 16-bit values that overflow
-before their scale is applied, and scales that are no fp16 numbers."""
+"""Stored operands at the ends of their ranges: signs of zeros, padding after a
+negative factor, scales far from 1 whose products are ordinary numbers, 16-bit
+values that would overflow before their scale is applied, and scales that are no
+fp16 numbers."""
 import numpy as np
 import pytest
 import torch
@@ -90,6 +91,20 @@ def test_opposite_scales_of_two_stored_operands(g, shift):
         check(C, a, b.T, "f32")
 
 
+@pytest.mark.parametrize("shift", [124, -124, 125, -125])
+def test_opposite_scales_on_the_tensor_core(g, shift):
+    """The same past the streaming kernel's rows: the block-scaled MMA takes both
+    scales at once."""
+    for M, N, K in [(40, 50, 300), (200, 300, 600)]:
+        r = np.random.default_rng(M)
+        A, a = stored(g, (r.standard_normal((M, K)) * 2.0 ** shift).astype(np.float32), "fp4")
+        B, b = stored(g, (r.standard_normal((N, K)) * 2.0 ** -shift).astype(np.float32), "fp4")
+        C = torch.empty((M, N), device="cuda")
+        g.gemm_mx(A, B, C)
+        assert g.last_path() == "mx_tc"
+        check(C, a, b.T, "f32")
+
+
 def test_opposite_scales_keep_nan(g):
     r = np.random.default_rng(1)
     x = (r.standard_normal((5, 96)) * 2.0 ** 124).astype(np.float32)
@@ -116,3 +131,41 @@ def test_large_bf16_rows_times_small_weights(g, fmt):
         C = torch.empty((M, 70), dtype=torch.bfloat16, device="cuda")
         g.gemm_mx(x, B, C, transB=True)
         check(C, f64(x), b.T, "bf16")
+
+
+def test_fp16_rows_times_scales_past_fp16(g):
+    """A power-of-two scale that is no fp16 number: up to 32 rows of A, with B
+    stored [N, K], it stays in fp32; in every other product of 16-bit rows the
+    values are rounded to fp16 first."""
+    r = np.random.default_rng(3)
+    w = r.standard_normal((96, 256)).astype(np.float32)
+    w[0] *= 2.0 ** -20   # values of fp16's subnormal range
+    w[1] *= 2.0 ** -40   # below it
+    w[2] *= 2.0 ** 13    # scales up to 2^13, values within range
+    w[3] *= 2.0 ** 30    # beyond it
+    B, b = stored(g, w, "fp4")
+    with np.errstate(over="ignore"):
+        half = b.astype(np.float16).astype(np.float64)
+    for M in (1, 32, 33, 100):
+        gen = torch.Generator().manual_seed(M)
+        A = torch.randn((M, 256), generator=gen).half().cuda() / 16
+        C = torch.empty((M, 96), dtype=torch.float16, device="cuda")
+        g.gemm_mx(A, B, C, transB=True)
+        assert (g.last_path() == "mx_stream") == (M <= 32)
+        v = b if M <= 32 else half
+        keep = [j for j in range(96) if j != 3]
+        check(C[:, keep].contiguous(), f64(A), v[keep].T, "f16")
+        if M <= 32:  # finite products of about 2^30, past fp16 only in C
+            want = (f64(A) @ b[3]).astype(np.float32)
+            assert np.all(np.abs(want) > 65520) and np.array_equal(f64(C[:, 3]), np.sign(want) * np.inf)
+        else:
+            assert not torch.isfinite(C[:, 3]).any()
+    # stored [K, N]: always rounded
+    At = torch.randn((4, 96), generator=torch.Generator().manual_seed(5)).half().cuda() / 16
+    At[:, 3] = 0.25
+    C = torch.empty((4, 256), dtype=torch.float16, device="cuda")
+    g.gemm_mx(At, B, C)
+    big = np.abs(b[3]) > 65520
+    keep = np.flatnonzero(~big)
+    check(C[:, keep].contiguous(), f64(At), half[:, keep], "f16")
+    assert not torch.isfinite(C[:, np.flatnonzero(big)]).any()
