@@ -419,7 +419,10 @@ def mx_quantize(X, Q, transX=False, mult=1.0, act="none", Y=None, stream=None):
     """Stores mult * op(X) in Q (an Mx) and, with Y, writes Y = act(op(X)) in the
     same pass: the forward pass of an activation whose input is checkpointed.
     X is [rows, cols] (or [cols, rows] with transX) float32, float16 or bfloat16;
-    Y has X's dtype and shape and may be X.  Returns Q."""
+    Y has X's dtype and shape and may be X.  Returns Q.
+
+    mult is not kept with Q, whose values are those of mult * X: give 1 / mult to a
+    product as alpha, or multiply what mx_dequantize() returns by it."""
     dt, sx = X.dtype, X.shape
     dtype = _DTYPES.get(dt)
     if dtype is None:
@@ -513,7 +516,12 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
     stored [K, N], or [N, K] with transB; A and C share a dtype.
     A and B Mx of the same 4-bit format, both stored along K (A [M, K], B
     [N, K]): C = act(alpha * A @ B.T + beta * C + bias); transA and transB stay
-    False.  Returns C."""
+    False.  Returns C.
+
+    With a float16 tensor A the values of B are rounded to float16 first: exact but
+    beyond its range (below 2^-14, above 65504).  Up to 32 rows of A with transB a
+    power-of-two scale of 4-bit codes stays in fp32 there instead, so such an
+    operand gives other results from 33 rows on."""
     dt = C.dtype
     dtype = _DTYPES.get(dt)
     if dtype is None:

@@ -21,9 +21,21 @@ constexpr int64_t LIM = (int64_t)1 << 31;
 // stages, tiles and a grid's strides (up to 2^17 elements past an end) in 32 bits.
 constexpr int64_t PRODUCT_LIM = LIM - ((int64_t)1 << 18);
 
-// Rows up to which a product streams its 4-bit right operand.
-constexpr int64_t WGRAD_ROWS = 32;  // (columns of A, in the tn product)
-constexpr int64_t STREAM_ROWS = 32;  // (what the streaming kernel holds)
+// Rows (columns of A, in the tn product) up to which the streaming kernels take a
+// product: as many as they hold.  In a graph, us, at 32 of them, streamed against
+// converted (expanded: 61, 18, 20; int8 66, 19, 20):
+//                       8192 x 8192    5632 x 2048    2048 x 5632  (N x K)
+//   nt fp4 fp16         23.0 / 28.0     9.2 /  9.6    11.0 / 11.1
+//   nt fp4 bf16         24.3 / 32.9     9.6 / 10.5    11.4 / 12.2
+//   nt fp4_e4m3 fp16    19.3 / 28.6     8.2 /  9.3     9.8 / 11.0
+//   tn int8 fp16        26.0 / 35.0     9.5 / 10.9    11.7 / 12.7
+//   tn int8 bf16        31.4 / 35.0    10.3 / 10.7    13.6 / 12.6
+// Two stored operands take the same bound, where the 4-bit tensor-core kernel
+// would be level or faster from one row on with fp4 (8192 x 8192: 8 rows 20.4 /
+// 18.4, 32 rows 46.0 / 12.3) and from 16 on with fp4_e4m3 (8 rows 15.9 / 19.2, 16
+// rows 20.0 / 18.8, 32 rows 29.0 / 13.3).
+constexpr int64_t WGRAD_ROWS = 32;
+constexpr int64_t STREAM_ROWS = 32;
 
 inline bool known_format(int f) { return f >= GEMM_MX_FP4 && f <= GEMM_MX_INT8; }
 inline bool known_type(int d) {

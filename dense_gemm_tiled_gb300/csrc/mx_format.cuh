@@ -75,8 +75,8 @@ __device__ __forceinline__ uint32_t mx_scale_byte(float amax) {
 }
 
 // ---------------------------------------------------------------- pairs of fp32
-// Two IEEE fp32 operations an instruction; the elementwise kernels are near the
-// issue limit, so they work on pairs throughout.
+// Two IEEE fp32 operations an instruction; the elementwise kernels issue more than
+// half of what an SM can, so they work on pairs throughout.
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pair(float lo, float hi) {
   f32x2 r;

@@ -22,10 +22,16 @@
 // order, so a result does not depend on timing.
 //   tcgen05 would use 8 to 32 of its 128 rows here and take 16-bit operands from
 // shared memory, which the codes would have to be written to first; the warp MMAs
-// take them from registers and are nowhere near a limit.  Measured: 8 x 8192 x
-// 8192 14.6 us (fp4, fp16) and 16.4 (fp4_e4m3, bf16), 2.4 and 2.3 TB/s, bound by
-// the instructions that make operands of codes; 1 x 5632 x 2048 5.3 us, launch and
-// one load's latency.
+// take them from registers and are nowhere near a limit.
+//   Measured in a graph, us, and of that: start and join without a K loop; with
+// the loop's loads but no products; all but the finishing of C
+//   8 x 8192 x 8192 fp4_e4m3 bf16   16.8     3.6   10.3   15.2   (5.6 by its bytes)
+//   8 x 8192 x 8192 fp4 fp16        15.2     3.6   10.0   13.5
+//   32 x 8192 x 8192 fp4 fp16       22.9     3.7   11.4   20.6
+//   1 x 5632 x 2048 fp4 fp16         5.6     2.4    3.8    4.7
+// so no one part bounds it: with four stages a block, making operands of codes
+// takes about as long again as waiting for them, and neither hides the other (2.0
+// instructions a cycle of 4, DRAM at 24 %; barriers are the largest stall).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

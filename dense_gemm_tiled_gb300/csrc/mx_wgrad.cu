@@ -5,9 +5,12 @@
 // A [T, M] fp16 or bf16 with M up to 32 columns, q the checkpoint of the
 // layer's input, [T, N] (the tn product of "Metal GEMM Kernels for LoRA Training
 // on Apple Silicon", section 5, with its right operand stored in 8 bits).
-// Bound by the bytes of the checkpoint, each read once: 32 x 8192 x 8192 fp16 takes
-// 25.8 us, 2.7 TB/s, where 70 MB at HBM's rate would be 10.4; what is left is the
-// instructions that turn codes into operands.
+// The bytes of the checkpoint, each read once, are its floor: 32 x 8192 x 8192 fp16
+// takes 25.8 us, 2.7 TB/s, where 70 MB at HBM's rate would be 10.4.  Of that, start
+// and join without a K loop 4.2; with its loads but no products 18.3; all but the
+// finishing of C 23.9.  So the loads, at two blocks an SM, come first (DRAM 31 % busy),
+// then turning codes into operands, which they hide in part only (1.7 instructions
+// a cycle of 4).
 //
 // A block takes 128 columns of the checkpoint and a slice of T; a cluster's
 // blocks share the columns and split T.  A producer warp brings 64 rows of q (128-
@@ -20,7 +23,7 @@
 //   Every row has a scale of its own, so a pair of rows needs both scales side by
 // side: one more warp makes these once a stage (32 row pairs x 4 blocks) for all
 // the others, which otherwise spent a third of their instructions on them (28.3
-// -> 25.8 us at the size below; two blocks of ten warps an SM: three, at 64
+// -> 25.8 us at the size above; two blocks of ten warps an SM: three, at 64
 // registers a thread, 31.3; the loading warp making them as well, 36).
 //   A code becomes fp16 by putting its byte into 1024's fraction (1024 + q + 128,
 // exact); one FMA by the scale takes 1152 times the scale away, exactly while

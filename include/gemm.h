@@ -286,7 +286,8 @@ int64_t gemm_mx_scale_bytes(int format, int64_t rows, int64_t cols);
  *   [rows, cols]: the forward pass of an activation whose input is kept in 8
  *   bits.  Not with transX (GEMM_ERR_UNSUPPORTED); act without Y is an error.
  *   Y may be X itself with the same pitch.  GEMM_ACT_GELU is x Phi(x), in fp32
- *   within a few ulp for every x.  (gemm_ex()'s fused x/2 (1 + erf(x / sqrt 2)) is
+ *   within a few ulp for every x, in 16 bits within 1e-7 |x| before its rounding
+ *   and 1.5 % of the value down to x = -8.5.  (gemm_ex()'s fused x/2 (1 + erf(x / sqrt 2)) is
  *   evaluated as that sum, whose error is about 2^-22 |x|: in fp32 the two differ
  *   by as much, and for x below -4 mostly by gemm_ex()'s.)  GEMM_ACT_RELU is x
  *   where x > 0, else 0, as gemm_ex()'s: a NaN becomes 0.
@@ -334,8 +335,9 @@ int gemm_mx4(int format, int64_t M, int64_t N, int64_t K, int dtype, float alpha
  * A and C of dtype as in gemm(); B stored in `format` as [K, N] (blocks along
  * N) or, with transB, as [N, K] (blocks along K); ldb in BYTES.  The values of
  * B are rounded to dtype before the product, which is exact but where fp16's
- * range ends (with few rows of A a power-of-two scale beyond fp16's range is kept
- * in fp32 instead).  Takes scratch in stream order where B is expanded for the
+ * range ends: a value below 2^-14 may lose bits or vanish, one above 65504 becomes
+ * infinite.  (Up to 32 rows of A with transB, a power-of-two 4-bit scale beyond
+ * fp16's range is kept in fp32 instead.)  Takes scratch in stream order where B is expanded for the
  * other types' kernels, and where rows of A are not 16-byte aligned.
  */
 int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype,
