@@ -7,7 +7,8 @@ missing -- there is no fallback.  The `inputs` module (seeded synthetic data)
 does not load the library, so it can be imported on a machine without a GPU.
 """
 _BINDING = ("gemm", "gemm_raw", "gemm_host", "check_device_status", "status_string", "Mx",
-            "mx_empty", "mx_quantize", "mx_dequantize", "mx_act_backward", "gemm_mx")
+            "mx_empty", "mx_quantize", "mx_dequantize", "mx_act_backward", "gemm_mx", "gemm_fused",
+            "gemm_fused_backward", "gemm_grouped", "gemm_grouped_backward", "gemm_grouped_wgrad")
 __all__ = [*_BINDING, "binding", "inputs"]
 
 

@@ -30,6 +30,21 @@ _lib.gemm_host.restype = _int
 _lib.gemm_strided_batched.argtypes = [_int, _int, _i64, _i64, _i64, _int, _flt, _flt, _vp, _i64,
                                       _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp]
 _lib.gemm_strided_batched.restype = _int
+_lib.gemm_fused.argtypes = [_int, _int, _i64, _i64, _i64, _int, _flt, _vp, _i64, _vp, _i64, _vp,
+                            _int, _flt, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+_lib.gemm_fused.restype = _int
+_lib.gemm_fused_backward.argtypes = [_int, _int, _i64, _i64, _i64, _int, _flt, _vp, _i64, _vp,
+                                     _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp]
+_lib.gemm_fused_backward.restype = _int
+_lib.gemm_grouped.argtypes = [_int, _i64, _i64, _i64, _i64, _vp, _int, _flt, _vp, _i64, _vp, _i64,
+                              _i64, _vp, _int, _flt, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+_lib.gemm_grouped.restype = _int
+_lib.gemm_grouped_backward.argtypes = [_int, _i64, _i64, _i64, _i64, _vp, _int, _flt, _vp, _i64,
+                                       _vp, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp]
+_lib.gemm_grouped_backward.restype = _int
+_lib.gemm_grouped_wgrad.argtypes = [_i64, _i64, _i64, _i64, _vp, _int, _flt, _flt, _vp, _i64, _vp,
+                                    _i64, _vp, _i64, _i64, _vp]
+_lib.gemm_grouped_wgrad.restype = _int
 _lib.gemm_mx_row_bytes.argtypes = [_int, _i64]
 _lib.gemm_mx_row_bytes.restype = _i64
 _lib.gemm_mx_scale_bytes.argtypes = [_int, _i64, _i64]
@@ -74,7 +89,7 @@ F32_3XTF32 = 4
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_TIMEOUT = range(7)
 PATHS = {0: "none", 1: "scale", 2: "ffma", 3: "ffma_splitk", 4: "tc", 5: "tc_splitk",
          6: "ffma_batched", 7: "tc_batched", 8: "per_entry", 9: "mx", 10: "mx_tc",
-         11: "mx_stream", 12: "mx_convert"}
+         11: "mx_stream", 12: "mx_convert", 13: "fused_tc", 14: "fused_ffma"}
 
 
 class GemmError(RuntimeError):
@@ -577,6 +592,207 @@ def gemm_mx(A, B, C, transA=False, transB=False, alpha=1.0, beta=0.0, stream=Non
                           float(alpha), float(beta), A.data_ptr() or None,
                           _ld_of(sa, A.stride()), codes, pitch, scales, C.data_ptr() or None,
                           _ld_of(sc, C.stride()), bp, ACTS[act], s)
+    if rc != OK:
+        raise GemmError(rc)
+    return C
+
+
+# ---------------------------------------------------------------------------
+# Products with a full epilogue, and products grouped by expert
+# ---------------------------------------------------------------------------
+def _like(t, name, dt, dev, shape):
+    """(address, row pitch) of a further matrix of a call, or (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype != dt or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name}: a {tuple(shape)} CUDA tensor of the operands' dtype and device")
+    return t.data_ptr() or None, _ld_of(shape, t.stride())
+
+
+def _flat(t, name, dt, dev, shape):
+    """Address of a contiguous tensor of a call, or None for None."""
+    if t is None:
+        return None
+    if t.dtype != dt or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {tuple(shape)} CUDA tensor of dtype {dt} on the "
+                         "operands' device")
+    return t.data_ptr() or None
+
+
+def _common(A, B, Y, name):
+    """dtype code, torch dtype and device of a call's matrices."""
+    dt = Y.dtype
+    dtype = _DTYPES.get(dt)
+    if A.dtype != dt or B.dtype != dt:
+        raise TypeError("the operands and the result share a dtype")
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    dev = Y.get_device()
+    if dev < 0 or A.get_device() != dev or B.get_device() != dev:
+        raise ValueError(f"{name}() takes CUDA tensors of one device")
+    return dtype, dt, dev
+
+
+def _product(A, B, Y, transA, transB):
+    sa, sb, sy = A.shape, B.shape, Y.shape
+    if len(sa) != 2 or len(sb) != 2 or len(sy) != 2:
+        raise ValueError("matrices are 2-D")
+    M, K = (sa[1], sa[0]) if transA else sa
+    Kb, N = (sb[1], sb[0]) if transB else sb
+    if K != Kb:
+        raise ValueError(f"inner dimensions differ: {K} vs {Kb}")
+    if sy[0] != M or sy[1] != N:
+        raise ValueError(f"the result is {tuple(sy)}, expected {(M, N)}")
+    return M, N, K, _ld_of(sa, A.stride()), _ld_of(sb, B.stride()), _ld_of(sy, Y.stride())
+
+
+def _act_code(act):
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"unknown activation {act!r}")
+    return code
+
+
+def gemm_fused(A, B, Y, transA=False, transB=False, alpha=1.0, bias=None, act="none",
+               residual=None, beta=1.0, preact=None, stream=None):
+    """U = alpha * op(A) @ op(B) + bias and Y = act(U) + beta * residual, in one pass.
+
+    A, B as in gemm(); Y [M, N].  bias: N contiguous elements; residual: [M, N], which
+    may be Y; preact: [M, N], receives U (rounded to its dtype) for the backward pass;
+    each may be None.  All share a dtype (float32, float16 or bfloat16) and a device.
+    Returns Y."""
+    dtype, dt, dev = _common(A, B, Y, "gemm_fused")
+    M, N, K, lda, ldb, ldy = _product(A, B, Y, transA, transB)
+    code = _act_code(act)
+    bp = _flat(bias, "bias", dt, dev, (N,))
+    rp, ldr = _like(residual, "residual", dt, dev, Y.shape)
+    up, ldu = _like(preact, "preact", dt, dev, Y.shape)
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
+    rc = _lib.gemm_fused(1 if transA else 0, 1 if transB else 0, M, N, K, dtype, float(alpha),
+                         A.data_ptr() or None, lda, B.data_ptr() or None, ldb, bp, code,
+                         float(beta), rp, ldr, up, ldu, Y.data_ptr() or None, ldy, s)
+    if rc != OK:
+        raise GemmError(rc)
+    return Y
+
+
+def gemm_fused_backward(A, B, dX, preact, transA=False, transB=False, alpha=1.0, act="gelu",
+                        dbias=None, stream=None):
+    """dX = (alpha * op(A) @ op(B)) * act'(preact), and dbias[j] = sum_i dX[i, j] (a
+    contiguous float32 tensor of N elements, or None): with A the gradient of a layer's
+    output and B its weight, the gradient of what went into the activation before it.
+    preact [M, N] as gemm_fused() stored it (None with act 'none'); dX may be preact.
+    Returns dX."""
+    import torch
+    dtype, dt, dev = _common(A, B, dX, "gemm_fused_backward")
+    M, N, K, lda, ldb, ldx = _product(A, B, dX, transA, transB)
+    code = _act_code(act)
+    up, ldu = _like(preact, "preact", dt, dev, dX.shape)
+    if code and preact is None:
+        raise ValueError("preact: the activation's input")
+    dp = _flat(dbias, "dbias", torch.float32, dev, (N,))
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
+    rc = _lib.gemm_fused_backward(1 if transA else 0, 1 if transB else 0, M, N, K, dtype,
+                                  float(alpha), A.data_ptr() or None, lda, B.data_ptr() or None,
+                                  ldb, code, up, ldu, dX.data_ptr() or None, ldx, dp, s)
+    if rc != OK:
+        raise GemmError(rc)
+    return dX
+
+
+def _groups(offsets, dev):
+    """Number of groups and address of the offsets."""
+    import torch
+    if offsets.dtype != torch.int32:
+        raise TypeError("offsets are int32")
+    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.get_device() != dev or \
+            not offsets.is_contiguous():
+        raise ValueError("offsets: groups + 1 contiguous int32 values on the operands' device")
+    return offsets.numel() - 1, offsets.data_ptr()
+
+
+def _grouped_product(A, B, Y, offsets, dev, transB):
+    sa, sb, sy = A.shape, B.shape, Y.shape
+    if len(sa) != 2 or len(sb) != 3 or len(sy) != 2:
+        raise ValueError("A and the result are 2-D, B is [groups, rows, cols]")
+    groups, op = _groups(offsets, dev)
+    if sb[0] != groups:
+        raise ValueError(f"B holds {sb[0]} matrices, offsets {groups} groups")
+    rows, K = sa
+    Kb, N = (sb[2], sb[1]) if transB else (sb[1], sb[2])
+    if K != Kb:
+        raise ValueError(f"inner dimensions differ: {K} vs {Kb}")
+    if sy[0] != rows or sy[1] != N:
+        raise ValueError(f"the result is {tuple(sy)}, expected {(rows, N)}")
+    return (rows, N, K, groups, op, _ld_of(sa, A.stride()), _ld3(B),
+            int(B.stride(0)) if groups > 1 else 0, _ld_of(sy, Y.stride()))
+
+
+def gemm_grouped(A, B, Y, offsets, transB=False, alpha=1.0, bias=None, act="none",
+                 residual=None, beta=1.0, preact=None, stream=None):
+    """gemm_fused() by groups of rows, as a router sends tokens to experts: on rows
+    offsets[g] .. offsets[g + 1] of A, residual, preact and Y,
+        U = alpha * A @ op(B[g]) + bias[g],  Y = act(U) + beta * residual.
+
+    A [rows, K]; B [groups, K, N], or [groups, N, K] with transB; Y [rows, N]; offsets:
+    groups + 1 ascending int32 on the GPU (nothing waits for them); bias [groups, N].
+    Rows outside every group are left as they are.  Returns Y."""
+    dtype, dt, dev = _common(A, B, Y, "gemm_grouped")
+    rows, N, K, groups, op, lda, ldb, strideb, ldy = _grouped_product(A, B, Y, offsets, dev, transB)
+    code = _act_code(act)
+    bp = _flat(bias, "bias", dt, dev, (groups, N))
+    rp, ldr = _like(residual, "residual", dt, dev, Y.shape)
+    up, ldu = _like(preact, "preact", dt, dev, Y.shape)
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
+    rc = _lib.gemm_grouped(1 if transB else 0, rows, N, K, groups, op, dtype, float(alpha),
+                           A.data_ptr() or None, lda, B.data_ptr() or None, ldb, strideb, bp, code,
+                           float(beta), rp, ldr, up, ldu, Y.data_ptr() or None, ldy, s)
+    if rc != OK:
+        raise GemmError(rc)
+    return Y
+
+
+def gemm_grouped_backward(A, B, dX, offsets, preact, transB=False, alpha=1.0, act="gelu",
+                          dbias=None, stream=None):
+    """gemm_fused_backward() by groups of rows (see gemm_grouped()): dX = (alpha * A @
+    op(B[g])) * act'(preact) on each group's rows, dbias [groups, N] float32 its column
+    sums by group (zero for an empty one), or None.  Returns dX."""
+    import torch
+    dtype, dt, dev = _common(A, B, dX, "gemm_grouped_backward")
+    rows, N, K, groups, op, lda, ldb, strideb, ldx = _grouped_product(A, B, dX, offsets, dev, transB)
+    code = _act_code(act)
+    up, ldu = _like(preact, "preact", dt, dev, dX.shape)
+    if code and preact is None:
+        raise ValueError("preact: the activation's input")
+    dp = _flat(dbias, "dbias", torch.float32, dev, (groups, N))
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
+    rc = _lib.gemm_grouped_backward(1 if transB else 0, rows, N, K, groups, op, dtype, float(alpha),
+                                    A.data_ptr() or None, lda, B.data_ptr() or None, ldb, strideb,
+                                    code, up, ldu, dX.data_ptr() or None, ldx, dp, s)
+    if rc != OK:
+        raise GemmError(rc)
+    return dX
+
+
+def gemm_grouped_wgrad(A, B, C, offsets, alpha=1.0, beta=0.0, stream=None):
+    """C[g] = alpha * A[rows of g].T @ B[rows of g] + beta * C[g]: the gradient of each
+    group's matrix.  A [rows, M], B [rows, N], C [groups, M, N]; offsets as in
+    gemm_grouped().  An empty group's C[g] becomes beta * C[g].  Returns C."""
+    dtype, dt, dev = _common(A, B, C, "gemm_grouped_wgrad")
+    sa, sb, sc = A.shape, B.shape, C.shape
+    if len(sa) != 2 or len(sb) != 2 or len(sc) != 3:
+        raise ValueError("A and B are 2-D, C is [groups, M, N]")
+    groups, op = _groups(offsets, dev)
+    if sa[0] != sb[0]:
+        raise ValueError(f"A has {sa[0]} rows, B {sb[0]}")
+    if sc[0] != groups or sc[1] != sa[1] or sc[2] != sb[1]:
+        raise ValueError(f"C is {tuple(sc)}, expected {(groups, sa[1], sb[1])}")
+    s = (stream.cuda_stream if stream is not None else _current_stream(dev)) or None
+    rc = _lib.gemm_grouped_wgrad(sa[0], sa[1], sb[1], groups, op, dtype, float(alpha), float(beta),
+                                 A.data_ptr() or None, _ld_of(sa, A.stride()),
+                                 B.data_ptr() or None, _ld_of(sb, B.stride()),
+                                 C.data_ptr() or None, _ld3(C),
+                                 int(C.stride(0)) if groups > 1 else 0, s)
     if rc != OK:
         raise GemmError(rc)
     return C

@@ -20,6 +20,7 @@ namespace gb300 {
 // Bits of the per-device status word.
 enum : uint32_t {
   STATUS_WAIT_TIMEOUT = 1u,  // an mbarrier wait ran out of time
+  STATUS_BAD_OFFSETS = 2u,   // a grouped product's offsets do not ascend within its rows
 };
 
 struct WaitCtl {

@@ -1141,7 +1141,8 @@ int gemm_check_device_status(gemm_stream_t stream) {
     const unsigned int zero = 0;
     if (cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
       return GEMM_ERR_CUDA;
-    return GEMM_ERR_TIMEOUT;
+    // (common.cuh: 1 a wait that ran out, 2 offsets of a grouped product)
+    return (word & 1u) != 0 ? GEMM_ERR_TIMEOUT : GEMM_ERR_INVALID_ARG;
   }
   return GEMM_OK;
 }

@@ -329,6 +329,53 @@ size_t mx_act_backward_scratch(int rows, int cols, int num_sms);  // (0: none ne
 cudaError_t launch_mx_act_backward(const MxActBwdArgs& a, LaunchCtx& ctx);
 cudaError_t launch_mx4(const Mx4Args& a, LaunchCtx& ctx);
 
+// ---------------------------------------------------------------- fused and grouped products
+// (entry points: include/gemm.h, gemm_fused and gemm_grouped)
+enum { FUSED_DENSE = 0, FUSED_ROWS = 1, FUSED_INNER = 2 };  // one matrix, groups of rows, groups of K
+enum { FUSED_NONE = 0, FUSED_ADD = 1, FUSED_SLOPE = 2 };    // what the epilogue's input is: none, R, U
+enum { FUSED_TILE_PAIR, FUSED_TILE_128, FUSED_TILE_64, FUSED_TILES };
+struct FusedArgs {
+  int kind, dtype;     // dtype: 0 fp32, 1 fp16, 2 bf16
+  int transA, transB;
+  int M, N, K;         // M: rows of all groups (FUSED_INNER: of each C); K: of all groups there
+  int groups;          // 1 for FUSED_DENSE
+  const int* offsets;  // groups + 1 in device memory
+  const void* A;
+  int64_t lda;
+  const void* B;
+  int64_t ldb, stride_b;
+  float alpha, beta;   // beta: of R, or of C (FUSED_INNER)
+  const void* bias;    // [groups][N], or null
+  int act;
+  int mode;
+  const void* in;      // R or U (mode); FUSED_INNER: C
+  int64_t ld_in;
+  void* U;             // pre-activation to store, or null
+  int64_t ldu;
+  void* Y;
+  int64_t ldy, stride_y;
+  float* part;         // fused_part_floats() floats for the column sums, or null
+  int num_sms;
+  int fault_injection;
+  int tile;            // FUSED_TILE_* (16-bit types)
+};
+// Column sums come in slots of 32 rows: group g's begin at o[g] / 32 + g.
+inline int64_t fused_part_floats(int64_t rows, int64_t groups, int64_t N) {
+  return (rows / 32 + groups + 1) * N;
+}
+int fused_pick(const FusedArgs& a);  // the tile
+// 16-bit operands with 16-byte aligned rows (A, B) on the tensor cores;
+// cudaErrorNotSupported (nothing launched) where a tensor map does not take them
+cudaError_t launch_fused(const FusedArgs& a, LaunchCtx& ctx);
+cudaError_t launch_fused_bf16(const FusedArgs& a, LaunchCtx& ctx);
+// dbias[g][j] = the sum of group g's slots of `part`
+cudaError_t launch_fused_dbias(const FusedArgs& a, float* dbias, LaunchCtx& ctx);
+// fp32: the raw products of a grouped call into P (FUSED_ROWS, pitch ldp), or C
+// itself (FUSED_INNER)
+cudaError_t launch_sgemm_grouped(const FusedArgs& a, float* P, int64_t ldp, LaunchCtx& ctx);
+// fp32: the epilogue of the raw products P (rows of the groups only); P may be Y or U
+cudaError_t launch_fused_finish(const FusedArgs& a, const float* P, int64_t ldp, LaunchCtx& ctx);
+
 // What the entry points of every translation unit share (gemm_api.cu).
 struct ApiState {
   int dev, sms;

@@ -26,6 +26,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "gelu.cuh"
 #include "internal.h"
 #include "mx_format.cuh"
 
@@ -113,38 +114,6 @@ __device__ __forceinline__ uint32_t max_abs_bits(const float (&x)[16]) {
   return m;
 }
 
-// 16-bit types.  For a pair x, given as n = -|x|: c = erfc(|x| / sqrt 2) / 2 =
-// Phi(-|x|) and e = exp(-x^2 / 2), which the gelu and its derivative share:
-//   erfc(z) = t (a1 + t (a2 + ... )) exp(-z^2),  t = 1 / (1 + p z),
-// within 1.5e-7 (M. Abramowitz and I. Stegun, "Handbook of Mathematical
-// Functions", 7.1.26), which the rounding to 16 bits covers but in the far tail:
-// 0.3 % of gelu(-5.7) = -3e-8, 1.2 % of gelu(-8.5) = -8e-17.  A value costs an
-// exponential, a reciprocal and five paired operations; with erff and expf, the
-// forward and backward pass at 16384 x 5632 bf16 took 465 us against 232 with
-// scalar operations of this form.
-__device__ __forceinline__ f32x2 normal_tail2(f32x2 n, f32x2& e) {
-  float a, b;
-  unpair(fma2(n, pair(-0.3275911f * 0.70710678f), pair(1.f)), a, b);
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
-  const f32x2 t = pair(a, b);
-  unpair(mul2(mul2(n, n), pair(-0.72134752f)), a, b);
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
-  e = pair(a, b);
-  f32x2 c = fma2(t, pair(0.5f * 1.061405429f), pair(0.5f * -1.453152027f));
-  c = fma2(t, c, pair(0.5f * 1.421413741f));
-  c = fma2(t, c, pair(0.5f * -0.284496736f));
-  c = fma2(t, c, pair(0.5f * 0.254829592f));
-  return mul2(mul2(t, c), e);
-}
-// -|x|, not below -64 (where c and e are 0 already), so that an infinity meets no
-// 0; a NaN stays one
-__device__ __forceinline__ float minus_abs(float x) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(-fabsf(x)), "f"(-64.f));
-  return r;
-}
 // x Phi(x) = max(x, 0) - |x| Phi(-|x|); fp32 results within a few ulp, from
 // normcdff (both tails keep their relative accuracy; the rational form's error
 // would be several ulp between -3.5 and -0.5).  That costs time: forward and

@@ -47,6 +47,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "groups.cuh"
 #include "internal.h"
 #include "tensor_map.h"
 
@@ -153,12 +154,18 @@ struct Params {
   unsigned int* status;
   uint64_t timeout_ns;
   int fault_injection;
+  // grouped products (KIND_ROWS, KIND_INNER): `groups` matrices of B (stride_b) or
+  // of C (stride_c), their rows of A or their ranges of K from `offsets`
+  const int* offsets;
+  int groups;
 };
 
 // Kernel kinds: one output tile per block (C), one K slice of a tile per
 // block (raw partials, reduced by a second kernel), or persistent blocks over
-// whole tiles and then shared K steps (C, with in-kernel fix-up).
-constexpr int KIND_TILE = 0, KIND_SPLIT = 1, KIND_PERSIST = 2;
+// whole tiles and then shared K steps (C, with in-kernel fix-up); or a tile per
+// block of a grouped product, over its groups' rows or, blockIdx.y being the group,
+// its range of K (sgemm_grouped.cu).
+constexpr int KIND_TILE = 0, KIND_SPLIT = 1, KIND_PERSIST = 2, KIND_ROWS = 3, KIND_INNER = 4;
 
 // ---------------------------------------------------------------- staging
 // Tile layouts per operand and stage:
@@ -418,11 +425,13 @@ __device__ __forceinline__ int lane_row(int arow, int i) {
 // contributor goes on, with the sum of all contributions.  Then the epilogue
 // (alpha, beta, bias, activation) stores the lane's block of C, or, in a
 // split launch, its raw sums in slice blockIdx.z of `partial`.  SYNC: the
-// barrier over the computing threads (compute_sync); RI: lane_row's layout.
+// barrier over the computing threads (compute_sync); RI: lane_row's layout; rows:
+// those of Cg.
 template <class TL, int KIND, int SYNC, bool RI = false>
 __device__ __forceinline__ void finish_item(const Params& p, uint64_t (&acc)[8][TL::JP],
                                             const Item& w, int64_t sk_first, int m0, int n0,
-                                            float* Cg, int tid, int arow, int bcol, int& s_last) {
+                                            float* Cg, int rows, int tid, int arow, int bcol,
+                                            int& s_last) {
   constexpr int BM = TL::BM, BN = TL::BN, THREADS = TL::THREADS, JP = TL::JP, HB = TL::HB;
   if constexpr (KIND == KIND_PERSIST) {
     if (!w.whole) {
@@ -486,7 +495,7 @@ __device__ __forceinline__ void finish_item(const Params& p, uint64_t (&acc)[8][
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int gm = m0 + lane_row<RI>(arow, i);
-    if (gm >= p.M) continue;
+    if (gm >= rows) continue;
 #pragma unroll
     for (int h = 0; h < HB; ++h) {
       const int gn = n0 + bcol + h * 16;
@@ -559,9 +568,26 @@ __global__ void __launch_bounds__(TL::THREADS, TL::MIN_BLOCKS) sgemm_ffma_kernel
   const int bcol = wn + tx * 4;     // lane cols: bcol + 16 h + {0..3}, h < HB
   const int aswz = (arow >> 2) & TL::SWZ_MASK;  // row-tile chunk permutation, same for all 8 lane rows
 
-  const float* const Ag = p.A + (int64_t)blockIdx.y * p.stride_a;
-  const float* const Bg = p.B + (int64_t)blockIdx.y * p.stride_b;
-  float* const Cg = p.C + (int64_t)blockIdx.y * p.stride_c;
+  const float* Ag = p.A + (int64_t)blockIdx.y * p.stride_a;
+  const float* Bg = p.B + (int64_t)blockIdx.y * p.stride_b;
+  float* Cg = p.C + (int64_t)blockIdx.y * p.stride_c;
+  int rows = p.M;
+  [[maybe_unused]] int group_tile = 0;
+  if constexpr (KIND == KIND_ROWS || KIND == KIND_INNER) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0)
+      check_offsets(p.offsets, p.groups, KIND == KIND_ROWS ? p.M : p.K, p.status, lane);
+  }
+  if constexpr (KIND == KIND_ROWS) {
+    // (every warp finds the block's tile by itself)
+    RowTiles<BM> walk;
+    walk.init(p.offsets, p.groups, p.M, lane);
+    int g, lo;
+    if (!walk.find(p.offsets, p.groups, p.M, p.tiles_n, blockIdx.x, lane, g, lo, rows, group_tile))
+      return;
+    Ag += (int64_t)lo * p.lda;
+    Bg += (int64_t)g * p.stride_b;
+    Cg += (int64_t)lo * p.ldc;
+  }
   const uint32_t sbase = smem_u32(smem);
 
   // work state: non-persistent blocks do one item; persistent blocks walk
@@ -583,19 +609,31 @@ __global__ void __launch_bounds__(TL::THREADS, TL::MIN_BLOCKS) sgemm_ffma_kernel
       w.kend = min(p.K, w.kbeg + p.k_slice);
       w.seg0 = 0;
       w.whole = true;
+      if constexpr (KIND == KIND_INNER) {
+        int n;
+        group_span(p.offsets, blockIdx.y, p.K, w.kbeg, n);
+        w.kend = w.kbeg + n;
+      }
     } else {
       if (!walk.next<BK>(p, G, w)) break;
     }
     first_item = false;
     int m0, n0;
-    tile_origin<TL>(p, w.t, m0, n0);
+    if constexpr (KIND == KIND_ROWS) {
+      // (row tiles of a group next to each other: they share a panel of B)
+      const int rt = (rows + BM - 1) / BM;
+      m0 = group_tile % rt * BM;
+      n0 = group_tile / rt * TL::BN;
+    } else {
+      tile_origin<TL>(p, w.t, m0, n0);
+    }
     const int kbeg = w.kbeg, kend = w.kend;
     const int nk = (kend - kbeg + BK - 1) / BK;
 
     auto stage_load = [&](int s, int k0) {
       const uint32_t st = sbase + (uint32_t)(s * STAGE_FLOATS) * 4u;
-      if constexpr (A_K) load_rows<TL, VEC>(st, Ag, p.lda, m0, p.M, k0, kend, tid);
-      else load_kmajor<TL, VEC, BM, APAD>(st, Ag, p.lda, m0, p.M, k0, kend, tid);
+      if constexpr (A_K) load_rows<TL, VEC>(st, Ag, p.lda, m0, rows, k0, kend, tid);
+      else load_kmajor<TL, VEC, BM, APAD>(st, Ag, p.lda, m0, rows, k0, kend, tid);
       const uint32_t sb = st + A_FLOATS * 4u;
       if constexpr (B_K) load_transpose<TL, TL::BN, BPAD>(sb, Bg, p.ldb, n0, p.N, k0, kend, tid);
       else load_kmajor<TL, VEC, TL::BN, BPAD>(sb, Bg, p.ldb, n0, p.N, k0, kend, tid);
@@ -655,7 +693,7 @@ __global__ void __launch_bounds__(TL::THREADS, TL::MIN_BLOCKS) sgemm_ffma_kernel
     }
     cp_async_wait<0>();
 
-    finish_item<TL, KIND, 0>(p, acc, w, walk.sk_first, m0, n0, Cg, tid, arow, bcol, s_last);
+    finish_item<TL, KIND, 0>(p, acc, w, walk.sk_first, m0, n0, Cg, rows, tid, arow, bcol, s_last);
   }
 }
 
@@ -842,7 +880,7 @@ __global__ void __launch_bounds__(TL::THREADS + 32, TL::MIN_BLOCKS)
       }
       if (++stage == NST) { stage = 0; phase ^= 1u; }
     }
-    finish_item<TL, KIND, TL::THREADS, A_K>(p, acc, w, walk.sk_first, m0, n0, p.C, tid, arow,
+    finish_item<TL, KIND, TL::THREADS, A_K>(p, acc, w, walk.sk_first, m0, n0, p.C, p.M, tid, arow,
                                             bcol, s_last);
   }
 }

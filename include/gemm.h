@@ -346,9 +346,93 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
             gemm_stream_t stream);
 
 /*
+ * gemm_fused -- a layer's forward product with all that follows it, in one pass:
+ *
+ *     U = alpha * op(A) * op(B) + bias[j],    Y = act(U) + beta * R
+ *
+ * (gemm_ex() adds beta * C before the activation; here the residual R comes after
+ * it, and U can be kept for the backward pass.)
+ *
+ * dtype: GEMM_F32, GEMM_F16_F32ACC or GEMM_BF16_F32ACC, of every matrix and of bias.
+ * bias: N elements, or NULL.  act: a gemm_act_t, applied to the fp32 value of U
+ *   before its rounding.  GEMM_ACT_GELU as in gemm_mx_quantize(); in fp32 without U
+ *   and R it is gemm_ex()'s.
+ * R: M x N with ldr, or NULL; beta == 0 reads no R.  R may be Y itself with the same
+ *   pitch.
+ * U: M x N with ldu, stored rounded to dtype; or NULL.
+ * M, N and K up to 2^31 - 2^18 (else GEMM_ERR_UNSUPPORTED).  Outputs may overlap no
+ * input but as said (GEMM_ERR_ALIAS).  K == 0: the product is zero.  16-bit operands
+ * whose rows are not 16-byte aligned are copied to scratch in stream order.
+ */
+int gemm_fused(int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype, float alpha,
+               const void* A, int64_t lda, const void* B, int64_t ldb, const void* bias, int act,
+               float beta, const void* R, int64_t ldr, void* U, int64_t ldu, void* Y, int64_t ldy,
+               gemm_stream_t stream);
+
+/*
+ * gemm_fused_backward -- the gradient that passes back through a product and the
+ * activation before it:
+ *
+ *     dX = (alpha * op(A) * op(B)) * act'(U),    dbias[j] = sum_i dX[i, j]
+ *
+ * U: the stored pre-activation, M x N with ldu; not read with GEMM_ACT_NONE (may then
+ *   be NULL).  act': relu 1 where U > 0, else dX is 0; gelu Phi(U) + U phi(U).
+ * dX: M x N with lddx; may be U itself with the same pitch.
+ * dbias: N fp32 sums of dX before its rounding (in an order that does not change from
+ *   call to call), or NULL.  M == 0 sets them to zero.
+ */
+int gemm_fused_backward(int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype,
+                        float alpha, const void* A, int64_t lda, const void* B, int64_t ldb, int act,
+                        const void* U, int64_t ldu, void* dX, int64_t lddx, float* dbias,
+                        gemm_stream_t stream);
+
+/*
+ * gemm_grouped -- gemm_fused() by groups of rows, as a router sends tokens to experts:
+ * for each group g, on rows offsets[g] .. offsets[g+1] - 1 of A, R, U and Y,
+ *
+ *     U = alpha * A * op(B_g) + bias[g][j],    Y = act(U) + beta * R
+ *
+ * offsets: groups + 1 int32 in DEVICE memory, ascending within 0 .. rows; the call
+ *   does not wait for them.  Groups may be empty and of any size; rows before
+ *   offsets[0] and from offsets[groups] on are neither used nor written.  Offsets that
+ *   do not ascend within 0 .. rows make results unspecified, but nothing outside the
+ *   given matrices is read or written, and gemm_check_device_status() then returns
+ *   GEMM_ERR_INVALID_ARG.
+ * A: rows x K (lda).  B_g = B + g * strideB: K x N, or with transB N x K (ldb).  A
+ *   stride of 0 shares one matrix.
+ * bias: groups x N contiguous, or NULL.  groups up to 65535.
+ */
+int gemm_grouped(int transB, int64_t rows, int64_t N, int64_t K, int64_t groups,
+                 const int32_t* offsets, int dtype, float alpha, const void* A, int64_t lda,
+                 const void* B, int64_t ldb, int64_t strideB, const void* bias, int act, float beta,
+                 const void* R, int64_t ldr, void* U, int64_t ldu, void* Y, int64_t ldy,
+                 gemm_stream_t stream);
+
+/* gemm_grouped_backward -- gemm_fused_backward() by groups of rows (see
+ * gemm_grouped()); dbias: groups x N contiguous, zero for an empty group. */
+int gemm_grouped_backward(int transB, int64_t rows, int64_t N, int64_t K, int64_t groups,
+                          const int32_t* offsets, int dtype, float alpha, const void* A, int64_t lda,
+                          const void* B, int64_t ldb, int64_t strideB, int act, const void* U,
+                          int64_t ldu, void* dX, int64_t lddx, float* dbias, gemm_stream_t stream);
+
+/*
+ * gemm_grouped_wgrad -- the gradient of each group's matrix, over its rows:
+ *
+ *     C_g = alpha * A_g^T * B_g + beta * C_g
+ *
+ * A: rows x M (lda), B: rows x N (ldb), A_g and B_g their rows of group g (offsets as
+ * in gemm_grouped()); C_g = C + g * strideC: M x N (ldc), which must not overlap one
+ * another.  An empty group's C_g is beta * C_g (zero with beta == 0, which reads no C).
+ */
+int gemm_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int64_t groups, const int32_t* offsets,
+                       int dtype, float alpha, float beta, const void* A, int64_t lda, const void* B,
+                       int64_t ldb, void* C, int64_t ldc, int64_t strideC, gemm_stream_t stream);
+
+/*
  * gemm_check_device_status -- synchronises `stream`, then reads and clears
  * the current device's status word.  Returns GEMM_ERR_TIMEOUT if a kernel
- * gave up on a wait since the last check, GEMM_ERR_CUDA if the stream
+ * gave up on a wait since the last check, GEMM_ERR_INVALID_ARG if a grouped
+ * product's offsets did not ascend within its rows, GEMM_ERR_CUDA if the stream
  * reported an error, GEMM_OK otherwise.
  */
 int gemm_check_device_status(gemm_stream_t stream);
@@ -380,8 +464,10 @@ typedef enum {
     GEMM_PATH_MX = 9,          /* microscaled storage: quantise, dequantise, act backward */
     GEMM_PATH_MX_TC = 10,      /* product of 4-bit operands: block-scaled tcgen05 kernel */
     GEMM_PATH_MX_STREAM = 11,  /* few rows times a stored right operand, read once */
-    GEMM_PATH_MX_CONVERT = 12  /* 16-bit rows times a stored right operand, converted inside
+    GEMM_PATH_MX_CONVERT = 12, /* 16-bit rows times a stored right operand, converted inside
                                   the tcgen05 kernel */
+    GEMM_PATH_FUSED_TC = 13,   /* fused or grouped product: its tcgen05 kernel */
+    GEMM_PATH_FUSED_FFMA = 14  /* the same in fp32: FFMA kernels, then the epilogue */
 } gemm_path_t;
 
 int gemm_last_path(void);
