@@ -71,28 +71,25 @@ __global__ void __launch_bounds__(256) fused_finish_kernel(const FinishParams p)
         f[i] = in && p.mode != FUSED_NONE ? p.in[(m0 + i0 + i) * p.ld_in + n] : 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-#pragma unroll
-        for (int k = i; k < i + 2; ++k) {
-          v[k] = p.alpha * v[k] + bias;
-          if (p.U && i0 + k < rows) p.U[(m0 + i0 + k) * p.ldu + n] = v[k];
-        }
-        if (p.mode == FUSED_SLOPE) {
-          slope_pair<float>(v[i], v[i + 1], f[i], f[i + 1], p.act);
-        } else {
-          act_pair<float>(v[i], v[i + 1], p.act);
-          if (p.mode == FUSED_ADD) {
-            v[i] = __fmaf_rn(p.beta, f[i], v[i]);
-            v[i + 1] = __fmaf_rn(p.beta, f[i + 1], v[i + 1]);
-          }
-        }
-#pragma unroll
-        for (int k = i; k < i + 2; ++k)
-          if (i0 + k < rows) {
-            p.Y[(m0 + i0 + k) * p.ldy + n] = v[k];
-            sum += v[k];
-          }
+      for (int i = 0; i < 8; ++i) {
+        v[i] = p.alpha * v[i] + bias;
+        if (p.U && i0 + i < rows) p.U[(m0 + i0 + i) * p.ldu + n] = v[i];
       }
+      if (p.mode == FUSED_SLOPE) {
+        slope_of<float>(v, f, p.act);
+      } else {
+        act_of<float>(v, p.act);
+        if (p.mode == FUSED_ADD) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(p.beta, f[i], v[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < rows) {
+          p.Y[(m0 + i0 + i) * p.ldy + n] = v[i];
+          sum += v[i];
+        }
     }
     if (p.part) p.part[(int64_t)slot * p.N + n] = sum;
   }

@@ -161,19 +161,19 @@ __device__ __forceinline__ void fu_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo,
         : "memory");
 }
 
-// Column sums over the warp's 32 rows: lane l gets the sum of v[l] over the lanes,
-// in a fixed order (each step sends half of the columns to the lane across and
-// adds those received to the other half: 31 shuffles in all).
-__device__ __forceinline__ float warp_column_sum(float (&v)[32], int lane) {
+// Column sums of 16 columns over the warp's 32 rows, in a fixed order: each step sends
+// half of the columns to the lane across and adds those received to the other half.
+// Lanes l and l ^ 1 get the sum of column l / 2.
+__device__ __forceinline__ float warp_column_sum(float (&v)[16], int lane) {
 #pragma unroll
-  for (int d = 16; d >= 1; d /= 2)
+  for (int d = 8; d >= 1; d /= 2)
 #pragma unroll
     for (int i = 0; i < d; ++i) {
-      const bool up = (lane & d) != 0;
+      const bool up = (lane & (2 * d)) != 0;
       const float give = up ? v[i] : v[i + d], keep = up ? v[i + d] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * d);
     }
-  return v[0];
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
 // Byte offset of column c (of 64) of row r in a staging buffer: 16-byte chunks in
@@ -498,18 +498,14 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
       tc_fence_after();
       const uint32_t t_row =
           tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + hh * CW);
-      const bool zero = u.k_len == 0;  // no product was added up
       if (nbox == 0) release_acc(buf);
 #pragma unroll 1
       for (int i = 0; i < nbox; ++i, ++boxes) {
         const int gn = gn0 + 64 * i, cols = min(p.N - gn, 64);
         const uint32_t yb = bufs + (uint32_t)(y_buf(boxes) * 4096), ub = bufs + 4096u;
-        uint32_t r[2][32];
+        uint32_t r[16];
         __syncwarp();
-        tmem_ld_32x32b_x32(t_row + (uint32_t)(i * 64), r[0]);
-        tmem_ld_32x32b_x32(t_row + (uint32_t)(i * 64 + 32), r[1]);
-        tmem_ld_wait();
-        if (i == nbox - 1) release_acc(buf);
+        tmem_ld_32x32b_x16(t_row + (uint32_t)(i * 64), r);
         // this box's buffers are free, `in` is there
         bool there = true;
         if (lane == 0) {
@@ -537,85 +533,95 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
         }
         // (the next box's `in` goes into the other buffer while this one is worked on)
         if (has_in && p.tma_in && !has_u && i + 1 < nbox) request(boxes + 1, gn + 64, gm);
+        // Sixteen columns at a time, the next sixteen's accumulators on their way.  (Not
+        // unrolled: the code that one call takes of all that is here then stays in the
+        // instruction cache; unrolled over 64 columns, steps that a call does not take
+        // slowed it as well: wgrad of 4000 rows of 8 groups 140 us, 117 without the
+        // slope's code in the kernel.)
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t next[16];
+          if (c < 3) tmem_ld_32x32b_x16(t_row + (uint32_t)(i * 64 + 16 * c + 16), next);
+          const int col = gn + 16 * c;
+          float v[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          for (int e = 0; e < 16; ++e) v[e] = p.alpha * __uint_as_float(r[e]);
+          if (u.k_len == 0) {  // (no product was added up)
 #pragma unroll
-          for (int ww = 0; ww < 4; ++ww) {
-            const int w = 4 * h + ww, col = gn + 8 * w;
-            const uint32_t at = (uint32_t)(lane * 128 + ((w ^ (lane & 7)) * 16));
-            float v[8];
+            for (int e = 0; e < 16; ++e) v[e] = 0.f;
+          }
+          if (p.bias) {
+            const T* b = static_cast<const T*>(p.bias) + (int64_t)u.g * p.N + col;
+            if (p.bias_vec && col + 15 < p.N) {
+              uint4 bv[2] = {__ldg(reinterpret_cast<const uint4*>(b)),
+                             __ldg(reinterpret_cast<const uint4*>(b) + 1)};
+              const typename E::T2* b2 = reinterpret_cast<const typename E::T2*>(bv);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = zero ? 0.f : p.alpha * __uint_as_float(r[h][8 * ww + e]);
-            if (p.bias) {
-              const T* b = static_cast<const T*>(p.bias) + (int64_t)u.g * p.N + col;
-              if (p.bias_vec && col + 7 < p.N) {
-                const uint4 bv = __ldg(reinterpret_cast<const uint4*>(b));
-                const typename E::T2* b2 = reinterpret_cast<const typename E::T2*>(&bv);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float2 f = E::unpack(b2[e]);
-                  v[2 * e] += f.x;
-                  v[2 * e + 1] += f.y;
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (col + e < p.N) v[e] += E::to(b[e]);
+              for (int e = 0; e < 8; ++e) {
+                const float2 f = E::unpack(b2[e]);
+                v[2 * e] += f.x;
+                v[2 * e + 1] += f.y;
               }
-            }
-            auto put = [&](uint32_t dst) {
-              uint4 o;
-              typename E::T2* oh = reinterpret_cast<typename E::T2*>(&o);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) oh[e] = E::pack(v[2 * e], v[2 * e + 1]);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(o.x),
-                           "r"(o.y), "r"(o.z), "r"(o.w)
-                           : "memory");
-            };
-            if (has_u) put(ub + at);
-            float f[8];
-            if (has_in) {
-              uint4 ci;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(ci.x), "=r"(ci.y), "=r"(ci.z), "=r"(ci.w)
-                           : "r"(yb + at)
-                           : "memory");
-              const typename E::T2* c2 = reinterpret_cast<const typename E::T2*>(&ci);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 x = E::unpack(c2[e]);
-                f[2 * e] = x.x;
-                f[2 * e + 1] = x.y;
-              }
-            }
-            if (p.mode == FUSED_SLOPE) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                slope_pair<T>(v[2 * e], v[2 * e + 1], f[2 * e], f[2 * e + 1], p.act);
             } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) act_pair<T>(v[2 * e], v[2 * e + 1], p.act);
-              if (p.mode == FUSED_ADD) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __fmaf_rn(p.beta, f[e], v[e]);
-              }
-            }
-            put(yb + at);
-            if (p.part) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                r[h][8 * ww + e] = __float_as_uint(lane < rows ? v[e] : 0.f);
+              for (int e = 0; e < 16; ++e)
+                if (col + e < p.N) v[e] += E::to(b[e]);
             }
           }
+          const uint32_t at[2] = {(uint32_t)(lane * 128 + (((2 * c) ^ (lane & 7)) * 16)),
+                                  (uint32_t)(lane * 128 + (((2 * c + 1) ^ (lane & 7)) * 16))};
+          auto put = [&](uint32_t dst) {
+            uint4 o[2];
+            typename E::T2* oh = reinterpret_cast<typename E::T2*>(o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) oh[e] = E::pack(v[2 * e], v[2 * e + 1]);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + at[w]), "r"(o[w].x),
+                           "r"(o[w].y), "r"(o[w].z), "r"(o[w].w)
+                           : "memory");
+          };
+          if (has_u) put(ub);
+          if (p.mode != FUSED_SLOPE) act_of<T>(v, p.act);
+          if (has_in) {
+            uint4 ci[2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(ci[w].x), "=r"(ci[w].y), "=r"(ci[w].z), "=r"(ci[w].w)
+                           : "r"(yb + at[w])
+                           : "memory");
+            const typename E::T2* c2 = reinterpret_cast<const typename E::T2*>(ci);
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 x = E::unpack(c2[e]);
+              f[2 * e] = x.x;
+              f[2 * e + 1] = x.y;
+            }
+            if (p.mode == FUSED_SLOPE) {
+              slope_of<T>(v, f, p.act);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __fmaf_rn(p.beta, f[e], v[e]);
+            }
+          }
+          put(yb);
           if (p.part) {
-            float s[32];
+            if (lane >= rows) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(r[h][e]);
-            const float sum = warp_column_sum(s, lane);
+              for (int e = 0; e < 16; ++e) v[e] = 0.f;
+            }
+            const float sum = warp_column_sum(v, lane);
             const int64_t slot = (int64_t)(u.g_lo >> 5) + u.g + ((gm - u.g_lo) >> 5);
-            if (32 * h + lane < cols) p.part[slot * p.N + gn + 32 * h + lane] = sum;
+            if ((lane & 1) == 0 && col + (lane >> 1) < p.N) p.part[slot * p.N + col + (lane >> 1)] = sum;
           }
+          __syncwarp();
+          tmem_ld_wait();
+          if (c == 2 && i == nbox - 1) release_acc(buf);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = next[e];
         }
         // a box that the group's end cuts is stored row by row
         const bool cut = p.kind == FUSED_ROWS && rows < 32;

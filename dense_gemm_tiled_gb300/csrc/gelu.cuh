@@ -40,51 +40,61 @@ __device__ __forceinline__ float minus_abs(float x) {
   return r;
 }
 
-// x0, x1 -> act(x0), act(x1) (0 none, 1 relu: x where x > 0, else 0, 2 gelu).  The
-// gelu as max(x, 0) - |x| Phi(-|x|): for 16-bit results from the form above, for
-// fp32 ones from normcdff, within a few ulp in both tails.
-template <typename T>
-__device__ __forceinline__ void act_pair(float& x0, float& x1, int act) {
-  if (act == 0) return;
-  const float m0 = x0 > 0.f ? x0 : 0.f, m1 = x1 > 0.f ? x1 : 0.f;
+// v -> act(v) (0 none, 1 relu: v where v > 0, else 0, 2 gelu).  The gelu as max(x, 0) -
+// |x| Phi(-|x|): for 16-bit results from the form above, for fp32 ones from normcdff,
+// within a few ulp in both tails.
+template <typename T, int N>
+__device__ __forceinline__ void act_of(float (&v)[N], int act) {
   if (act == 1) {
-    x0 = m0;
-    x1 = m1;
-  } else if constexpr (sizeof(T) == 4) {
-    const float n0 = minus_abs(x0), n1 = minus_abs(x1);
-    x0 = __fmaf_rn(n0, normcdff(n0), m0);
-    x1 = __fmaf_rn(n1, normcdff(n1), m1);
-  } else {
-    const f32x2 n = pair(minus_abs(x0), minus_abs(x1));
-    f32x2 e;
-    const f32x2 c = normal_tail2(n, e);
-    unpair(fma2(n, c, pair(m0, m1)), x0, x1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] > 0.f ? v[i] : 0.f;
+  } else if (act == 2) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float m0 = v[i] > 0.f ? v[i] : 0.f, m1 = v[i + 1] > 0.f ? v[i + 1] : 0.f;
+      if constexpr (sizeof(T) == 4) {
+        const float n0 = minus_abs(v[i]), n1 = minus_abs(v[i + 1]);
+        v[i] = __fmaf_rn(n0, normcdff(n0), m0);
+        v[i + 1] = __fmaf_rn(n1, normcdff(n1), m1);
+      } else {
+        const f32x2 n = pair(minus_abs(v[i]), minus_abs(v[i + 1]));
+        f32x2 e;
+        const f32x2 c = normal_tail2(n, e);
+        unpair(fma2(n, c, pair(m0, m1)), v[i], v[i + 1]);
+      }
+    }
   }
 }
 
-// d0 *= act'(x0), d1 *= act'(x1).  relu: d where x > 0, else 0 (whatever d is);
-// gelu: h = Phi(-|x|) - |x| phi(x) where x < 0, else 1 - h.
-template <typename T>
-__device__ __forceinline__ void slope_pair(float& d0, float& d1, float x0, float x1, int act) {
-  if (act == 0) return;
+// d *= act'(x).  relu: d where x > 0, else 0 (whatever d is); gelu: h = Phi(-|x|) -
+// |x| phi(x) where x < 0, else 1 - h.
+template <typename T, int N>
+__device__ __forceinline__ void slope_of(float (&d)[N], const float (&x)[N], int act) {
   if (act == 1) {
-    d0 = x0 > 0.f ? d0 : 0.f;
-    d1 = x1 > 0.f ? d1 : 0.f;
-  } else if constexpr (sizeof(T) == 4) {
-    const float n0 = minus_abs(x0), n1 = minus_abs(x1);
-    const float h0 = __fmaf_rn(n0 * 0.39894228f, expf(-0.5f * n0 * n0), normcdff(n0));
-    const float h1 = __fmaf_rn(n1 * 0.39894228f, expf(-0.5f * n1 * n1), normcdff(n1));
-    d0 *= x0 < 0.f ? h0 : 1.f - h0;
-    d1 *= x1 < 0.f ? h1 : 1.f - h1;
-  } else {
-    const f32x2 n = pair(minus_abs(x0), minus_abs(x1));
-    f32x2 e;
-    const f32x2 c = normal_tail2(n, e);
-    const f32x2 h = fma2(mul2(n, pair(0.39894228f)), e, c);
-    float h0, h1, g0, g1;
-    unpair(h, h0, h1);
-    unpair(fma2(h, pair(-1.f), pair(1.f)), g0, g1);
-    unpair(mul2(pair(d0, d1), pair(x0 < 0.f ? h0 : g0, x1 < 0.f ? h1 : g1)), d0, d1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = x[i] > 0.f ? d[i] : 0.f;
+  } else if (act == 2) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = i; k < i + 2; ++k) {
+          const float n = minus_abs(x[k]);
+          const float h = __fmaf_rn(n * 0.39894228f, expf(-0.5f * n * n), normcdff(n));
+          d[k] *= x[k] < 0.f ? h : 1.f - h;
+        }
+      } else {
+        const f32x2 n = pair(minus_abs(x[i]), minus_abs(x[i + 1]));
+        f32x2 e;
+        const f32x2 c = normal_tail2(n, e);
+        const f32x2 h = fma2(mul2(n, pair(0.39894228f)), e, c);
+        float h0, h1, g0, g1;
+        unpair(h, h0, h1);
+        unpair(fma2(h, pair(-1.f), pair(1.f)), g0, g1);
+        unpair(mul2(pair(d[i], d[i + 1]), pair(x[i] < 0.f ? h0 : g0, x[i + 1] < 0.f ? h1 : g1)), d[i],
+               d[i + 1]);
+      }
+    }
   }
 }
 
