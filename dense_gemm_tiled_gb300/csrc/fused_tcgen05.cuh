@@ -11,7 +11,7 @@
 // inner dimension of C_g's product (FUSED_INNER).
 //
 // The block is that of the 4-bit product (mx4_tcgen05.cu): a TMA producer warp, a
-// warp that issues the MMAs, eight epilogue warps; persistent workers (blocks, or
+// warp that issues the MMAs, epilogue warps; persistent workers (blocks, or
 // pairs of blocks on 2-SM MMAs) walk the tiles.  What the groups change:
 //  * A tile's place follows from the offsets alone, so every role finds it by
 //    itself: a warp looks at 32 groups at once (tile counts by lane, their running
@@ -27,10 +27,13 @@
 //    at (x, n - 64, r): it ends with those n rows, in both operands alike, and what
 //    lies ahead of them is out of range and reads as zero.  One map bounds every
 //    group, with nothing masked in shared memory.
-//  * R or U comes in by TMA ahead of the accumulator, into the staging buffer that
-//    the result leaves from; column sums are taken from registers, 32 rows at a
-//    time, by a transposing shuffle reduction, and joined by fused_dbias_kernel in
-//    the order of the rows.
+//  * Sixteen epilogue warps, a box of 32 rows x 64 columns of the tile each: what they
+//    do to a value is a chain of dependent instructions (a gelu or its slope, a
+//    rounding), and four warps a scheduler hide its latency where two did not
+//    (wgrad of 4000 rows of 8 groups 102 -> 92 us).  R or U comes by TMA, ahead of the
+//    accumulator, into the staging buffer that the result then leaves from; column
+//    sums are taken from registers, 32 rows at a time, by a transposing shuffle
+//    reduction, and joined by fused_dbias_kernel in the order of the rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -44,16 +47,15 @@
 namespace gb300 {
 namespace {
 
-constexpr int FU_EPI = 8;      // epilogue warps: two per lane quarter, half of the columns each
+constexpr int FU_EPI = 16;     // epilogue warps
 constexpr int FU_THREADS = 64 + 32 * FU_EPI;
-constexpr int FU_NBUF = 2;     // staging buffers (32 rows x 128 bytes) of an epilogue warp
 
 template <int BN, bool PAIR>
 struct FuCfg {
-  static constexpr int HALVES = BN >= 128 ? 2 : 1;  // epilogue warps in use per lane quarter
+  static constexpr int SHARES = BN / 64;  // epilogue warps in use per lane quarter
   static constexpr int B_BYTES = (PAIR ? BN / 2 : BN) * 128;
   static constexpr int STAGE_BYTES = A_TILE_BYTES + B_BYTES;
-  static constexpr int STAGING_BYTES = 4 * HALVES * FU_NBUF * 4096;
+  static constexpr int STAGING_BYTES = 4 * SHARES * 4096;
   static constexpr int FIXED = 1024 + 512;
   static constexpr int RAW = (SMEM_LIMIT - FIXED - STAGING_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = RAW < 8 ? RAW : 8;
@@ -80,7 +82,8 @@ struct FuParams {
   int64_t ldu;
   void* Y;
   int64_t ldy, stride_y;
-  int tma_in, tma_u, tma_y;  // 16-byte aligned rows: through the tensor-memory-access unit
+  int tma_in, tma_y;  // 16-byte aligned rows: through the tensor-memory-access unit
+  int vec_u;          // 32-byte aligned rows
   float* part;         // column sums of each 32 rows of a group, [rows / 32 + groups + 1][N]
   unsigned int* status;
   uint64_t timeout_ns;
@@ -181,31 +184,7 @@ __device__ __forceinline__ float warp_column_sum(float (&v)[16], int lane) {
 __device__ __forceinline__ uint32_t fu_at(int r, int c) {
   return (uint32_t)(r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
 }
-// Rows off 16-byte alignment between global memory and a staging buffer, by the
-// whole warp, a row's 64 columns at a time (rows and columns past the ends
-// excepted).
-template <typename T>
-__device__ __forceinline__ void fu_rows_in(const T* src, int64_t ld, int rows, int cols,
-                                           uint32_t sbuf, int lane) {
-  const uint16_t* s = reinterpret_cast<const uint16_t*>(src);
-#pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += 8) {
-    uint16_t v[8][2];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        v[i][h] = (r0 + i < rows && lane + 32 * h < cols) ? s[(int64_t)(r0 + i) * ld + lane + 32 * h]
-                                                          : (uint16_t)0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(sbuf + fu_at(r0 + i, lane + 32 * h)),
-                     "h"(v[i][h])
-                     : "memory");
-  }
-}
+// A box's rows from its staging buffer to memory, row by row
 // (vec: 16-byte aligned rows, eight lanes a row)
 template <typename T>
 __device__ __forceinline__ void fu_rows_out(T* dst, int64_t ld, int rows, int cols, bool vec,
@@ -239,8 +218,8 @@ __device__ __forceinline__ void fu_rows_out(T* dst, int64_t ld, int rows, int co
 template <typename T, int BN, bool A_MN, bool B_MN, bool PAIR>
 __global__ void __launch_bounds__(FU_THREADS, 1)
     fused_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmI, const __grid_constant__ CUtensorMap tmU,
-                    const __grid_constant__ CUtensorMap tmY, const FuParams p) {
+                    const __grid_constant__ CUtensorMap tmI, const __grid_constant__ CUtensorMap tmY,
+                    const FuParams p) {
   using C_ = FuCfg<BN, PAIR>;
   using E = Elem<T>;
   constexpr int STAGES = C_::STAGES;
@@ -263,11 +242,10 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
   auto accf_bar = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + b); };
   auto acce_bar = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 + b); };
   const uint32_t drain_bar = bar0 + 8u * (uint32_t)(2 * STAGES + 4);
-  auto in_bar = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 5 + b); };
-  constexpr int NIN = 4 * C_::HALVES * FU_NBUF;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + NIN);
+  auto in_bar = [&](int w) { return bar0 + 8u * (uint32_t)(2 * STAGES + 5 + w); };
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + 4 * C_::SHARES);
   volatile uint32_t* const abort_flag = tmem_slot + 1;
-  static_assert(8 * (2 * STAGES + 6 + NIN) <= 512, "barrier area");
+  static_assert(8 * (2 * STAGES + 6 + 4 * C_::SHARES) <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -279,10 +257,10 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), (PAIR ? 2 : 1) * 32 * 4 * C_::HALVES);
+      mbar_init(acce_bar(b), (PAIR ? 2 : 1) * 32 * 4 * C_::SHARES);
     }
     mbar_init(drain_bar, 1);
-    for (int b = 0; b < NIN; ++b) mbar_init(in_bar(b), 1);
+    for (int w = 0; w < 4 * C_::SHARES; ++w) mbar_init(in_bar(w), 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -452,203 +430,197 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // tensor-memory lanes 32q .. 32q + 31
     const int ew = warp - 2;
-    const int hh = ew / 4;    // its share of the columns
-    constexpr int CW = BN / C_::HALVES, BOXES = CW / 64;
-    static_assert(CW % 64 == 0, "a share is whole boxes");
-    const uint32_t bufs = staging_addr + (uint32_t)(ew * FU_NBUF * 4096);
-    const bool has_in = p.mode != FUSED_NONE, has_u = p.U != nullptr;
-    // Boxes of 32 rows x 64 columns take the two buffers in turn; with U stored
-    // too, the first is Y's (and R's) and the second U's.
-    int boxes = 0;                     // boxes so far
-    uint32_t in_flight = 0, in_phase = 0;  // loads of `in` under way by buffer, and their parity (lane 0)
-    auto y_buf = [&](int i) { return has_u ? 0 : (i & 1); };
+    const int share = ew / 4;  // its 64 columns of the tile
+    const uint32_t sbuf = staging_addr + (uint32_t)(ew * 4096);
     auto release_acc = [&](int buf) {
       tc_fence_before();
       if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(acce_bar(buf), 0u));
       else mbar_arrive(acce_bar(buf));
     };
-    // requests `in`'s box into its buffer, once the stores before have read it
-    auto request = [&](int i, int gn, int gm) {
-      if (lane == 0) {
-        const int b = y_buf(i);
-        bulk_wait_read<0>();
-        mbar_arrive_expect_tx(in_bar(ew * FU_NBUF + b), 4096u);
-        if (p.kind == FUSED_INNER)
-          tma_load_3d(bufs + (uint32_t)(b * 4096), &tmI, gn, gm, u.g, in_bar(ew * FU_NBUF + b));
-        else
-          tma_load_3d(bufs + (uint32_t)(b * 4096), &tmI, gn, gm, 0, in_bar(ew * FU_NBUF + b));
-        in_flight |= 1u << b;
-      }
-    };
+    uint32_t in_phase = 0;
+    bool in_flight = false;  // (lane 0)
     int it = 0;
-    bool dead = false;
-    for (int64_t t = worker; hh < C_::HALVES && !dead && walk.find(p, t, rank, lane, u);
-         t += workers, ++it) {
+    for (int64_t t = worker; share < C_::SHARES && walk.find(p, t, rank, lane, u); t += workers, ++it) {
       const int buf = it & 1;
-      const int gm = u.m0 + q * 32;                          // this warp's rows
-      const int rows = min(max(u.row_end - gm, 0), 32);
-      const int gn0 = u.n0 + hh * CW;                        // its columns
-      // boxes with something in them (at least none: a share may lie past N)
-      const int nbox = rows > 0 ? min(max((p.N - gn0 + 63) / 64, 0), BOXES) : 0;
-      if (has_in && p.tma_in && nbox > 0) request(boxes, gn0, gm);
+      const int gm = u.m0 + q * 32, gn = u.n0 + 64 * share;  // the warp's box
+      const int rows = min(max(u.row_end - gm, 0), 32), cols = min(p.N - gn, 64);
+      const bool work = rows > 0 && cols > 0;
+      const int64_t gy = p.kind == FUSED_INNER ? (int64_t)u.g * p.stride_y : 0;
+      // R, U or C: the box into the staging buffer, once the last store has read that;
+      // rows off alignment by their lanes instead, sixteen columns ahead
+      const bool in_box = work && p.mode != FUSED_NONE && p.tma_in;
+      const bool in_lanes = work && p.mode != FUSED_NONE && !p.tma_in;
+      if (in_box && lane == 0) {
+        bulk_wait_read<0>();
+        mbar_arrive_expect_tx(in_bar(ew), 4096u);
+        tma_load_3d(sbuf, &tmI, gn, gm, p.kind == FUSED_INNER ? u.g : 0, in_bar(ew));
+        in_flight = true;
+      }
+      uint32_t ahead[8];
+      const uint16_t* const src = reinterpret_cast<const uint16_t*>(
+          static_cast<const T*>(p.in) + gy + (int64_t)(gm + lane) * p.ld_in + gn);
+      auto read_in = [&](int c) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const int at = 16 * c + e;
+          const uint32_t lo = lane < rows && at < cols ? src[at] : 0u;
+          const uint32_t hi = lane < rows && at + 1 < cols ? src[at + 1] : 0u;
+          ahead[e / 2] = lo | hi << 16;
+        }
+      };
+      if (in_lanes) read_in(0);
       bool got = false;
       if (lane == 0) got = mbar_wait(accf_bar(buf), (uint32_t)(it >> 1) & 1u, wc);
       got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
       if (!got) break;
       tc_fence_after();
+      if (!work) {
+        release_acc(buf);
+        continue;
+      }
       const uint32_t t_row =
-          tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + hh * CW);
-      if (nbox == 0) release_acc(buf);
+          tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + 64 * share);
+      got = true;
+      if (lane == 0) {
+        if (in_box) {
+          got = mbar_wait(in_bar(ew), in_phase, wc);
+          if (got) {
+            in_phase ^= 1u;
+            in_flight = false;
+          }
+        } else {
+          bulk_wait_read<0>();  // the last store has read the buffer
+        }
+      }
+      got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+      if (!got) break;
+      // Sixteen columns at a time.  (Not unrolled: the code that one call takes of all
+      // that is here then stays in the instruction cache; unrolled over 64 columns,
+      // steps that a call does not take slowed it as well: wgrad of 4000 rows of 8
+      // groups 140 us, 117 without the slope's code in the kernel.)
 #pragma unroll 1
-      for (int i = 0; i < nbox; ++i, ++boxes) {
-        const int gn = gn0 + 64 * i, cols = min(p.N - gn, 64);
-        const uint32_t yb = bufs + (uint32_t)(y_buf(boxes) * 4096), ub = bufs + 4096u;
+      for (int c = 0; c < 4; ++c) {
+        const int col = gn + 16 * c;
         uint32_t r[16];
-        __syncwarp();
-        tmem_ld_32x32b_x16(t_row + (uint32_t)(i * 64), r);
-        // this box's buffers are free, `in` is there
-        bool there = true;
-        if (lane == 0) {
-          const int b = y_buf(boxes);
-          if (has_in && p.tma_in) {
-            there = mbar_wait(in_bar(ew * FU_NBUF + b), (in_phase >> b) & 1u, wc);
-            if (there) {
-              in_phase ^= 1u << b;
-              in_flight &= ~(1u << b);
+        tmem_ld_32x32b_x16(t_row + (uint32_t)(16 * c), r);
+        const uint32_t at[2] = {sbuf + (uint32_t)(lane * 128 + (((2 * c) ^ (lane & 7)) * 16)),
+                                sbuf + (uint32_t)(lane * 128 + (((2 * c + 1) ^ (lane & 7)) * 16))};
+        uint32_t now[8];
+        if (in_box) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(now[4 * w]), "=r"(now[4 * w + 1]), "=r"(now[4 * w + 2]),
+                           "=r"(now[4 * w + 3])
+                         : "r"(at[w])
+                         : "memory");
+        } else if (in_lanes) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) now[e] = ahead[e];
+          if (c < 3) read_in(c + 1);
+        }
+        tmem_ld_wait();
+        if (c == 3) release_acc(buf);
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = p.alpha * __uint_as_float(r[e]);
+        if (u.k_len == 0) {  // (no product was added up)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        }
+        if (p.bias) {
+          const T* b = static_cast<const T*>(p.bias) + (int64_t)u.g * p.N + col;
+          if (p.bias_vec && col + 15 < p.N) {
+            uint4 bv[2] = {__ldg(reinterpret_cast<const uint4*>(b)),
+                           __ldg(reinterpret_cast<const uint4*>(b) + 1)};
+            const typename E::T2* b2 = reinterpret_cast<const typename E::T2*>(bv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 f = E::unpack(b2[e]);
+              v[2 * e] += f.x;
+              v[2 * e + 1] += f.y;
             }
-          } else if (has_u || has_in) {
-            bulk_wait_read<0>();
           } else {
-            bulk_wait_read<1>();  // (the store before last)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (col + e < p.N) v[e] += E::to(b[e]);
           }
         }
-        there = __shfl_sync(0xffffffffu, there ? 1 : 0, 0) != 0;
-        if (!there) { dead = true; break; }
-        if (has_in && !p.tma_in) {
-          const T* src = static_cast<const T*>(p.in) + gn +
-                         (p.kind == FUSED_INNER ? (int64_t)u.g * p.stride_y : (int64_t)0) +
-                         (int64_t)gm * p.ld_in;
-          fu_rows_in(src, p.ld_in, rows, cols, yb, lane);
-          __syncwarp();
-        }
-        // (the next box's `in` goes into the other buffer while this one is worked on)
-        if (has_in && p.tma_in && !has_u && i + 1 < nbox) request(boxes + 1, gn + 64, gm);
-        // Sixteen columns at a time, the next sixteen's accumulators on their way.  (Not
-        // unrolled: the code that one call takes of all that is here then stays in the
-        // instruction cache; unrolled over 64 columns, steps that a call does not take
-        // slowed it as well: wgrad of 4000 rows of 8 groups 140 us, 117 without the
-        // slope's code in the kernel.)
-        tmem_ld_wait();
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t next[16];
-          if (c < 3) tmem_ld_32x32b_x16(t_row + (uint32_t)(i * 64 + 16 * c + 16), next);
-          const int col = gn + 16 * c;
-          float v[16];
+        auto pack = [&](uint4 (&o)[2]) {
+          typename E::T2* oh = reinterpret_cast<typename E::T2*>(o);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = p.alpha * __uint_as_float(r[e]);
-          if (u.k_len == 0) {  // (no product was added up)
+          for (int e = 0; e < 8; ++e) oh[e] = E::pack(v[2 * e], v[2 * e + 1]);
+        };
+        if (p.U && lane < rows) {
+          uint4 o[2];
+          pack(o);
+          T* const dst = static_cast<T*>(p.U) + (int64_t)(gm + lane) * p.ldu + col;
+          if (p.vec_u && col + 15 < p.N) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+                         "r"(o[0].x), "r"(o[0].y), "r"(o[0].z), "r"(o[0].w), "r"(o[1].x), "r"(o[1].y),
+                         "r"(o[1].z), "r"(o[1].w)
+                         : "memory");
+          } else {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (col + e < p.N)
+                reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+          }
+        }
+        if (p.mode != FUSED_SLOPE) act_of<T>(v, p.act);
+        if (p.mode != FUSED_NONE) {
+          const typename E::T2* c2 = reinterpret_cast<const typename E::T2*>(now);
+          float f[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 x = E::unpack(c2[e]);
+            f[2 * e] = x.x;
+            f[2 * e + 1] = x.y;
+          }
+          if (p.mode == FUSED_SLOPE) {
+            slope_of<T>(v, f, p.act);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __fmaf_rn(p.beta, f[e], v[e]);
+          }
+        }
+        uint4 o[2];
+        pack(o);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at[w]), "r"(o[w].x),
+                       "r"(o[w].y), "r"(o[w].z), "r"(o[w].w)
+                       : "memory");
+        if (p.part) {
+          if (lane >= rows) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = 0.f;
           }
-          if (p.bias) {
-            const T* b = static_cast<const T*>(p.bias) + (int64_t)u.g * p.N + col;
-            if (p.bias_vec && col + 15 < p.N) {
-              uint4 bv[2] = {__ldg(reinterpret_cast<const uint4*>(b)),
-                             __ldg(reinterpret_cast<const uint4*>(b) + 1)};
-              const typename E::T2* b2 = reinterpret_cast<const typename E::T2*>(bv);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 f = E::unpack(b2[e]);
-                v[2 * e] += f.x;
-                v[2 * e + 1] += f.y;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (col + e < p.N) v[e] += E::to(b[e]);
-            }
-          }
-          const uint32_t at[2] = {(uint32_t)(lane * 128 + (((2 * c) ^ (lane & 7)) * 16)),
-                                  (uint32_t)(lane * 128 + (((2 * c + 1) ^ (lane & 7)) * 16))};
-          auto put = [&](uint32_t dst) {
-            uint4 o[2];
-            typename E::T2* oh = reinterpret_cast<typename E::T2*>(o);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) oh[e] = E::pack(v[2 * e], v[2 * e + 1]);
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + at[w]), "r"(o[w].x),
-                           "r"(o[w].y), "r"(o[w].z), "r"(o[w].w)
-                           : "memory");
-          };
-          if (has_u) put(ub);
-          if (p.mode != FUSED_SLOPE) act_of<T>(v, p.act);
-          if (has_in) {
-            uint4 ci[2];
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(ci[w].x), "=r"(ci[w].y), "=r"(ci[w].z), "=r"(ci[w].w)
-                           : "r"(yb + at[w])
-                           : "memory");
-            const typename E::T2* c2 = reinterpret_cast<const typename E::T2*>(ci);
-            float f[16];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 x = E::unpack(c2[e]);
-              f[2 * e] = x.x;
-              f[2 * e + 1] = x.y;
-            }
-            if (p.mode == FUSED_SLOPE) {
-              slope_of<T>(v, f, p.act);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __fmaf_rn(p.beta, f[e], v[e]);
-            }
-          }
-          put(yb);
-          if (p.part) {
-            if (lane >= rows) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = 0.f;
-            }
-            const float sum = warp_column_sum(v, lane);
-            const int64_t slot = (int64_t)(u.g_lo >> 5) + u.g + ((gm - u.g_lo) >> 5);
-            if ((lane & 1) == 0 && col + (lane >> 1) < p.N) p.part[slot * p.N + col + (lane >> 1)] = sum;
-          }
-          __syncwarp();
-          tmem_ld_wait();
-          if (c == 2 && i == nbox - 1) release_acc(buf);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = next[e];
+          const float sum = warp_column_sum(v, lane);
+          const int64_t slot = (int64_t)(u.g_lo >> 5) + u.g + ((gm - u.g_lo) >> 5);
+          if ((lane & 1) == 0 && col + (lane >> 1) < p.N) p.part[slot * p.N + col + (lane >> 1)] = sum;
         }
-        // a box that the group's end cuts is stored row by row
-        const bool cut = p.kind == FUSED_ROWS && rows < 32;
-        const bool ty = p.tma_y && !cut, tu = p.tma_u && !cut;
-        if (!ty || (has_u && !tu)) __syncwarp();
-        if (!ty)
-          fu_rows_out(static_cast<T*>(p.Y) + (int64_t)u.g * p.stride_y + (int64_t)gm * p.ldy + gn,
-                      p.ldy, rows, cols, p.tma_y, yb, lane);
-        if (has_u && !tu)
-          fu_rows_out(static_cast<T*>(p.U) + (int64_t)gm * p.ldu + gn, p.ldu, rows, cols, p.tma_u, ub,
-                      lane);
+        __syncwarp();  // (the tensor-memory loads are the warp's together)
+      }
+      // a box that the group's end cuts is stored row by row, as are rows off alignment
+      if (!p.tma_y || (p.kind == FUSED_ROWS && rows < 32)) {
+        fu_rows_out(static_cast<T*>(p.Y) + gy + (int64_t)gm * p.ldy + gn, p.ldy, rows, cols, p.tma_y,
+                    sbuf, lane);
+        __syncwarp();
+      } else {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (has_u && tu) tma_store_3d(&tmU, gn, gm, 0, ub);
-          if (ty) tma_store_3d(&tmY, gn, gm, p.kind == FUSED_INNER ? u.g : 0, yb);
+          tma_store_3d(&tmY, gn, gm, p.kind == FUSED_INNER ? u.g : 0, sbuf);
           bulk_commit();
         }
-        if (has_in && p.tma_in && has_u && i + 1 < nbox) request(boxes + 1, gn + 64, gm);
       }
     }
     if (lane == 0) {
       bulk_wait_all();
-      // (after an abort: loads still in flight land before shared memory is released)
-      for (int b = 0; b < FU_NBUF; ++b)
-        if ((in_flight >> b) & 1u)
-          mbar_wait_drain(in_bar(ew * FU_NBUF + b), (in_phase >> b) & 1u, p.timeout_ns);
+      // (after an abort: a load still in flight lands before shared memory is released)
+      if (in_flight) mbar_wait_drain(in_bar(ew), in_phase, p.timeout_ns);
     }
   }
 
@@ -717,16 +689,15 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
   auto aligned = [](const void* q, int64_t ld) { return ((uintptr_t)q & 15u) == 0 && ld % 8 == 0; };
   p.tma_y = aligned(a.Y, a.ldy) && (!inner || a.groups == 1 || a.stride_y % 8 == 0);
   p.tma_in = a.mode != FUSED_NONE && aligned(a.in, a.ld_in) && (!inner || p.tma_y);
-  p.tma_u = a.U && aligned(a.U, a.ldu);
+  p.vec_u = ((uintptr_t)a.U & 31u) == 0 && a.ldu % 16 == 0;
   p.part = a.part;
   p.status = ctx.status;
   p.timeout_ns = ctx.timeout_ns;
   p.fault_injection = a.fault_injection;
   constexpr CUtensorMapDataType TY = Elem<T>::TMA;
   const CUtensorMapSwizzle SW = CU_TENSOR_MAP_SWIZZLE_128B;
-  CUtensorMap mA, mB, mI, mU, mY;
+  CUtensorMap mA, mB, mI, mY;
   memset(&mI, 0, sizeof(mI));
-  memset(&mU, 0, sizeof(mU));
   memset(&mY, 0, sizeof(mY));
   // (a stride of 0: one matrix)
   const int64_t matrices = a.stride_b != 0 ? a.groups : 1;
@@ -743,21 +714,17 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
     memset(&mA, 0, sizeof(mA));
     memset(&mB, 0, sizeof(mB));
   }
-  if (inner) {
-    if (p.tma_y)
-      ok = ok && make_map(&mY, TY, a.Y, a.M, a.N, a.ldy, 64, 32, SW, a.groups, a.stride_y, 2);
-    mI = mY;  // (C_g itself)
-  } else {
-    if (p.tma_y) ok = ok && make_map(&mY, TY, a.Y, a.M, a.N, a.ldy, 64, 32);
-    if (p.tma_in) ok = ok && make_map(&mI, TY, a.in, a.M, a.N, a.ld_in, 64, 32);
-    if (p.tma_u) ok = ok && make_map(&mU, TY, a.U, a.M, a.N, a.ldu, 64, 32);
-  }
+  if (p.tma_y)
+    ok = ok && (inner ? make_map(&mY, TY, a.Y, a.M, a.N, a.ldy, 64, 32, SW, a.groups, a.stride_y, 2)
+                      : make_map(&mY, TY, a.Y, a.M, a.N, a.ldy, 64, 32));
+  if (inner) mI = mY;  // (C itself)
+  else if (p.tma_in) ok = ok && make_map(&mI, TY, a.in, a.M, a.N, a.ld_in, 64, 32);
   if (!ok) return cudaErrorNotSupported;
   const int slots = fused_slots<T, BN, A_MN, B_MN, PAIR>(a.num_sms);
   const int workers = (int)(most < slots ? most : slots);
   ctx.grid = PAIR ? 2 * workers : workers;
   const cudaError_t e = launch_kernel(kern, dim3(ctx.grid), dim3(FU_THREADS), C_::SMEM_BYTES,
-                                      ctx.stream, PAIR ? 2 : 1, mA, mB, mI, mU, mY, p);
+                                      ctx.stream, PAIR ? 2 : 1, mA, mB, mI, mY, p);
   if (e == cudaSuccess) ctx.launches++;
   return e;
 }
