@@ -89,7 +89,8 @@ F32_3XTF32 = 4
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_TIMEOUT = range(7)
 PATHS = {0: "none", 1: "scale", 2: "ffma", 3: "ffma_splitk", 4: "tc", 5: "tc_splitk",
          6: "ffma_batched", 7: "tc_batched", 8: "per_entry", 9: "mx", 10: "mx_tc",
-         11: "mx_stream", 12: "mx_convert", 13: "fused_tc", 14: "fused_ffma"}
+         11: "mx_stream", 12: "mx_convert", 13: "fused_tc", 14: "fused_ffma",
+         15: "fused_stream"}
 
 
 class GemmError(RuntimeError):

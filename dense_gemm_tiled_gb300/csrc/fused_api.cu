@@ -122,6 +122,7 @@ int run_call(Call& c, cudaStream_t stream) {
   if (rc != GEMM_OK) return rc;
   LaunchCtx ctx{stream, st.status, st.timeout_ns, 0};
   FusedArgs& a = c.a;
+  a.splits = 1;
   a.num_sms = st.sms;
   a.fault_injection = st.fault_injection;
   const bool inner = a.kind == FUSED_INNER, none = a.M == 0 && !inner;  // (no rows at all)
@@ -172,7 +173,13 @@ int run_call(Call& c, cudaStream_t stream) {
     const bool copy_b = a.K > 0 && (!aligned16(a.B, a.ldb) || (nb > 1 && a.stride_b % 8 != 0));
     const int64_t bytes_a = copy_a ? pad256(c.a_rows * ((c.a_cols + 7) / 8 * 8) * 2) : 0;
     const int64_t bytes_b = copy_b ? pad256(nb * c.b_rows * ((c.b_cols + 7) / 8 * 8) * 2) : 0;
-    e = ws.get((size_t)(part_bytes + bytes_a + bytes_b), stream);
+    const bool few = !inner && !a.transA && a.transB && a.M <= FUSED_FEW_ROWS &&
+                     a.mode != FUSED_SLOPE && !c.dbias;
+    a.splits = 1;
+    if (!few) fused_plan(a);
+    a.ldp = (a.N + 15) / 16 * 16;
+    const int64_t bytes_p = a.splits > 1 ? pad256((int64_t)a.splits * a.M * a.ldp * 4) : 0;
+    e = ws.get((size_t)(part_bytes + bytes_a + bytes_b + bytes_p), stream);
     if (e != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, e);
     char* at = static_cast<char*>(ws.ptr);
     a.part = part_bytes ? reinterpret_cast<float*>(at) : nullptr;
@@ -182,8 +189,14 @@ int run_call(Call& c, cudaStream_t stream) {
       if (copy_a) e = repack(a.A, a.lda, no_stride, c.a_rows, c.a_cols, 1, at + part_bytes, ctx);
       if (e == cudaSuccess && copy_b)
         e = repack(a.B, a.ldb, a.stride_b, c.b_rows, c.b_cols, nb, at + part_bytes + bytes_a, ctx);
-      a.tile = fused_pick(a);
-      if (e == cudaSuccess) e = launch_fused(a, ctx);
+      if (e == cudaSuccess && few) {
+        path = GEMM_PATH_FUSED_STREAM;
+        e = launch_fused_stream(a, ctx);
+      } else if (e == cudaSuccess) {
+        if (a.splits > 1) a.P = reinterpret_cast<float*>(at + part_bytes + bytes_a + bytes_b);
+        e = launch_fused(a, ctx);
+        if (e == cudaSuccess && a.splits > 1) e = launch_fused_finish(a, a.P, a.ldp, ctx);
+      }
     }
   }
   if (e == cudaSuccess && c.dbias) e = launch_fused_dbias(a, c.dbias, ctx);

@@ -1,10 +1,12 @@
-// What fused products do outside their main kernel: the epilogue of fp32 products
-// (bias, activation or its slope, residual, column sums, over raw sums in memory),
-// and the join of the column sums of either type.
+// What fused products do outside their main kernel: the epilogue over raw sums in
+// memory, and the join of the column sums.
 //
-// fp32 products spend 2 K / 72 ps a value on the CUDA cores (K = 2048: 57 ps); a pass
-// over the values in memory costs 2 to 4 ps, so it is not worth an epilogue of its
-// own in each of their five kernels.
+// The raw sums are fp32 products -- 2 K / 72 ps a value on the CUDA cores (K = 2048: 57
+// ps), where a pass over the values in memory costs 2 to 4 ps, so it is not worth an
+// epilogue of its own in each of their five kernels -- or the slices of K of a 16-bit
+// product with few tiles (512 x 2048 x 5632: four of 64 tiles instead of 64 for 152 SMs).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,30 +20,59 @@ namespace {
 struct FinishParams {
   int M, N, groups;
   const int* offsets;  // null: one group of all rows
-  const float* P;
+  const float* P;      // [splits][M][ldp]
   int64_t ldp;
+  int splits;
   float alpha, beta;
-  const float* bias;
+  const void* bias;
   int act, mode;
-  const float* in;
+  const void* in;
   int64_t ld_in;
-  float* U;
+  void* U;
   int64_t ldu;
-  float* Y;
+  void* Y;
   int64_t ldy;
   float* part;
-  int chunks;  // of 256 columns
+  int chunks;  // of 64 V columns
   int64_t units;
 };
 
-// A slot of 32 rows (group g's begin at o[g] / 32 + g) x 256 columns a block, a
-// column a thread.
-__global__ void __launch_bounds__(256) fused_finish_kernel(const FinishParams p) {
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+
+// V values of a row, V sizeof(T) bytes aligned
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+// A slot of 32 rows (group g's begin at o[g] / 32 + g) x 64 V columns a block: a thread
+// has V columns of four rows, and asks for those of all slices (up to S of them) at once.
+// V is 4 where every matrix has such rows, else 1.
+constexpr int FIN_THREADS = 512;
+template <typename T, int V, int S>
+__global__ void __launch_bounds__(FIN_THREADS) fused_finish_kernel(const FinishParams p) {
+  __shared__ float join[8][64 * V];
   pdl_wait();
   pdl_trigger();
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   for (int64_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
     const int slot = (int)(unit / p.chunks);
-    const int n = (int)(unit - (int64_t)slot * p.chunks) * 256 + (int)threadIdx.x;
+    const int n = ((int)(unit - (int64_t)slot * p.chunks) * 64 + tx) * V;
     int g = 0, lo = 0, len = p.M;
     if (p.offsets) {
       // the last group whose first slot is not past this one
@@ -57,41 +88,83 @@ __global__ void __launch_bounds__(256) fused_finish_kernel(const FinishParams p)
     }
     const int r0 = (slot - (lo >> 5) - g) * 32;
     const int rows = r0 < 0 ? 0 : min(32, len - r0);
-    if (rows <= 0 || n >= p.N) continue;
-    const int64_t m0 = (int64_t)lo + r0;
-    const float bias = p.bias ? __ldg(p.bias + (int64_t)g * p.N + n) : 0.f;
-    float sum = 0.f;
-#pragma unroll 1
-    for (int i0 = 0; i0 < rows; i0 += 8) {
-      float v[8], f[8];
+    if (rows <= 0) continue;  // (the whole block)
+    float sum[V];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in = i0 + i < rows;
-        v[i] = in ? p.P[(m0 + i0 + i) * p.ldp + n] : 0.f;
-        f[i] = in && p.mode != FUSED_NONE ? p.in[(m0 + i0 + i) * p.ld_in + n] : 0.f;
-      }
+    for (int j = 0; j < V; ++j) sum[j] = 0.f;
+    if (n < p.N) {
+      float bias[V];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = p.alpha * v[i] + bias;
-        if (p.U && i0 + i < rows) p.U[(m0 + i0 + i) * p.ldu + n] = v[i];
-      }
-      if (p.mode == FUSED_SLOPE) {
-        slope_of<float>(v, f, p.act);
-      } else {
-        act_of<float>(v, p.act);
-        if (p.mode == FUSED_ADD) {
+      for (int j = 0; j < V; ++j)
+        bias[j] = p.bias ? to_f(static_cast<const T*>(p.bias)[(int64_t)g * p.N + n + j]) : 0.f;
+      const int i0 = 4 * ty;
+      if (i0 < rows) {
+        float v[4 * V], f[4 * V];
+        Vec<float, V> x[S][4];
+        Vec<T, V> y[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(p.beta, f[i], v[i]);
+        for (int i = 0; i < 4; ++i) {
+          const int64_t m = (int64_t)lo + r0 + min(i0 + i, rows - 1);
+          if (p.mode != FUSED_NONE)
+            y[i] = *reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(p.in) + m * p.ld_in + n);
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+            if (s < p.splits)
+              x[s][i] = *reinterpret_cast<const Vec<float, V>*>(p.P + ((int64_t)s * p.M + m) * p.ldp + n);
         }
-      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i0 + i < rows) {
-          p.Y[(m0 + i0 + i) * p.ldy + n] = v[i];
-          sum += v[i];
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            v[i * V + j] = x[0][i].v[j];
+            f[i * V + j] = p.mode != FUSED_NONE ? to_f(y[i].v[j]) : 0.f;
+#pragma unroll
+            for (int s = 1; s < S; ++s)
+              if (s < p.splits) v[i * V + j] += x[s][i].v[j];
+          }
+        auto put = [&](void* to, int64_t ld) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i0 + i >= rows) continue;
+            Vec<T, V> o;
+#pragma unroll
+            for (int j = 0; j < V; ++j) o.v[j] = from_f<T>(v[i * V + j]);
+            *reinterpret_cast<Vec<T, V>*>(static_cast<T*>(to) + ((int64_t)lo + r0 + i0 + i) * ld + n) = o;
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) v[i] = p.alpha * v[i] + bias[i % V];
+        if (p.U) put(p.U, p.ldu);
+        if (p.mode == FUSED_SLOPE) {
+          slope_of<T>(v, f, p.act);
+        } else {
+          act_of<T>(v, p.act);
+          if (p.mode == FUSED_ADD) {
+#pragma unroll
+            for (int i = 0; i < 4 * V; ++i) v[i] = __fmaf_rn(p.beta, f[i], v[i]);
+          }
         }
+        put(p.Y, p.ldy);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) sum[j] += i0 + i < rows ? v[i * V + j] : 0.f;
+      }
     }
-    if (p.part) p.part[(int64_t)slot * p.N + n] = sum;
+    if (p.part) {
+      __syncthreads();  // (the last unit's sums are read)
+#pragma unroll
+      for (int j = 0; j < V; ++j) join[ty][tx * V + j] = sum[j];
+      __syncthreads();
+      const int at = (int)(unit - (int64_t)slot * p.chunks) * 64 * V + threadIdx.x;
+      if ((int)threadIdx.x < 64 * V && at < p.N)
+      {
+        float all = join[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) all += join[w][threadIdx.x];
+        p.part[(int64_t)slot * p.N + at] = all;
+      }
+    }
   }
 }
 
@@ -129,30 +202,47 @@ __global__ void __launch_bounds__(256) fused_dbias_kernel(const float* __restric
 
 }  // namespace
 
-cudaError_t launch_fused_finish(const FusedArgs& a, const float* P, int64_t ldp, LaunchCtx& ctx) {
+template <typename T>
+static cudaError_t launch_finish(const FusedArgs& a, const float* P, int64_t ldp, LaunchCtx& ctx) {
   FinishParams p;
   p.M = a.M; p.N = a.N;
   p.groups = a.groups;
   p.offsets = a.kind == FUSED_DENSE ? nullptr : a.offsets;
   p.P = P;
   p.ldp = ldp;
+  p.splits = a.splits;
   p.alpha = a.alpha; p.beta = a.beta;
-  p.bias = static_cast<const float*>(a.bias);
+  p.bias = a.bias;
   p.act = a.act; p.mode = a.mode;
-  p.in = static_cast<const float*>(a.in);
+  p.in = a.in;
   p.ld_in = a.ld_in;
-  p.U = static_cast<float*>(a.U);
+  p.U = a.U;
   p.ldu = a.ldu;
-  p.Y = static_cast<float*>(a.Y);
+  p.Y = a.Y;
   p.ldy = a.ldy;
   p.part = a.part;
-  p.chunks = (a.N + 255) / 256;
+  auto four = [](const void* q, int64_t ld, size_t e) {
+    return !q || (((uintptr_t)q % (4 * e)) == 0 && ld % 4 == 0);
+  };
+  const bool vec = a.N % 4 == 0 && four(P, ldp, 4) && four(a.Y, a.ldy, sizeof(T)) &&
+                   four(a.U, a.ldu, sizeof(T)) && (a.mode == FUSED_NONE || four(a.in, a.ld_in, sizeof(T)));
+  p.chunks = (a.N + (vec ? 255 : 63)) / (vec ? 256 : 64);
   p.units = (a.M / 32 + a.groups + 1) * (int64_t)p.chunks;
   const int64_t most = (int64_t)a.num_sms * 64;
-  const cudaError_t e = launch_kernel(fused_finish_kernel, dim3((unsigned)(p.units < most ? p.units : most)),
-                                      dim3(256), 0, ctx.stream, 1, p);
+  const dim3 grid((unsigned)(p.units < most ? p.units : most));
+  auto kern = vec ? (a.splits == 1 ? fused_finish_kernel<T, 4, 1> : fused_finish_kernel<T, 4, FUSED_MAX_SPLITS>)
+                  : (a.splits == 1 ? fused_finish_kernel<T, 1, 1> : fused_finish_kernel<T, 1, FUSED_MAX_SPLITS>);
+  const cudaError_t e = launch_kernel(kern, grid, dim3(FIN_THREADS), 0, ctx.stream, 1, p);
   if (e == cudaSuccess) ctx.launches++;
   return e;
+}
+
+cudaError_t launch_fused_finish(const FusedArgs& a, const float* P, int64_t ldp, LaunchCtx& ctx) {
+  switch (a.dtype) {
+    case 0: return launch_finish<float>(a, P, ldp, ctx);
+    case 1: return launch_finish<__half>(a, P, ldp, ctx);
+    default: return launch_finish<__nv_bfloat16>(a, P, ldp, ctx);
+  }
 }
 
 cudaError_t launch_fused_dbias(const FusedArgs& a, float* dbias, LaunchCtx& ctx) {

@@ -6,36 +6,56 @@
 
 namespace gb300 {
 
-int fused_pick(const FusedArgs& a) {
+void fused_plan(FusedArgs& a) {
+  // The tile and slices of K with the least estimated time, in ns: rounds of units over
+  // the GPU x (K steps x the bytes that a block's shared memory takes in for one, at 97
+  // bytes a ns -- what bounds the main loop whatever the tile: 256 x 256 pairs 0.33 us a
+  // step, 128 x 64 0.25 -- + a unit's start and epilogue), and with slices their sums'
+  // way through memory and a second kernel.  The host does not know the groups' sizes:
+  // rows spread evenly over groups.
+  const struct { int bm, bn, slots, fixed; } shape[FUSED_TILES] = {
+      {256, 256, a.num_sms / 2, 3500}, {128, 128, a.num_sms, 2500}, {128, 64, a.num_sms, 2000}};
   static const int forced = [] {
     const char* e = getenv("GEMM_GB300_FUSED_TILE");
     return e ? atoi(e) : -1;
   }();
-  if (forced >= 0 && forced < FUSED_TILES) return forced;
-  // The tile with the least estimated time: rounds of tiles over the GPU x (K steps x
-  // the bytes a block moves for one + a tile's start and epilogue, as bytes).  The
-  // host does not know the groups' sizes: rows spread evenly over groups.
-  const struct { int bm, bn, slots, kib, fixed; } shape[FUSED_TILES] = {
-      {256, 256, a.num_sms / 2, 40, 160}, {128, 128, a.num_sms, 32, 100}, {128, 64, a.num_sms, 24, 80}};
+  static const int forced_splits = [] {
+    const char* e = getenv("GEMM_GB300_FUSED_SPLITS");
+    return e ? atoi(e) : 0;
+  }();
   const bool rows = a.kind == FUSED_ROWS, inner = a.kind == FUSED_INNER;
   const int64_t live = rows ? (a.groups < a.M ? a.groups : a.M) : 1;
   const int64_t per = ((int64_t)a.M + live - 1) / live;
   const int64_t kk = inner ? ((int64_t)a.K + a.groups - 1) / a.groups : a.K;
   const int64_t steps = (kk + 63) / 64;
-  int best = 0;
+  const bool a_rows = !a.transA && !inner;
   double least = 0;
+  a.tile = -1;
+  a.splits = 1;
   for (int i = 0; i < FUSED_TILES; ++i) {
-    const int64_t tiles = live * ((per + shape[i].bm - 1) / shape[i].bm) *
-                          (((int64_t)a.N + shape[i].bn - 1) / shape[i].bn) *
+    if (forced >= 0 && forced < FUSED_TILES && i != forced) continue;
+    const int64_t tm = (per + shape[i].bm - 1) / shape[i].bm;
+    const int64_t tiles = live * tm * (((int64_t)a.N + shape[i].bn - 1) / shape[i].bn) *
                           (inner ? a.groups : 1);
-    const int64_t rounds = (tiles + shape[i].slots - 1) / shape[i].slots;
-    const double cost = (double)rounds * ((double)steps * shape[i].kib + shape[i].fixed);
-    if (i == 0 || cost < least) {
-      least = cost;
-      best = i;
+    // bytes of a step: rows of A in boxes of 32, B's columns (half of them a block of a pair)
+    const int64_t rows_in = a_rows && per < 128 ? (per + 31) / 32 * 32 : 128;
+    const double ns = (double)(rows_in + (i == FUSED_TILE_PAIR ? 128 : shape[i].bn)) * 128 / 97;
+    for (int s = 1; s <= FUSED_MAX_SPLITS; ++s) {
+      const int64_t each = (steps + s - 1) / s;
+      if (s > 1 && (a.kind != FUSED_DENSE || (s - 1) * each >= steps || each < 4)) continue;
+      if (forced_splits > 0 && a.kind == FUSED_DENSE && s != forced_splits && (s > 1 || steps >= 4 * forced_splits))
+        continue;
+      const int64_t rounds = (tiles * s + shape[i].slots - 1) / shape[i].slots;
+      double cost = (double)rounds * ((double)each * ns + shape[i].fixed);
+      if (s > 1) cost += 2500 + (double)a.M * a.N * 8 * s / 6000;
+      if (a.tile < 0 || cost < least) {
+        least = cost;
+        a.tile = i;
+        a.splits = s;
+      }
     }
   }
-  return best;
+  if (a.tile < 0) a.tile = forced >= 0 && forced < FUSED_TILES ? forced : FUSED_TILE_128;
 }
 
 cudaError_t launch_fused(const FusedArgs& a, LaunchCtx& ctx) {

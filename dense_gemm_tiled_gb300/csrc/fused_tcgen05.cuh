@@ -71,6 +71,11 @@ struct FuParams {
   int b_mask;          // 0: one matrix of B for all groups, else -1
   int tiles_m, tiles_n;
   int64_t tiles;       // (not FUSED_ROWS)
+  // slices of K (FUSED_DENSE): a unit is a tile's slice of k_slice columns, whose raw sums
+  // go to P [splits][M][ldp]; 1: none
+  int splits, k_slice;
+  float* P;
+  int64_t ldp;
   float alpha, beta;
   const void* bias;    // [groups][N], or null
   int bias_vec;        // its rows 16-byte aligned
@@ -94,7 +99,7 @@ struct FuParams {
 // the end of its rows, the tile's first column, its group, and the range of the
 // inner dimension.
 struct FuTile {
-  int m0, row_end, n0, g, g_lo, k_lo, k_len;
+  int m0, row_end, n0, g, g_lo, k_lo, k_len, slice;
 };
 
 // A worker's tiles, asked for in ascending order by every role of the block (whole
@@ -112,18 +117,25 @@ struct FuWalk {
     u.row_end = p.M;
     u.k_lo = 0;
     u.k_len = p.K;
+    u.slice = 0;
     if (p.kind == FUSED_ROWS) {
       int n;
       if (!rows.find(p.offsets, p.groups, p.M, p.tiles_n, t, lane, u.g, u.g_lo, n, loc)) return false;
       u.row_end = u.g_lo + n;
       rt = (n + BMT - 1) / BMT;
-    } else if (t >= p.tiles) {
+    } else if (t >= p.tiles * p.splits) {
       return false;
     } else if (p.kind == FUSED_INNER) {
       const int per = rt * p.tiles_n;
       u.g = (int)(t / per);
       loc = (int)(t - (int64_t)u.g * per);
       group_span(p.offsets, u.g, p.K, u.k_lo, u.k_len);
+    } else if (p.splits > 1) {
+      // (a tile's slices side by side)
+      loc = (int)(t / p.splits);
+      u.slice = (int)t - loc * p.splits;
+      u.k_lo = u.slice * p.k_slice;
+      u.k_len = min(p.K - u.k_lo, p.k_slice);
     }
     // bands of GROUP_M row tiles, column by column
     const int per_band = GROUP_M * p.tiles_n;
@@ -217,7 +229,8 @@ __device__ __forceinline__ void fu_rows_out(T* dst, int64_t ld, int rows, int co
 
 template <typename T, int BN, bool A_MN, bool B_MN, bool PAIR>
 __global__ void __launch_bounds__(FU_THREADS, 1)
-    fused_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    fused_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                    const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmI, const __grid_constant__ CUtensorMap tmY,
                     const FuParams p) {
   using C_ = FuCfg<BN, PAIR>;
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
           const uint32_t sb = sa + (uint32_t)A_TILE_BYTES;
           const int k0 = kb * BK;
           // operands stored by k: rows of groups from k_lo on (see above), or all rows
-          const int ky = p.kind == FUSED_INNER ? min(u.k_len - k0 - BK, 0) : k0;
+          const int ky = p.kind == FUSED_INNER ? min(u.k_len - k0 - BK, 0) : u.k_lo + k0;
           const int kz = p.kind == FUSED_INNER ? u.k_lo + k0 : 0;
           if (leader) {
             auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -320,11 +333,17 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
             // 64-column atoms past the last column are not loaded (what they would add
             // to is not stored)
             constexpr int ATOMS = BN / 64 / (PAIR ? 2 : 1);
+            // nor are rows of A past the group's last, 32 at a time (a box of 128 where
+            // there are more than 96)
+            auto a_boxes = [&](int from) { return min(max((u.row_end - from + 31) / 32, 0), 4); };
             if (rank == 0) {
               uint32_t bytes = STAGE_TX;
               if constexpr (A_MN) {
                 const int have = min(max((p.M - u.m0 + 63) / 64, 0), BMT / 64);
                 bytes -= (uint32_t)(BMT / 64 - have) * 8192u;
+              } else {
+                bytes -= (uint32_t)(4 - a_boxes(u.m0)) * 4096u;
+                if constexpr (PAIR) bytes -= (uint32_t)(4 - a_boxes(u.m0 + BM)) * 4096u;
               }
               if constexpr (B_MN) {
                 const int have = min((p.N - u.n0 + 63) / 64, BN / 64);
@@ -338,7 +357,11 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
                 if (u.m0 + 64 * h < p.M)
                   load(sa + (uint32_t)h * 8192u, &tmA, u.m0 + 64 * h, ky, kz, bar);
             } else {
-              load(sa, &tmA, k0, u.m0, 0, bar);
+              const int boxes = a_boxes(u.m0);
+              if (boxes == 4) load(sa, &tmA, u.k_lo + k0, u.m0, 0, bar);
+              else
+                for (int h = 0; h < boxes; ++h)
+                  load(sa + (uint32_t)h * 4096u, &tmA32, u.k_lo + k0, u.m0 + 32 * h, 0, bar);
             }
             if constexpr (B_MN) {
 #pragma unroll
@@ -349,7 +372,7 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
                        p.kind == FUSED_INNER ? kz : u.g & p.b_mask, bar);
               }
             } else {
-              load(sb, &tmB, k0, u.n0 + rank * (BN / 2), u.g & p.b_mask, bar);
+              load(sb, &tmB, u.k_lo + k0, u.n0 + rank * (BN / 2), u.g & p.b_mask, bar);
             }
           }
           pending |= 1u << stage;
@@ -521,6 +544,20 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
         }
         tmem_ld_wait();
         if (c == 3) release_acc(buf);
+        if (p.splits > 1) {
+          // raw sums of the slice: 64 bytes of this lane's row of P (whose rows are whole)
+          if (lane < rows && col < p.ldp) {
+            float* const d = p.P + ((int64_t)u.slice * p.M + gm + lane) * p.ldp + col;
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + e),
+                           "r"(r[e]), "r"(r[e + 1]), "r"(r[e + 2]), "r"(r[e + 3]), "r"(r[e + 4]),
+                           "r"(r[e + 5]), "r"(r[e + 6]), "r"(r[e + 7])
+                           : "memory");
+          }
+          __syncwarp();
+          continue;
+        }
         float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = p.alpha * __uint_as_float(r[e]);
@@ -603,6 +640,7 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
         }
         __syncwarp();  // (the tensor-memory loads are the warp's together)
       }
+      if (p.splits > 1) continue;
       // a box that the group's end cuts is stored row by row, as are rows off alignment
       if (!p.tma_y || (p.kind == FUSED_ROWS && rows < 32)) {
         fu_rows_out(static_cast<T*>(p.Y) + gy + (int64_t)gm * p.ldy + gn, p.ldy, rows, cols, p.tma_y,
@@ -678,17 +716,25 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
   const int64_t most = (int64_t)(p.tiles_m + (rows ? (a.groups < a.M ? a.groups : a.M) : 0)) *
                        p.tiles_n * (inner ? a.groups : 1);
   p.tiles = most;
+  // (slices of whole K steps, none of them empty: fused_plan)
+  p.splits = a.splits;
+  const int steps = (a.K + BK - 1) / BK;
+  p.k_slice = (steps + a.splits - 1) / a.splits * BK;
+  if (a.splits > 1 && (a.kind != FUSED_DENSE || !a.P || (int64_t)(a.splits - 1) * p.k_slice >= a.K))
+    return cudaErrorInvalidValue;
+  p.P = a.P;
+  p.ldp = a.ldp;
   p.alpha = a.alpha; p.beta = a.beta;
   p.bias = a.bias;
   p.bias_vec = ((uintptr_t)a.bias & 15u) == 0 && a.N % 8 == 0;
   p.act = a.act;
-  p.mode = a.mode;
+  p.mode = a.splits > 1 ? FUSED_NONE : a.mode;
   p.in = a.in; p.ld_in = a.ld_in;
   p.U = a.U; p.ldu = a.ldu;
   p.Y = a.Y; p.ldy = a.ldy; p.stride_y = inner ? a.stride_y : 0;
   auto aligned = [](const void* q, int64_t ld) { return ((uintptr_t)q & 15u) == 0 && ld % 8 == 0; };
   p.tma_y = aligned(a.Y, a.ldy) && (!inner || a.groups == 1 || a.stride_y % 8 == 0);
-  p.tma_in = a.mode != FUSED_NONE && aligned(a.in, a.ld_in) && (!inner || p.tma_y);
+  p.tma_in = p.mode != FUSED_NONE && aligned(a.in, a.ld_in) && (!inner || p.tma_y);
   p.vec_u = ((uintptr_t)a.U & 31u) == 0 && a.ldu % 16 == 0;
   p.part = a.part;
   p.status = ctx.status;
@@ -696,7 +742,8 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
   p.fault_injection = a.fault_injection;
   constexpr CUtensorMapDataType TY = Elem<T>::TMA;
   const CUtensorMapSwizzle SW = CU_TENSOR_MAP_SWIZZLE_128B;
-  CUtensorMap mA, mB, mI, mY;
+  CUtensorMap mA, mA32, mB, mI, mY;
+  memset(&mA32, 0, sizeof(mA32));
   memset(&mI, 0, sizeof(mI));
   memset(&mY, 0, sizeof(mY));
   // (a stride of 0: one matrix)
@@ -706,7 +753,9 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
   if (a.K > 0) {
     if (inner) ok = rows_map(&mA, TY, a.A, a.K, a.M, a.lda) && rows_map(&mB, TY, a.B, a.K, a.N, a.ldb);
     else {
-      ok = A_MN ? make_map(&mA, TY, a.A, a.K, a.M, a.lda, 64, 64) : make_map(&mA, TY, a.A, a.M, a.K, a.lda, 64, BM);
+      if (A_MN) ok = make_map(&mA, TY, a.A, a.K, a.M, a.lda, 64, 64);
+      else ok = make_map(&mA, TY, a.A, a.M, a.K, a.lda, 64, BM) &&
+                make_map(&mA32, TY, a.A, a.M, a.K, a.lda, 64, 32);
       if (B_MN) ok = ok && make_map(&mB, TY, a.B, a.K, a.N, a.ldb, 64, 64, SW, matrices, a.stride_b, 2);
       else ok = ok && make_map(&mB, TY, a.B, a.N, a.K, a.ldb, 64, PAIR ? BN / 2 : BN, SW, matrices, a.stride_b, 2);
     }
@@ -721,10 +770,11 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
   else if (p.tma_in) ok = ok && make_map(&mI, TY, a.in, a.M, a.N, a.ld_in, 64, 32);
   if (!ok) return cudaErrorNotSupported;
   const int slots = fused_slots<T, BN, A_MN, B_MN, PAIR>(a.num_sms);
-  const int workers = (int)(most < slots ? most : slots);
+  const int64_t units = most * a.splits;
+  const int workers = (int)(units < slots ? units : slots);
   ctx.grid = PAIR ? 2 * workers : workers;
   const cudaError_t e = launch_kernel(kern, dim3(ctx.grid), dim3(FU_THREADS), C_::SMEM_BYTES,
-                                      ctx.stream, PAIR ? 2 : 1, mA, mB, mI, mY, p);
+                                      ctx.stream, PAIR ? 2 : 1, mA, mA32, mB, mI, mY, p);
   if (e == cudaSuccess) ctx.launches++;
   return e;
 }

@@ -334,6 +334,7 @@ cudaError_t launch_mx4(const Mx4Args& a, LaunchCtx& ctx);
 enum { FUSED_DENSE = 0, FUSED_ROWS = 1, FUSED_INNER = 2 };  // one matrix, groups of rows, groups of K
 enum { FUSED_NONE = 0, FUSED_ADD = 1, FUSED_SLOPE = 2 };    // what the epilogue's input is: none, R, U
 enum { FUSED_TILE_PAIR, FUSED_TILE_128, FUSED_TILE_64, FUSED_TILES };
+constexpr int FUSED_MAX_SPLITS = 4;
 struct FusedArgs {
   int kind, dtype;     // dtype: 0 fp32, 1 fp16, 2 bf16
   int transA, transB;
@@ -357,23 +358,35 @@ struct FusedArgs {
   float* part;         // fused_part_floats() floats for the column sums, or null
   int num_sms;
   int fault_injection;
-  int tile;            // FUSED_TILE_* (16-bit types)
+  // 16-bit types, from fused_plan(): FUSED_TILE_*; slices of K whose raw sums go to P
+  // [splits][M][ldp] (FUSED_DENSE), or 1
+  int tile, splits;
+  float* P;
+  int64_t ldp;
 };
 // Column sums come in slots of 32 rows: group g's begin at o[g] / 32 + g.
 inline int64_t fused_part_floats(int64_t rows, int64_t groups, int64_t N) {
   return (rows / 32 + groups + 1) * N;
 }
-int fused_pick(const FusedArgs& a);  // the tile
+void fused_plan(FusedArgs& a);  // its tile and slices
 // 16-bit operands with 16-byte aligned rows (A, B) on the tensor cores;
 // cudaErrorNotSupported (nothing launched) where a tensor map does not take them
 cudaError_t launch_fused(const FusedArgs& a, LaunchCtx& ctx);
 cudaError_t launch_fused_bf16(const FusedArgs& a, LaunchCtx& ctx);
+// forward products of up to FUSED_FEW_ROWS rows in all (operands as above, B stored by
+// rows of K): every matrix whose group has rows read once.  In a graph, us, against the
+// tensor-core kernel: 5632 x 2048 8 rows 9.3 / 14.6, 16 rows 10.8 / 14.4, 32 rows 14.7 /
+// 14.0; 8192 x 8192 16 rows 31.9 / 37.6, 32 rows 41.5 / 37.6; 1408 x 2048 of 64 groups, 16
+// rows in 16 of them 19.8 / 31.1, 32 rows in 24 31.1 / 29.6.
+constexpr int FUSED_FEW_ROWS = 16;
+cudaError_t launch_fused_stream(const FusedArgs& a, LaunchCtx& ctx);
 // dbias[g][j] = the sum of group g's slots of `part`
 cudaError_t launch_fused_dbias(const FusedArgs& a, float* dbias, LaunchCtx& ctx);
 // fp32: the raw products of a grouped call into P (FUSED_ROWS, pitch ldp), or C
 // itself (FUSED_INNER)
 cudaError_t launch_sgemm_grouped(const FusedArgs& a, float* P, int64_t ldp, LaunchCtx& ctx);
-// fp32: the epilogue of the raw products P (rows of the groups only); P may be Y or U
+// the epilogue of the raw products P, `splits` of them to be added up (rows of the
+// groups only); of one in fp32, P may be Y or U
 cudaError_t launch_fused_finish(const FusedArgs& a, const float* P, int64_t ldp, LaunchCtx& ctx);
 
 // What the entry points of every translation unit share (gemm_api.cu).

@@ -467,7 +467,8 @@ typedef enum {
     GEMM_PATH_MX_CONVERT = 12, /* 16-bit rows times a stored right operand, converted inside
                                   the tcgen05 kernel */
     GEMM_PATH_FUSED_TC = 13,   /* fused or grouped product: its tcgen05 kernel */
-    GEMM_PATH_FUSED_FFMA = 14  /* the same in fp32: FFMA kernels, then the epilogue */
+    GEMM_PATH_FUSED_FFMA = 14, /* the same in fp32: FFMA kernels, then the epilogue */
+    GEMM_PATH_FUSED_STREAM = 15 /* the same of a few rows, B read once by warp MMAs */
 } gemm_path_t;
 
 int gemm_last_path(void);

@@ -54,6 +54,7 @@ SHAPES = [
     (1, 1, 1), (1, 5632, 2048), (3, 40, 8), (17, 33, 65), (32, 64, 64), (33, 65, 63),
     (128, 128, 128), (129, 257, 192), (200, 304, 136), (255, 64, 1024), (300, 513, 70),
     (512, 520, 333), (1000, 200, 48),
+    (17, 72, 4104), (130, 264, 4100), (300, 1030, 2056), (512, 2048, 1030),
 ]
 
 
@@ -493,6 +494,22 @@ def test_wait_that_runs_out(g):
     for e, (lo, hi) in enumerate([(0, 130), (130, 300)]):
         _, _, y, ey = ref.forward(f64(A[lo:hi]), f64(W[e]), "bf16")
         ref.check(Y[lo:hi], y, ey)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("sizes,ahead,behind", [
+    ([1], 0, 0), ([8], 0, 0), ([9], 0, 0), ([16], 0, 0), ([0, 1, 0], 0, 0), ([2, 0, 0, 7, 1], 1, 2),
+    ([1] * 16, 0, 0), ([0] * 33 + [5] + [0] * 40 + [9], 2, 0), ([0, 0], 0, 4),
+    ([9] + [1] * 7 + [0] * 40, 0, 0)])
+@pytest.mark.parametrize("N,K", [(1, 1), (7, 8), (40, 65), (72, 512), (130, 520), (64, 1000),
+                                 (1408, 2048), (24, 5000)])
+def test_few_rows(g, sizes, ahead, behind, N, K, dtype):
+    """Up to 16 rows in all: the streaming kernel, every depth of its copies."""
+    for act, bias, res, pre in (("gelu", True, True, True), ("none", False, False, False)):
+        grouped_call(g, sizes, ahead, behind, N, K, dtype, True, act, bias, res, pre, N + K)
+        assert g.last_path() == "fused_stream"
+    grouped_call(g, sizes, ahead, behind, N, K, dtype, True, "relu", True, True, False, 3, 8, 8)
+    grouped_call(g, sizes, ahead, behind, N, K, dtype, True, "relu", True, True, False, 3, 3, 1)
 
 
 # ------------------------------------------------------------------ an expert's MLP
