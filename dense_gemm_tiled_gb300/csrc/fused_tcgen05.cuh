@@ -27,13 +27,11 @@
 //    at (x, n - 64, r): it ends with those n rows, in both operands alike, and what
 //    lies ahead of them is out of range and reads as zero.  One map bounds every
 //    group, with nothing masked in shared memory.
-//  * Sixteen epilogue warps, a box of 32 rows x 64 columns of the tile each: what they
-//    do to a value is a chain of dependent instructions (a gelu or its slope, a
-//    rounding), and four warps a scheduler hide its latency where two did not
-//    (wgrad of 4000 rows of 8 groups 102 -> 92 us).  R or U comes by TMA, ahead of the
-//    accumulator, into the staging buffer that the result then leaves from; column
-//    sums are taken from registers, 32 rows at a time, by a transposing shuffle
-//    reduction, and joined by fused_dbias_kernel in the order of the rows.
+//  * Eight or sixteen epilogue warps (see fu_threads) work on boxes of 32 rows x 64
+//    columns.  R or U comes by TMA, ahead of the accumulator, into the staging buffer
+//    that the result then leaves from; column sums are taken from registers, 32 rows at
+//    a time, by a transposing shuffle reduction, and joined by fused_dbias_kernel in the
+//    order of the rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -47,12 +45,17 @@
 namespace gb300 {
 namespace {
 
-constexpr int FU_EPI = 16;     // epilogue warps
-constexpr int FU_THREADS = 64 + 32 * FU_EPI;
+// W: epilogue warps.  Their boxes' steps are chains of dependent instructions, so what a
+// tile's epilogue costs goes by warps and by registers, which let the steps of several
+// values run side by side: 256 x 256 pairs take sixteen warps of 96 registers, but eight
+// of 168 for the slope of an activation (us, eight / sixteen: 16384 x 5632 x 2048
+// backward 250 / 271, 32768 rows of 64 groups backward 193 / 203; 4000 rows of 8 groups
+// forward 85.6 / 82.7, their weights' gradients 103 / 93).
+constexpr int fu_threads(int W) { return 64 + 32 * W; }
 
 template <int BN, bool PAIR>
 struct FuCfg {
-  static constexpr int SHARES = BN / 64;  // epilogue warps in use per lane quarter
+  static constexpr int SHARES = BN / 64;  // boxes of a tile's 32 rows
   static constexpr int B_BYTES = (PAIR ? BN / 2 : BN) * 128;
   static constexpr int STAGE_BYTES = A_TILE_BYTES + B_BYTES;
   static constexpr int STAGING_BYTES = 4 * SHARES * 4096;
@@ -126,13 +129,13 @@ struct FuWalk {
     } else if (t >= p.tiles * p.splits) {
       return false;
     } else if (p.kind == FUSED_INNER) {
-      const int per = rt * p.tiles_n;
-      u.g = (int)(t / per);
-      loc = (int)(t - (int64_t)u.g * per);
+      const unsigned int per = (unsigned int)rt * (unsigned int)p.tiles_n;
+      u.g = (int)((unsigned int)t / per);
+      loc = (int)((unsigned int)t - (unsigned int)u.g * per);
       group_span(p.offsets, u.g, p.K, u.k_lo, u.k_len);
     } else if (p.splits > 1) {
       // (a tile's slices side by side)
-      loc = (int)(t / p.splits);
+      loc = (int)t / p.splits;
       u.slice = (int)t - loc * p.splits;
       u.k_lo = u.slice * p.k_slice;
       u.k_len = min(p.K - u.k_lo, p.k_slice);
@@ -227,8 +230,8 @@ __device__ __forceinline__ void fu_rows_out(T* dst, int64_t ld, int rows, int co
     }
 }
 
-template <typename T, int BN, bool A_MN, bool B_MN, bool PAIR>
-__global__ void __launch_bounds__(FU_THREADS, 1)
+template <typename T, int BN, bool A_MN, bool B_MN, bool PAIR, int W>
+__global__ void __launch_bounds__(fu_threads(W), 1)
     fused_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                     const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmI, const __grid_constant__ CUtensorMap tmY,
@@ -237,6 +240,8 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
   using E = Elem<T>;
   constexpr int STAGES = C_::STAGES;
   constexpr int BMT = PAIR ? 2 * BM : BM;
+  // warps of a lane quarter with boxes: box b is warp b % BOX_WARPS's
+  constexpr int BOX_WARPS = W / 4 < C_::SHARES ? W / 4 : C_::SHARES;
   constexpr uint32_t STAGE_TX = (uint32_t)C_::STAGE_BYTES * (PAIR ? 2u : 1u);
   const int rank = PAIR ? (int)cluster_ctarank() : 0;
   const int worker = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), (PAIR ? 2 : 1) * 32 * 4 * C_::SHARES);
+      mbar_init(acce_bar(b), (PAIR ? 2 : 1) * 32 * 4 * BOX_WARPS);
     }
     mbar_init(drain_bar, 1);
     for (int w = 0; w < 4 * C_::SHARES; ++w) mbar_init(in_bar(w), 1);
@@ -453,212 +458,226 @@ __global__ void __launch_bounds__(FU_THREADS, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // tensor-memory lanes 32q .. 32q + 31
     const int ew = warp - 2;
-    const int share = ew / 4;  // its 64 columns of the tile
-    const uint32_t sbuf = staging_addr + (uint32_t)(ew * 4096);
+    const int hh = ew / 4;    // of the warps of its quarter
     auto release_acc = [&](int buf) {
       tc_fence_before();
       if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(acce_bar(buf), 0u));
       else mbar_arrive(acce_bar(buf));
     };
-    uint32_t in_phase = 0;
-    bool in_flight = false;  // (lane 0)
+    uint32_t in_phase = 0, in_flight = 0;  // loads of `in` by box: parity, under way (lane 0)
     int it = 0;
-    for (int64_t t = worker; share < C_::SHARES && walk.find(p, t, rank, lane, u); t += workers, ++it) {
+    for (int64_t t = worker; hh < BOX_WARPS && walk.find(p, t, rank, lane, u); t += workers, ++it) {
       const int buf = it & 1;
-      const int gm = u.m0 + q * 32, gn = u.n0 + 64 * share;  // the warp's box
-      const int rows = min(max(u.row_end - gm, 0), 32), cols = min(p.N - gn, 64);
-      const bool work = rows > 0 && cols > 0;
+      const int gm = u.m0 + q * 32;  // the warp's rows
+      const int rows = min(max(u.row_end - gm, 0), 32);
+      // boxes of the tile with something in them
+      const int boxes = rows > 0 ? min((p.N - u.n0 + 63) / 64, C_::SHARES) : 0;
       const int64_t gy = p.kind == FUSED_INNER ? (int64_t)u.g * p.stride_y : 0;
-      // R, U or C: the box into the staging buffer, once the last store has read that;
-      // rows off alignment by their lanes instead, sixteen columns ahead
-      const bool in_box = work && p.mode != FUSED_NONE && p.tma_in;
-      const bool in_lanes = work && p.mode != FUSED_NONE && !p.tma_in;
-      if (in_box && lane == 0) {
+      auto sbuf_of = [&](int b) { return staging_addr + (uint32_t)((4 * b + q) * 4096); };
+      // R, U or C: the boxes into their staging buffers, once the last stores have read
+      // those; rows off alignment by their lanes instead, sixteen columns ahead
+      const bool in_box = p.mode != FUSED_NONE && p.tma_in;
+      const bool in_lanes = p.mode != FUSED_NONE && !p.tma_in;
+      if (in_box && lane == 0 && hh < boxes) {
         bulk_wait_read<0>();
-        mbar_arrive_expect_tx(in_bar(ew), 4096u);
-        tma_load_3d(sbuf, &tmI, gn, gm, p.kind == FUSED_INNER ? u.g : 0, in_bar(ew));
-        in_flight = true;
-      }
-      uint32_t ahead[8];
-      const uint16_t* const src = reinterpret_cast<const uint16_t*>(
-          static_cast<const T*>(p.in) + gy + (int64_t)(gm + lane) * p.ld_in + gn);
-      auto read_in = [&](int c) {
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const int at = 16 * c + e;
-          const uint32_t lo = lane < rows && at < cols ? src[at] : 0u;
-          const uint32_t hi = lane < rows && at + 1 < cols ? src[at + 1] : 0u;
-          ahead[e / 2] = lo | hi << 16;
+        for (int b = hh; b < boxes; b += BOX_WARPS) {
+          mbar_arrive_expect_tx(in_bar(4 * b + q), 4096u);
+          tma_load_3d(sbuf_of(b), &tmI, u.n0 + 64 * b, gm, p.kind == FUSED_INNER ? u.g : 0,
+                      in_bar(4 * b + q));
+          in_flight |= 1u << b;
         }
-      };
-      if (in_lanes) read_in(0);
+      }
       bool got = false;
       if (lane == 0) got = mbar_wait(accf_bar(buf), (uint32_t)(it >> 1) & 1u, wc);
       got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
       if (!got) break;
       tc_fence_after();
-      if (!work) {
+      if (hh >= boxes) {
         release_acc(buf);
         continue;
       }
-      const uint32_t t_row =
-          tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + 64 * share);
-      got = true;
-      if (lane == 0) {
-        if (in_box) {
-          got = mbar_wait(in_bar(ew), in_phase, wc);
-          if (got) {
-            in_phase ^= 1u;
-            in_flight = false;
-          }
-        } else {
-          bulk_wait_read<0>();  // the last store has read the buffer
-        }
-      }
-      got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
-      if (!got) break;
-      // Sixteen columns at a time.  (Not unrolled: the code that one call takes of all
-      // that is here then stays in the instruction cache; unrolled over 64 columns,
-      // steps that a call does not take slowed it as well: wgrad of 4000 rows of 8
-      // groups 140 us, 117 without the slope's code in the kernel.)
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const int col = gn + 16 * c;
-        uint32_t r[16];
-        tmem_ld_32x32b_x16(t_row + (uint32_t)(16 * c), r);
-        const uint32_t at[2] = {sbuf + (uint32_t)(lane * 128 + (((2 * c) ^ (lane & 7)) * 16)),
-                                sbuf + (uint32_t)(lane * 128 + (((2 * c + 1) ^ (lane & 7)) * 16))};
-        uint32_t now[8];
-        if (in_box) {
+      for (int b = hh; b < boxes; b += BOX_WARPS) {
+        const uint32_t sbuf = sbuf_of(b);
+        const int gn = u.n0 + 64 * b, cols = min(p.N - gn, 64);
+        const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + 64 * b);
+        uint32_t ahead[8];
+        const uint16_t* const src = reinterpret_cast<const uint16_t*>(
+            static_cast<const T*>(p.in) + gy + (int64_t)(gm + lane) * p.ld_in + gn);
+        auto read_in = [&](int c) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(now[4 * w]), "=r"(now[4 * w + 1]), "=r"(now[4 * w + 2]),
-                           "=r"(now[4 * w + 3])
-                         : "r"(at[w])
-                         : "memory");
-        } else if (in_lanes) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) now[e] = ahead[e];
-          if (c < 3) read_in(c + 1);
-        }
-        tmem_ld_wait();
-        if (c == 3) release_acc(buf);
-        if (p.splits > 1) {
-          // raw sums of the slice: 64 bytes of this lane's row of P (whose rows are whole)
-          if (lane < rows && col < p.ldp) {
-            float* const d = p.P + ((int64_t)u.slice * p.M + gm + lane) * p.ldp + col;
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + e),
-                           "r"(r[e]), "r"(r[e + 1]), "r"(r[e + 2]), "r"(r[e + 3]), "r"(r[e + 4]),
-                           "r"(r[e + 5]), "r"(r[e + 6]), "r"(r[e + 7])
-                           : "memory");
+          for (int e = 0; e < 16; e += 2) {
+            const int at = 16 * c + e;
+            const uint32_t lo = lane < rows && at < cols ? src[at] : 0u;
+            const uint32_t hi = lane < rows && at + 1 < cols ? src[at + 1] : 0u;
+            ahead[e / 2] = lo | hi << 16;
           }
-          __syncwarp();
-          continue;
-        }
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = p.alpha * __uint_as_float(r[e]);
-        if (u.k_len == 0) {  // (no product was added up)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0.f;
-        }
-        if (p.bias) {
-          const T* b = static_cast<const T*>(p.bias) + (int64_t)u.g * p.N + col;
-          if (p.bias_vec && col + 15 < p.N) {
-            uint4 bv[2] = {__ldg(reinterpret_cast<const uint4*>(b)),
-                           __ldg(reinterpret_cast<const uint4*>(b) + 1)};
-            const typename E::T2* b2 = reinterpret_cast<const typename E::T2*>(bv);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 f = E::unpack(b2[e]);
-              v[2 * e] += f.x;
-              v[2 * e + 1] += f.y;
+        };
+        if (in_lanes) read_in(0);
+        got = true;
+        if (lane == 0) {
+          if (in_box) {
+            got = mbar_wait(in_bar(4 * b + q), (in_phase >> b) & 1u, wc);
+            if (got) {
+              in_phase ^= 1u << b;
+              in_flight &= ~(1u << b);
             }
           } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (col + e < p.N) v[e] += E::to(b[e]);
+            bulk_wait_read<0>();  // the last store has read the buffer
           }
         }
-        auto pack = [&](uint4 (&o)[2]) {
-          typename E::T2* oh = reinterpret_cast<typename E::T2*>(o);
+        got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+        if (!got) break;
+        // Sixteen columns at a time.  (Not unrolled: the code that one call takes of all
+        // that is here then stays in the instruction cache; unrolled over 64 columns,
+        // steps that a call does not take slowed it as well: wgrad of 4000 rows of 8
+        // groups 140 us, 117 without the slope's code in the kernel.)
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = gn + 16 * c;
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(t_row + (uint32_t)(16 * c), r);
+          const uint32_t at[2] = {sbuf + (uint32_t)(lane * 128 + (((2 * c) ^ (lane & 7)) * 16)),
+                                  sbuf + (uint32_t)(lane * 128 + (((2 * c + 1) ^ (lane & 7)) * 16))};
+          uint32_t now[8];
+          if (in_box) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) oh[e] = E::pack(v[2 * e], v[2 * e + 1]);
-        };
-        if (p.U && lane < rows) {
-          uint4 o[2];
-          pack(o);
-          T* const dst = static_cast<T*>(p.U) + (int64_t)(gm + lane) * p.ldu + col;
-          if (p.vec_u && col + 15 < p.N) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
-                         "r"(o[0].x), "r"(o[0].y), "r"(o[0].z), "r"(o[0].w), "r"(o[1].x), "r"(o[1].y),
-                         "r"(o[1].z), "r"(o[1].w)
-                         : "memory");
-          } else {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(o);
+            for (int w = 0; w < 2; ++w)
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(now[4 * w]), "=r"(now[4 * w + 1]), "=r"(now[4 * w + 2]),
+                             "=r"(now[4 * w + 3])
+                           : "r"(at[w])
+                           : "memory");
+          } else if (in_lanes) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (col + e < p.N)
-                reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            for (int e = 0; e < 8; ++e) now[e] = ahead[e];
+            if (c < 3) read_in(c + 1);
           }
-        }
-        if (p.mode != FUSED_SLOPE) act_of<T>(v, p.act);
-        if (p.mode != FUSED_NONE) {
-          const typename E::T2* c2 = reinterpret_cast<const typename E::T2*>(now);
-          float f[16];
+          tmem_ld_wait();
+          if (c == 3 && b + BOX_WARPS >= boxes) release_acc(buf);
+          if (p.splits > 1) {
+            // raw sums of the slice: 64 bytes of this lane's row of P (whose rows are whole)
+            if (lane < rows && col < p.ldp) {
+              float* const d = p.P + ((int64_t)u.slice * p.M + gm + lane) * p.ldp + col;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 x = E::unpack(c2[e]);
-            f[2 * e] = x.x;
-            f[2 * e + 1] = x.y;
+              for (int e = 0; e < 16; e += 8)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + e),
+                             "r"(r[e]), "r"(r[e + 1]), "r"(r[e + 2]), "r"(r[e + 3]), "r"(r[e + 4]),
+                             "r"(r[e + 5]), "r"(r[e + 6]), "r"(r[e + 7])
+                             : "memory");
+            }
+            __syncwarp();
+            continue;
           }
-          if (p.mode == FUSED_SLOPE) {
-            slope_of<T>(v, f, p.act);
-          } else {
+          float v[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __fmaf_rn(p.beta, f[e], v[e]);
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
+          if (p.alpha != 1.f) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= p.alpha;
           }
-        }
-        uint4 o[2];
-        pack(o);
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at[w]), "r"(o[w].x),
-                       "r"(o[w].y), "r"(o[w].z), "r"(o[w].w)
-                       : "memory");
-        if (p.part) {
-          if (lane >= rows) {
+          if (u.k_len == 0) {  // (no product was added up)
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = 0.f;
           }
-          const float sum = warp_column_sum(v, lane);
-          const int64_t slot = (int64_t)(u.g_lo >> 5) + u.g + ((gm - u.g_lo) >> 5);
-          if ((lane & 1) == 0 && col + (lane >> 1) < p.N) p.part[slot * p.N + col + (lane >> 1)] = sum;
+          if (p.bias) {
+            const T* b = static_cast<const T*>(p.bias) + (int64_t)u.g * p.N + col;
+            if (p.bias_vec && col + 15 < p.N) {
+              uint4 bv[2] = {__ldg(reinterpret_cast<const uint4*>(b)),
+                             __ldg(reinterpret_cast<const uint4*>(b) + 1)};
+              const typename E::T2* b2 = reinterpret_cast<const typename E::T2*>(bv);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 f = E::unpack(b2[e]);
+                v[2 * e] += f.x;
+                v[2 * e + 1] += f.y;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (col + e < p.N) v[e] += E::to(b[e]);
+            }
+          }
+          auto pack = [&](uint4 (&o)[2]) {
+            typename E::T2* oh = reinterpret_cast<typename E::T2*>(o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) oh[e] = E::pack(v[2 * e], v[2 * e + 1]);
+          };
+          if (p.U && lane < rows) {
+            uint4 o[2];
+            pack(o);
+            T* const dst = static_cast<T*>(p.U) + (int64_t)(gm + lane) * p.ldu + col;
+            if (p.vec_u && col + 15 < p.N) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+                           "r"(o[0].x), "r"(o[0].y), "r"(o[0].z), "r"(o[0].w), "r"(o[1].x), "r"(o[1].y),
+                           "r"(o[1].z), "r"(o[1].w)
+                           : "memory");
+            } else {
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (col + e < p.N)
+                  reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
+          }
+          if (p.mode != FUSED_SLOPE) act_of<T>(v, p.act);
+          if (p.mode != FUSED_NONE) {
+            const typename E::T2* c2 = reinterpret_cast<const typename E::T2*>(now);
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 x = E::unpack(c2[e]);
+              f[2 * e] = x.x;
+              f[2 * e + 1] = x.y;
+            }
+            if (p.mode == FUSED_SLOPE) {
+              slope_of<T>(v, f, p.act);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __fmaf_rn(p.beta, f[e], v[e]);
+            }
+          }
+          uint4 o[2];
+          pack(o);
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at[w]), "r"(o[w].x),
+                         "r"(o[w].y), "r"(o[w].z), "r"(o[w].w)
+                         : "memory");
+          if (p.part) {
+            if (lane >= rows) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = 0.f;
+            }
+            const float sum = warp_column_sum(v, lane);
+            const int64_t slot = (int64_t)(u.g_lo >> 5) + u.g + ((gm - u.g_lo) >> 5);
+            if ((lane & 1) == 0 && col + (lane >> 1) < p.N) p.part[slot * p.N + col + (lane >> 1)] = sum;
+          }
+          __syncwarp();  // (the tensor-memory loads are the warp's together)
         }
-        __syncwarp();  // (the tensor-memory loads are the warp's together)
-      }
-      if (p.splits > 1) continue;
-      // a box that the group's end cuts is stored row by row, as are rows off alignment
-      if (!p.tma_y || (p.kind == FUSED_ROWS && rows < 32)) {
-        fu_rows_out(static_cast<T*>(p.Y) + gy + (int64_t)gm * p.ldy + gn, p.ldy, rows, cols, p.tma_y,
-                    sbuf, lane);
-        __syncwarp();
-      } else {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tmY, gn, gm, p.kind == FUSED_INNER ? u.g : 0, sbuf);
-          bulk_commit();
+        if (p.splits > 1) continue;
+        // a box that the group's end cuts is stored row by row, as are rows off alignment
+        if (!p.tma_y || (p.kind == FUSED_ROWS && rows < 32)) {
+          fu_rows_out(static_cast<T*>(p.Y) + gy + (int64_t)gm * p.ldy + gn, p.ldy, rows, cols, p.tma_y,
+                      sbuf, lane);
+          __syncwarp();
+        } else {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmY, gn, gm, p.kind == FUSED_INNER ? u.g : 0, sbuf);
+            bulk_commit();
+          }
         }
       }
+      if (!got) break;
     }
     if (lane == 0) {
       bulk_wait_all();
       // (after an abort: a load still in flight lands before shared memory is released)
-      if (in_flight) mbar_wait_drain(in_bar(ew), in_phase, p.timeout_ns);
+      for (int b = 0; b < C_::SHARES; ++b)
+        if ((in_flight >> b) & 1u)
+          mbar_wait_drain(in_bar(4 * b + q), (in_phase >> b) & 1u, p.timeout_ns);
     }
   }
 
@@ -683,22 +702,22 @@ bool rows_map(CUtensorMap* m, CUtensorMapDataType type, const void* p, int64_t r
 }
 
 // Pairs resident at once (fewer than half the SMs where a GPC's do not all pair up)
-template <typename T, int BN, bool A_MN, bool B_MN, bool PAIR>
+template <typename T, int BN, bool A_MN, bool B_MN, bool PAIR, int W>
 int fused_slots(int num_sms) {
   if (!PAIR) return num_sms;
   static CountPerDevice slots;
   const int n = slots.get(call_device(), [num_sms] {
-    return resident_clusters((const void*)fused_tc_kernel<T, BN, A_MN, B_MN, PAIR>, 2, FU_THREADS,
+    return resident_clusters((const void*)fused_tc_kernel<T, BN, A_MN, B_MN, PAIR, W>, 2, fu_threads(W),
                              FuCfg<BN, PAIR>::SMEM_BYTES, dim3(2 * (num_sms / 2)));
   });
   return n > 0 ? n : num_sms / 2;
 }
 
-template <typename T, int BN, bool A_MN, bool B_MN, bool PAIR>
+template <typename T, int BN, bool A_MN, bool B_MN, bool PAIR, int W>
 cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
   using C_ = FuCfg<BN, PAIR>;
   constexpr int BMT = PAIR ? 2 * BM : BM;
-  auto kern = fused_tc_kernel<T, BN, A_MN, B_MN, PAIR>;
+  auto kern = fused_tc_kernel<T, BN, A_MN, B_MN, PAIR, W>;
   static OncePerDevice set;
   const cudaError_t attr = set.run(call_device(), cudaSuccess, [kern] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::SMEM_BYTES);
@@ -769,11 +788,12 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
   if (inner) mI = mY;  // (C itself)
   else if (p.tma_in) ok = ok && make_map(&mI, TY, a.in, a.M, a.N, a.ld_in, 64, 32);
   if (!ok) return cudaErrorNotSupported;
-  const int slots = fused_slots<T, BN, A_MN, B_MN, PAIR>(a.num_sms);
+  const int slots = fused_slots<T, BN, A_MN, B_MN, PAIR, W>(a.num_sms);
   const int64_t units = most * a.splits;
+  if (units >= (1ll << 31)) return cudaErrorNotSupported;
   const int workers = (int)(units < slots ? units : slots);
   ctx.grid = PAIR ? 2 * workers : workers;
-  const cudaError_t e = launch_kernel(kern, dim3(ctx.grid), dim3(FU_THREADS), C_::SMEM_BYTES,
+  const cudaError_t e = launch_kernel(kern, dim3(ctx.grid), dim3(fu_threads(W)), C_::SMEM_BYTES,
                                       ctx.stream, PAIR ? 2 : 1, mA, mA32, mB, mI, mY, p);
   if (e == cudaSuccess) ctx.launches++;
   return e;
@@ -782,9 +802,11 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
 template <typename T, bool A_MN, bool B_MN>
 cudaError_t launch_fused_l(const FusedArgs& a, LaunchCtx& ctx) {
   switch (a.tile) {
-    case FUSED_TILE_PAIR: return launch_fused_cfg<T, 256, A_MN, B_MN, true>(a, ctx);
-    case FUSED_TILE_128: return launch_fused_cfg<T, 128, A_MN, B_MN, false>(a, ctx);
-    default: return launch_fused_cfg<T, 64, A_MN, B_MN, false>(a, ctx);
+    case FUSED_TILE_PAIR:
+      return a.mode == FUSED_SLOPE && a.splits == 1 ? launch_fused_cfg<T, 256, A_MN, B_MN, true, 8>(a, ctx)
+                                                    : launch_fused_cfg<T, 256, A_MN, B_MN, true, 16>(a, ctx);
+    case FUSED_TILE_128: return launch_fused_cfg<T, 128, A_MN, B_MN, false, 8>(a, ctx);
+    default: return launch_fused_cfg<T, 64, A_MN, B_MN, false, 4>(a, ctx);
   }
 }
 template <typename T>
