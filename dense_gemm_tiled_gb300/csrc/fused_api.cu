@@ -134,6 +134,8 @@ int run_call(Call& c, cudaStream_t stream) {
     // the raw products go where the call writes anyway, but not over what it reads
     float* P = static_cast<float*>(a.U ? a.U : a.Y);
     int64_t ldp = a.U ? a.ldu : a.ldy;
+    // (bias and activation alone: the product's own kernels apply them)
+    const bool plain = a.kind == FUSED_DENSE && !a.U && a.mode == FUSED_NONE && !c.dbias;
     const bool apart = !inner && a.mode != FUSED_NONE && a.in == (const void*)P;
     const int64_t p_bytes = apart ? pad256((int64_t)a.M * a.N * 4) : 0;
     e = ws.get((size_t)(part_bytes + p_bytes), stream);
@@ -145,8 +147,6 @@ int run_call(Call& c, cudaStream_t stream) {
     }
     path = GEMM_PATH_FUSED_FFMA;
     if (a.kind == FUSED_DENSE && !none) {
-      // (bias and activation alone: gemm_ex())
-      const bool plain = !a.U && a.mode == FUSED_NONE && !a.part;
       Epilogue ep;
       if (plain) {
         ep.bias = a.bias;
@@ -154,11 +154,13 @@ int run_call(Call& c, cudaStream_t stream) {
       }
       const int r = api_gemm(a.transA, a.transB, a.M, a.N, a.K, GEMM_F32, plain ? a.alpha : 1.f, 0.f,
                              a.A, a.lda, a.B, a.ldb, P, ldp, stream, ep);
-      if (r != GEMM_OK || plain) return r;
+      if (r != GEMM_OK) return r;
+      if (plain) return GEMM_OK;
       ctx.launches = 0;
       e = launch_fused_finish(a, P, ldp, ctx);
       if (e == cudaSuccess && c.dbias) e = launch_fused_dbias(a, c.dbias, ctx);
       const int before = gemm_last_launches();
+      ctx.grid = gemm_last_grid();
       const int done = api_done(path, ctx, e);
       api_add_launches(before);
       return done;

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(FS_THREADS, FS_BLOCKS)
     for (int i = 0; i < FS_WARPS * DEPTH; ++i) mbar_init(smem_u32(bars + i), 1);
     abort_word = 0u;
     fence_mbar_init();
-    tma_prefetch_desc(&tmB);
+    if (p.K > 0) tma_prefetch_desc(&tmB);  // (else there is no map)
   }
   pdl_wait();
   pdl_trigger();

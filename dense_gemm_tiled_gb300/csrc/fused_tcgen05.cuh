@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const bool leader = elect_one();
-    if (leader) {
+    if (leader && p.K > 0) {  // (else there are no maps)
       tma_prefetch_desc(&tmA);
       tma_prefetch_desc(&tmB);
     }

@@ -181,7 +181,8 @@ def test_grouped_backward(g, sizes, ahead, behind, dtype):
 def test_grouped_wgrad(g, sizes, ahead, behind, dtype):
     at, offs = offsets_of(sizes, ahead)
     rows, E = at[-1] + behind, len(sizes)
-    for i, (M, N, beta) in enumerate([(40, 72, 0.0), (136, 264, 1.0), (300, 64, -0.5)]):
+    for i, (M, N, beta) in enumerate([(40, 72, 0.0), (136, 264, 1.0), (300, 64, -0.5), (1, 1, 0.0),
+                                      (1, 65, 1.0)]):
         A, B = matrix((rows, M), dtype, 3 + i), matrix((rows, N), dtype, 13 + i)
         for t in (A, B):
             t[:ahead] = NAN
@@ -310,6 +311,38 @@ def test_results_over_inputs(g, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [9, 70])
+def test_offsets_past_32_bits(g, rows, dtype):
+    """Rows and matrices whose offsets (in elements) pass 2^31."""
+    dt, ld, far = DT[dtype], (1 << 31) // rows + 16 - (1 << 31) // rows % 16 + (1 << 25), 1_200_000_000
+    N, K = 72, 40
+    bufs = [torch.empty(ld * rows, dtype=dt, device="cuda") for _ in range(2)]
+    wide = torch.empty(2 * far + N * K, dtype=dt, device="cuda")
+    A = bufs[0].as_strided((rows, K), (ld, 1))
+    Y = bufs[1].as_strided((rows, N), (ld, 1))
+    B = wide.as_strided((3, N, K), (far, K, 1))
+    A.copy_(matrix((rows, K), dtype, 1))
+    B.copy_(matrix((3, N, K), dtype, 2))
+    at, offs = offsets_of([3, 0, rows - 3])
+    g.gemm_grouped(A, B, Y, offs, transB=True, act="gelu")
+    for e, (lo, hi) in enumerate(zip(at, at[1:])):
+        _, _, y, ey = ref.forward(f64(A[lo:hi]), f64(B[e].t()), dtype, name="gelu")
+        ref.check(Y[lo:hi], y, ey, e)
+    U, db = matrix((rows, K), dtype, 4), torch.empty((3, K), device="cuda")
+    dX = bufs[0].as_strided((rows, K), (ld, 1), K)
+    g.gemm_grouped_backward(Y, B, dX, offs, U, dbias=db)
+    for e, (lo, hi) in enumerate(zip(at, at[1:])):
+        d, ed, s, es = ref.backward(f64(Y[lo:hi]), f64(B[e]), dtype, f64(U[lo:hi]))
+        ref.check(dX[lo:hi], d, ed, e)
+        ref.check(db[e], s, es, e)
+    C = wide.as_strided((3, K, N), (far, N, 1))
+    g.gemm_grouped_wgrad(A, Y, C, offs)
+    for e, (lo, hi) in enumerate(zip(at, at[1:])):
+        _, _, y, ey = ref.forward(f64(A[lo:hi].t()), f64(Y[lo:hi]), dtype)
+        ref.check(C[e], y, ey, e)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_shared_matrix(g, dtype):
     """One matrix for every group (a stride of 0)."""
     at, offs = offsets_of([20, 0, 45])
@@ -334,6 +367,8 @@ def test_empty_sizes(g, dtype):
     _, offs = offsets_of([15, 0, 5])
     g.gemm_grouped(new(20, 0), new(3, 24, 0), Y, offs, transB=True)
     assert (Y == 0).all()
+    Y = g.gemm_fused(new(3, 0), new(24, 0), new(3, 24), transB=True, bias=b, act="relu")
+    assert torch.equal(Y, torch.relu(b).expand(3, 24))  # (few rows)
     # no rows: nothing is written but sums and gradients, which are zero
     db = torch.full((24,), NAN, device="cuda")
     g.gemm_fused_backward(new(0, 8), new(8, 24), new(0, 24), new(0, 24), dbias=db)
