@@ -11,6 +11,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gelu.cuh"
 #include "groups.cuh"
 #include "internal.h"
@@ -34,7 +36,7 @@ struct FinishParams {
   void* Y;
   int64_t ldy;
   float* part;
-  int chunks;  // of 64 V columns
+  int chunks;  // of FIN_COLS columns
   int64_t units;
 };
 
@@ -55,25 +57,28 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// V values of a row, V sizeof(T) bytes aligned
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T v[V];
+// four values of a row, aligned
+template <typename T>
+struct alignas(sizeof(T) * 4) Vec4 {
+  T v[4];
 };
 
-// A slot of 32 rows (group g's begin at o[g] / 32 + g) x 64 V columns a block: a thread
-// has V columns of four rows, and asks for those of all slices (up to S of them) at once.
-// V is 4 where every matrix has such rows, else 1.
-constexpr int FIN_THREADS = 512;
-template <typename T, int V, int S>
+// A slot of 32 rows (group g's begin at o[g] / 32 + g) x 256 columns a block: a thread has
+// four columns of four rows, and asks for those of all slices (up to S of them) at once.
+// PACKED: the four follow one another, where every matrix has aligned rows of whole
+// fours; else they are 64 apart, so that a warp still reads what lies together.
+constexpr int FIN_THREADS = 512, FIN_COLS = 256;
+template <typename T, bool PACKED, int S>
 __global__ void __launch_bounds__(FIN_THREADS) fused_finish_kernel(const FinishParams p) {
-  __shared__ float join[8][64 * V];
+  __shared__ float join[8][FIN_COLS];
   pdl_wait();
   pdl_trigger();
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   for (int64_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
     const int slot = (int)(unit / p.chunks);
-    const int n = ((int)(unit - (int64_t)slot * p.chunks) * 64 + tx) * V;
+    const int n0 = (int)(unit - (int64_t)slot * p.chunks) * FIN_COLS;
+    const int at = PACKED ? 4 * tx : tx;  // its columns: n0 + at + step j
+    constexpr int step = PACKED ? 1 : 64;
     int g = 0, lo = 0, len = p.M;
     if (p.offsets) {
       // the last group whose first slot is not past this one
@@ -90,94 +95,97 @@ __global__ void __launch_bounds__(FIN_THREADS) fused_finish_kernel(const FinishP
     const int r0 = (slot - (lo >> 5) - g) * 32;
     const int rows = r0 < 0 ? 0 : min(32, len - r0);
     if (rows <= 0) continue;  // (the whole block)
-    float sum[V];
+    const int n = n0 + at;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const int i0 = 4 * ty;
+    if (n < p.N && i0 < rows) {
+      auto get = [&](const auto* row, auto& x) {  // four of a row from column 0 on
+        if constexpr (PACKED) {
+          x = *reinterpret_cast<const std::decay_t<decltype(x)>*>(row + n);
+        } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum[j] = 0.f;
-    if (n < p.N) {
-      float bias[V];
+          for (int j = 0; j < 4; ++j)
+            if (n + step * j < p.N) x.v[j] = row[n + step * j];
+        }
+      };
+      float v[16], f[16];
+      Vec4<float> x[S][4];
+      Vec4<T> y[4], b;
+      if (p.bias) get(static_cast<const T*>(p.bias) + (int64_t)g * p.N, b);
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        bias[j] = p.bias ? to_f(static_cast<const T*>(p.bias)[(int64_t)g * p.N + n + j]) : 0.f;
-      const int i0 = 4 * ty;
-      if (i0 < rows) {
-        float v[4 * V], f[4 * V];
-        Vec<float, V> x[S][4];
-        Vec<T, V> y[4];
+      for (int i = 0; i < 4; ++i) {
+        const int64_t m = (int64_t)lo + r0 + min(i0 + i, rows - 1);
+        if (p.mode != FUSED_NONE) get(static_cast<const T*>(p.in) + m * p.ld_in, y[i]);
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+          if (s < p.splits) get(p.P + ((int64_t)s * p.M + m) * p.ldp, x[s][i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[i] = x[0][i / 4].v[i % 4];
+        f[i] = p.mode != FUSED_NONE ? to_f(y[i / 4].v[i % 4]) : 0.f;
+#pragma unroll
+        for (int s = 1; s < S; ++s)
+          if (s < p.splits) v[i] += x[s][i / 4].v[i % 4];
+        v[i] = p.alpha * v[i] + (p.bias ? to_f(b.v[i % 4]) : 0.f);
+      }
+      auto put = [&](void* to, int64_t ld) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int64_t m = (int64_t)lo + r0 + min(i0 + i, rows - 1);
-          if (p.mode != FUSED_NONE)
-            y[i] = *reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(p.in) + m * p.ld_in + n);
+          if (i0 + i >= rows) continue;
+          T* const row = static_cast<T*>(to) + ((int64_t)lo + r0 + i0 + i) * ld + n;
+          if constexpr (PACKED) {
+            Vec4<T> o;
 #pragma unroll
-          for (int s = 0; s < S; ++s)
-            if (s < p.splits)
-              x[s][i] = *reinterpret_cast<const Vec<float, V>*>(p.P + ((int64_t)s * p.M + m) * p.ldp + n);
-        }
+            for (int j = 0; j < 4; ++j) o.v[j] = from_f<T>(v[4 * i + j]);
+            *reinterpret_cast<Vec4<T>*>(row) = o;
+          } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            v[i * V + j] = x[0][i].v[j];
-            f[i * V + j] = p.mode != FUSED_NONE ? to_f(y[i].v[j]) : 0.f;
-#pragma unroll
-            for (int s = 1; s < S; ++s)
-              if (s < p.splits) v[i * V + j] += x[s][i].v[j];
-          }
-        auto put = [&](void* to, int64_t ld) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i0 + i >= rows) continue;
-            Vec<T, V> o;
-#pragma unroll
-            for (int j = 0; j < V; ++j) o.v[j] = from_f<T>(v[i * V + j]);
-            *reinterpret_cast<Vec<T, V>*>(static_cast<T*>(to) + ((int64_t)lo + r0 + i0 + i) * ld + n) = o;
-          }
-        };
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) v[i] = p.alpha * v[i] + bias[i % V];
-        if (p.U) put(p.U, p.ldu);
-        if (p.mode == FUSED_SLOPE) {
-          slope_of<T>(v, f, p.act);
-        } else {
-          act_of<T>(v, p.act);
-          if (p.mode == FUSED_ADD) {
-#pragma unroll
-            for (int i = 0; i < 4 * V; ++i) v[i] = __fmaf_rn(p.beta, f[i], v[i]);
+            for (int j = 0; j < 4; ++j)
+              if (n + step * j < p.N) row[step * j] = from_f<T>(v[4 * i + j]);
           }
         }
-        put(p.Y, p.ldy);
+      };
+      if (p.U) put(p.U, p.ldu);
+      if (p.mode == FUSED_SLOPE) {
+        slope_of<T>(v, f, p.act);
+      } else {
+        act_of<T>(v, p.act);
+        if (p.mode == FUSED_ADD) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < V; ++j) sum[j] += i0 + i < rows ? v[i * V + j] : 0.f;
+          for (int i = 0; i < 16; ++i) v[i] = __fmaf_rn(p.beta, f[i], v[i]);
+        }
       }
+      put(p.Y, p.ldy);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[i % 4] += i0 + i / 4 < rows ? v[i] : 0.f;
     }
     if (p.part) {
       __syncthreads();  // (the last unit's sums are read)
 #pragma unroll
-      for (int j = 0; j < V; ++j) join[ty][tx * V + j] = sum[j];
+      for (int j = 0; j < 4; ++j) join[ty][at + step * j] = sum[j];
       __syncthreads();
-      const int at = (int)(unit - (int64_t)slot * p.chunks) * 64 * V + threadIdx.x;
-      if ((int)threadIdx.x < 64 * V && at < p.N)
-      {
+      if ((int)threadIdx.x < FIN_COLS && n0 + (int)threadIdx.x < p.N) {
         float all = join[0][threadIdx.x];
 #pragma unroll
         for (int w = 1; w < 8; ++w) all += join[w][threadIdx.x];
-        p.part[(int64_t)slot * p.N + at] = all;
+        p.part[(int64_t)slot * p.N + n0 + threadIdx.x] = all;
       }
     }
   }
 }
 
-// dbias[g][j] = the sum of group g's slots: 32 columns a block, eight warps taking
-// the slots in turn, their sums joined in warp order.
-__global__ void __launch_bounds__(256) fused_dbias_kernel(const float* __restrict__ part,
-                                                          const int* offsets, int M, int N,
-                                                          int chunks, int64_t units,
-                                                          float* __restrict__ dbias) {
+// dbias[g][j] = the sum of group g's slots: 32 columns a block, its warps taking the
+// slots in turn, their sums joined in warp order.  Thirty-two warps where a group has
+// many slots (one of 512: 8 us with eight, the call 258 -> 244), eight elsewhere (64 of
+// 16 slots on average: 4 us less).
+template <int DB_WARPS>
+__global__ void __launch_bounds__(32 * DB_WARPS)
+    fused_dbias_kernel(const float* __restrict__ part, const int* offsets, int M, int N, int chunks,
+                       int64_t units, float* __restrict__ dbias) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float join[8][32];
+  __shared__ float join[DB_WARPS][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int g = (int)(unit / chunks), n = (int)(unit - (int64_t)g * chunks) * 32 + lane;
@@ -188,14 +196,14 @@ __global__ void __launch_bounds__(256) fused_dbias_kernel(const float* __restric
     float sum = 0.f;
     if (n < N) {
 #pragma unroll 8
-      for (int s = warp; s < slots; s += 8) sum += src[(int64_t)s * N];
+      for (int s = warp; s < slots; s += DB_WARPS) sum += src[(int64_t)s * N];
     }
     __syncthreads();  // (the last unit's sums are read)
     join[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && n < N) {
 #pragma unroll
-      for (int w = 1; w < 8; ++w) sum += join[w][lane];
+      for (int w = 1; w < DB_WARPS; ++w) sum += join[w][lane];
       dbias[(int64_t)g * N + n] = sum;
     }
   }
@@ -225,14 +233,16 @@ static cudaError_t launch_finish(const FusedArgs& a, const float* P, int64_t ldp
   auto four = [](const void* q, int64_t ld, size_t e) {
     return !q || (((uintptr_t)q % (4 * e)) == 0 && ld % 4 == 0);
   };
-  const bool vec = a.N % 4 == 0 && four(P, ldp, 4) && four(a.Y, a.ldy, sizeof(T)) &&
-                   four(a.U, a.ldu, sizeof(T)) && (a.mode == FUSED_NONE || four(a.in, a.ld_in, sizeof(T)));
-  p.chunks = (a.N + (vec ? 255 : 63)) / (vec ? 256 : 64);
+  const bool packed = a.N % 4 == 0 && four(P, ldp, 4) && four(a.Y, a.ldy, sizeof(T)) &&
+                      four(a.U, a.ldu, sizeof(T)) && four(a.bias, a.N, sizeof(T)) &&
+                      (a.mode == FUSED_NONE || four(a.in, a.ld_in, sizeof(T)));
+  p.chunks = (a.N + FIN_COLS - 1) / FIN_COLS;
   p.units = (a.M / 32 + a.groups + 1) * (int64_t)p.chunks;
   const int64_t most = (int64_t)a.num_sms * 64;
   const dim3 grid((unsigned)(p.units < most ? p.units : most));
-  auto kern = vec ? (a.splits == 1 ? fused_finish_kernel<T, 4, 1> : fused_finish_kernel<T, 4, FUSED_MAX_SPLITS>)
-                  : (a.splits == 1 ? fused_finish_kernel<T, 1, 1> : fused_finish_kernel<T, 1, FUSED_MAX_SPLITS>);
+  constexpr int S = FUSED_MAX_SPLITS;
+  auto kern = packed ? (a.splits == 1 ? fused_finish_kernel<T, true, 1> : fused_finish_kernel<T, true, S>)
+                     : (a.splits == 1 ? fused_finish_kernel<T, false, 1> : fused_finish_kernel<T, false, S>);
   const cudaError_t e = launch_kernel(kern, grid, dim3(FIN_THREADS), 0, ctx.stream, 1, p);
   if (e == cudaSuccess) ctx.launches++;
   return e;
@@ -249,11 +259,12 @@ cudaError_t launch_fused_finish(const FusedArgs& a, const float* P, int64_t ldp,
 cudaError_t launch_fused_dbias(const FusedArgs& a, float* dbias, LaunchCtx& ctx) {
   const int chunks = (a.N + 31) / 32;
   const int64_t units = (int64_t)a.groups * chunks, most = (int64_t)a.num_sms * 64;
-  const cudaError_t e =
-      launch_kernel(fused_dbias_kernel, dim3((unsigned)(units < most ? units : most)), dim3(256), 0,
-                    ctx.stream, 1, (const float*)a.part,
-                    a.kind == FUSED_DENSE ? (const int*)nullptr : a.offsets, a.M, a.N, chunks, units,
-                    dbias);
+  const bool many = a.M / 32 >= 128ll * a.groups;
+  const cudaError_t e = launch_kernel(
+      many ? fused_dbias_kernel<32> : fused_dbias_kernel<8>,
+      dim3((unsigned)(units < most ? units : most)), dim3(many ? 1024 : 256), 0, ctx.stream, 1,
+      (const float*)a.part, a.kind == FUSED_DENSE ? (const int*)nullptr : a.offsets, a.M, a.N, chunks,
+      units, dbias);
   if (e == cudaSuccess) ctx.launches++;
   return e;
 }

@@ -55,6 +55,7 @@ SHAPES = [
     (128, 128, 128), (129, 257, 192), (200, 304, 136), (255, 64, 1024), (300, 513, 70),
     (512, 520, 333), (1000, 200, 48),
     (17, 72, 4104), (130, 264, 4100), (300, 1030, 2056), (512, 2048, 1030),
+    (4200, 72, 40),
 ]
 
 
