@@ -62,7 +62,7 @@ struct FuCfg {
   static constexpr int FIXED = 1024 + 512;
   static constexpr int RAW = (SMEM_LIMIT - FIXED - STAGING_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = RAW < 8 ? RAW : 8;
-  static constexpr int TMEM_COLS = 2 * BN;  // two accumulators
+  static constexpr int TMEM_COLS = BN == 192 ? 512 : 2 * BN;  // two accumulators (a power of two)
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + FIXED;
 };
 
@@ -805,6 +805,7 @@ cudaError_t launch_fused_l(const FusedArgs& a, LaunchCtx& ctx) {
     case FUSED_TILE_PAIR:
       return a.mode == FUSED_SLOPE && a.splits == 1 ? launch_fused_cfg<T, 256, A_MN, B_MN, true, 8>(a, ctx)
                                                     : launch_fused_cfg<T, 256, A_MN, B_MN, true, 16>(a, ctx);
+    case FUSED_TILE_192: return launch_fused_cfg<T, 192, A_MN, B_MN, false, 12>(a, ctx);
     case FUSED_TILE_128: return launch_fused_cfg<T, 128, A_MN, B_MN, false, 8>(a, ctx);
     default: return launch_fused_cfg<T, 64, A_MN, B_MN, false, 4>(a, ctx);
   }

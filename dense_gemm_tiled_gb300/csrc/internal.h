@@ -333,7 +333,7 @@ cudaError_t launch_mx4(const Mx4Args& a, LaunchCtx& ctx);
 // (entry points: include/gemm.h, gemm_fused and gemm_grouped)
 enum { FUSED_DENSE = 0, FUSED_ROWS = 1, FUSED_INNER = 2 };  // one matrix, groups of rows, groups of K
 enum { FUSED_NONE = 0, FUSED_ADD = 1, FUSED_SLOPE = 2 };    // what the epilogue's input is: none, R, U
-enum { FUSED_TILE_PAIR, FUSED_TILE_128, FUSED_TILE_64, FUSED_TILES };
+enum { FUSED_TILE_PAIR, FUSED_TILE_192, FUSED_TILE_128, FUSED_TILE_64, FUSED_TILES };
 constexpr int FUSED_MAX_SPLITS = 4;
 struct FusedArgs {
   int kind, dtype;     // dtype: 0 fp32, 1 fp16, 2 bf16
@@ -375,9 +375,9 @@ cudaError_t launch_fused(const FusedArgs& a, LaunchCtx& ctx);
 cudaError_t launch_fused_bf16(const FusedArgs& a, LaunchCtx& ctx);
 // forward products of up to FUSED_FEW_ROWS rows in all (operands as above, B stored by
 // rows of K): every matrix whose group has rows read once.  In a graph, us, against the
-// tensor-core kernel: 5632 x 2048 8 rows 9.3 / 14.6, 16 rows 10.8 / 14.4, 32 rows 14.7 /
-// 14.0; 8192 x 8192 16 rows 31.9 / 37.6, 32 rows 41.5 / 37.6; 1408 x 2048 of 64 groups, 16
-// rows in 16 of them 19.8 / 31.1, 32 rows in 24 31.1 / 29.6.
+// tensor-core kernel: 5632 x 2048 8 rows 9.3 / 13, 16 rows 11.0 / 12.0; 2048 x 5632 8 rows
+// 8.9 / 13.9; 8192 x 8192 8 rows 27.9 / 30.2, 16 rows 32.1 / 30.2; 1408 x 2048 of 64 groups,
+// 16 rows in 16 of them 19.8 / 27, 32 rows in 24 31.1 / 28.5.
 constexpr int FUSED_FEW_ROWS = 16;
 cudaError_t launch_fused_stream(const FusedArgs& a, LaunchCtx& ctx);
 // dbias[g][j] = the sum of group g's slots of `part`
