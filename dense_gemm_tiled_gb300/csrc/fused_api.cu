@@ -53,6 +53,11 @@ int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t 
   return GEMM_OK;
 }
 
+// A single row has any pitch: one that keeps it aligned.
+inline void one_row(int64_t rows, int64_t cols, int64_t* ld) {
+  if (rows <= 1) *ld = (cols + 15) / 16 * 16 > 0 ? (cols + 15) / 16 * 16 : 16;
+}
+
 // The sizes that a call gives, and its matrices' stored shapes.
 struct Call {
   FusedArgs a;
@@ -94,6 +99,9 @@ int check_call(Call& c, int64_t M, int64_t N, int64_t K, int64_t groups, int dty
     so.hi = so.lo + (uintptr_t)(groups + 1) * 4;
   }
   if (meet(c.sY, c.sA) || meet(c.sY, c.sB) || meet(c.sY, so)) return GEMM_ERR_ALIAS;
+  if (ny <= 1) one_row(M, N, &a.ldy);
+  one_row(c.a_rows, c.a_cols, &a.lda);
+  if (nb <= 1) one_row(c.b_rows, c.b_cols, &a.ldb);
   return GEMM_OK;
 }
 
@@ -229,12 +237,14 @@ int check_forward(Call& c, const void* bias, const void* R, int64_t ldr, void* U
     a.mode = FUSED_ADD;
     a.in = R;
     a.ld_in = ldr;
+    one_row(M, N, &a.ld_in);
   }
   if (U) {
     const int rc = check_matrix(U, M, N, ldu, 1, 0, e, &su);
     if (rc != GEMM_OK) return rc;
     a.U = U;
     a.ldu = ldu;
+    one_row(M, N, &a.ldu);
   }
   Span so;
   if (a.kind != FUSED_DENSE && a.groups > 0) {
@@ -244,7 +254,7 @@ int check_forward(Call& c, const void* bias, const void* R, int64_t ldr, void* U
   if (meet(c.sY, sb) || meet(su, sb) || meet(su, c.sA) || meet(su, c.sB) || meet(su, c.sY) ||
       meet(su, sr) || meet(su, so))
     return GEMM_ERR_ALIAS;
-  if (meet(c.sY, sr) && !(R == a.Y && (ldr == a.ldy || M <= 1))) return GEMM_ERR_ALIAS;
+  if (meet(c.sY, sr) && !(R == a.Y && a.ld_in == a.ldy)) return GEMM_ERR_ALIAS;
   return GEMM_OK;
 }
 
@@ -259,6 +269,7 @@ int check_backward(Call& c, const void* U, int64_t ldu, float* dbias) {
     a.mode = FUSED_SLOPE;
     a.in = U;
     a.ld_in = ldu;
+    one_row(M, N, &a.ld_in);
   }
   if (dbias && a.groups > 0 && N > 0) {
     if (((uintptr_t)dbias % 4) != 0) return GEMM_ERR_INVALID_ARG;
@@ -266,7 +277,7 @@ int check_backward(Call& c, const void* U, int64_t ldu, float* dbias) {
     sd.hi = sd.lo + (uintptr_t)((int64_t)a.groups * N * 4);
   }
   c.dbias = dbias;
-  if (meet(c.sY, su) && !(U == a.Y && (ldu == a.ldy || M <= 1))) return GEMM_ERR_ALIAS;
+  if (meet(c.sY, su) && !(U == a.Y && a.ld_in == a.ldy)) return GEMM_ERR_ALIAS;
   Span so;
   if (a.kind != FUSED_DENSE && a.groups > 0) {
     so.lo = (uintptr_t)a.offsets;

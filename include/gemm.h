@@ -421,8 +421,8 @@ int gemm_grouped_backward(int transB, int64_t rows, int64_t N, int64_t K, int64_
  *     C_g = alpha * A_g^T * B_g + beta * C_g
  *
  * A: rows x M (lda), B: rows x N (ldb), A_g and B_g their rows of group g (offsets as
- * in gemm_grouped()); C_g = C + g * strideC: M x N (ldc), which must not overlap one
- * another.  An empty group's C_g is beta * C_g (zero with beta == 0, which reads no C).
+ * in gemm_grouped()); C_g = C + g * strideC: M x N (ldc), strideC at least (M - 1) * ldc + N
+ * (else GEMM_ERR_ALIAS).  An empty group's C_g is beta * C_g (zero with beta == 0, which reads no C).
  */
 int gemm_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int64_t groups, const int32_t* offsets,
                        int dtype, float alpha, float beta, const void* A, int64_t lda, const void* B,

@@ -356,6 +356,67 @@ def test_shared_matrix(g, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sizes", [[3, 0, 7], [40, 0, 61]])
+def test_interleaved_matrices(g, sizes, dtype):
+    """Matrices of B whose rows lie between one another's."""
+    at, offs = offsets_of(sizes)
+    A = matrix((at[-1], 48), dtype, 1)
+    for tb, w in ((False, matrix((48, 3, 72), dtype, 2).permute(1, 0, 2)),
+                  (True, matrix((72, 3, 48), dtype, 3).permute(1, 0, 2)),
+                  (True, matrix((72, 3, 48), dtype, 3, pad=8).permute(1, 0, 2)),
+                  (False, matrix((48, 3, 77), dtype, 4).permute(1, 0, 2))):
+        N = w.shape[1] if tb else w.shape[2]
+        Y = torch.empty((at[-1], N), dtype=DT[dtype], device="cuda")
+        g.gemm_grouped(A, w, Y, offs, transB=tb)
+        for e, (lo, hi) in enumerate(zip(at, at[1:])):
+            _, _, y, ey = ref.forward(f64(A[lo:hi]), f64(w[e].t() if tb else w[e]), dtype)
+            ref.check(Y[lo:hi], y, ey, e)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_16_bit_value(g, dtype):
+    """gelu and its slope of every finite 16-bit value, the product being 0 or 1."""
+    v = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(DT[dtype])
+    v = v[v.isfinite()][: 65536 // 64 * 64 - 4096].contiguous()
+    x, n = v.double(), v.numel()
+    zero, one = torch.zeros((20, 16), dtype=DT[dtype], device="cuda"), torch.zeros((20, 16), dtype=DT[dtype], device="cuda")
+    one[:, 0] = 1
+    W = torch.ones((n, 16), dtype=DT[dtype], device="cuda")
+    for rows in (20, 3):  # (either kernel)
+        Y = torch.empty((rows, n), dtype=DT[dtype], device="cuda")
+        g.gemm_fused(zero[:rows], W, Y, transB=True, bias=v, act="gelu")
+        y = ref.act(x, "gelu").expand(rows, n)
+        e = 2.0 ** -22 * x.abs().expand(rows, n)
+        ref.check(Y, y, e + ref.rounding(y.abs() + e, dtype), "gelu")
+    dX = torch.empty((20, n), dtype=DT[dtype], device="cuda")
+    g.gemm_fused_backward(one, W, dX, v.expand(20, n).contiguous(), transB=True)
+    d = ref.slope(x, "gelu").expand(20, n)
+    ref.check(dX, d, 2.0 ** -20 + ref.rounding(d.abs() + 2.0 ** -20, dtype), "slope")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_single_rows(g, dtype):
+    """The pitch of a single row does not matter, however far."""
+    far = 1 << 42
+    A, W = matrix((1, 77), dtype, 1), matrix((1, 77), dtype, 2)
+    B, R = matrix((30, 77), dtype, 3, 0.2), matrix((1, 30), dtype, 4)
+    Y, U = torch.empty((1, 30), dtype=DT[dtype], device="cuda"), torch.empty((1, 30), dtype=DT[dtype], device="cuda")
+    one = lambda t: t.as_strided((1, t.shape[1]), (far, 1))  # noqa: E731
+    g.gemm_fused(one(A), B, one(Y), transB=True, residual=one(R), preact=one(U), act="gelu")
+    u, eu, y, ey = ref.forward(f64(A), f64(B.t()), dtype, name="gelu", residual=f64(R))
+    ref.check(Y, y, ey)
+    ref.check(U, u, eu)
+    d, ed, _, _ = ref.backward(f64(A), f64(B.t()), dtype, f64(U))
+    g.gemm_fused_backward(one(A), B, one(Y), one(U), transB=True)
+    ref.check(Y, d, ed)
+    X = matrix((40, 77), dtype, 5)
+    Z = torch.empty((40, 1), dtype=DT[dtype], device="cuda")
+    g.gemm_fused(X, one(W), Z, transB=True)  # one row of B
+    _, _, y, ey = ref.forward(f64(X), f64(W.t()), dtype)
+    ref.check(Z, y, ey)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_empty_sizes(g, dtype):
     dt = DT[dtype]
 
@@ -512,23 +573,24 @@ def test_offsets_that_do_not_ascend(g):
     assert g.check_device_status() == g.OK
 
 
-def test_wait_that_runs_out(g):
+@pytest.mark.parametrize("sizes", [[130, 170], [3, 8]])
+def test_wait_that_runs_out(g, sizes):
     """A load that never comes: the waits end, the status says so, the next call is right."""
-    A, W = matrix((300, 256), "bf16", 1), matrix((2, 256, 512), "bf16", 2)
-    _, offs = offsets_of([130, 170])
-    Y = torch.empty((300, 512), dtype=torch.bfloat16, device="cuda")
+    at, offs = offsets_of(sizes)
+    A, W = matrix((at[-1], 256), "bf16", 1), matrix((2, 512, 256), "bf16", 2)
+    Y = torch.empty((at[-1], 512), dtype=torch.bfloat16, device="cuda")
     g.set_wait_timeout_ns(50_000_000)
     try:
         g.set_fault_injection(1)
-        g.gemm_grouped(A, W, Y, offs)
+        g.gemm_grouped(A, W, Y, offs, transB=True)
         g.set_fault_injection(0)
         assert g.check_device_status() == g.ERR_TIMEOUT
     finally:
         g.set_fault_injection(0)
         g.set_wait_timeout_ns(0)
-    g.gemm_grouped(A, W, Y, offs)
-    for e, (lo, hi) in enumerate([(0, 130), (130, 300)]):
-        _, _, y, ey = ref.forward(f64(A[lo:hi]), f64(W[e]), "bf16")
+    g.gemm_grouped(A, W, Y, offs, transB=True)
+    for e, (lo, hi) in enumerate(zip(at, at[1:])):
+        _, _, y, ey = ref.forward(f64(A[lo:hi]), f64(W[e].t()), "bf16")
         ref.check(Y[lo:hi], y, ey)
 
 
