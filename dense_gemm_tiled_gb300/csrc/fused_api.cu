@@ -146,11 +146,17 @@ int run_call(Call& c, cudaStream_t stream) {
     const bool plain = a.kind == FUSED_DENSE && !a.U && a.mode == FUSED_NONE && !c.dbias;
     // (nor where rows off 16-byte alignment would slow the products: 1000 x 3001 x 777 112
     // us, 94 into aligned rows)
-    const bool apart = !inner && !plain &&
-                       ((a.mode != FUSED_NONE && a.in == (const void*)P) ||
-                        ((uintptr_t)P % 16) != 0 || ldp % 4 != 0);
+    // Slices of K are apart too; those of weights' gradients are finished as one matrix, so
+    // only where the groups' follow one another.
+    const int64_t p_rows = (int64_t)a.M * (inner ? a.groups : 1);
+    if (a.kind != FUSED_DENSE && !none &&
+        (!inner || (p_rows <= SIZE_LIM && (a.groups == 1 || a.stride_y == (int64_t)a.M * a.ldy))))
+      a.splits = sgemm_grouped_splits(a);
+    const bool apart = a.splits > 1 || (!inner && !plain &&
+                                        ((a.mode != FUSED_NONE && a.in == (const void*)P) ||
+                                         ((uintptr_t)P % 16) != 0 || ldp % 4 != 0));
     const int64_t pitch = (int64_t)(a.N + 3) / 4 * 4;
-    const int64_t p_bytes = apart ? pad256((int64_t)a.M * pitch * 4) : 0;
+    const int64_t p_bytes = apart ? pad256(a.splits * p_rows * pitch * 4) : 0;
     e = ws.get((size_t)(part_bytes + p_bytes), stream);
     if (e != cudaSuccess) return api_done(GEMM_PATH_NONE, ctx, e);
     a.part = part_bytes ? static_cast<float*>(ws.ptr) : nullptr;
@@ -180,7 +186,12 @@ int run_call(Call& c, cudaStream_t stream) {
     }
     if (!none) {
       e = launch_sgemm_grouped(a, P, ldp, ctx);
-      if (e == cudaSuccess && !inner) e = launch_fused_finish(a, P, ldp, ctx);
+      if (inner) {  // (the groups' rows of C, one after another)
+        a.kind = FUSED_DENSE;
+        a.M = (int)p_rows;
+        a.groups = 1;
+      }
+      if (e == cudaSuccess && (!inner || a.splits > 1)) e = launch_fused_finish(a, P, ldp, ctx);
     }
   } else {
     const bool copy_a = a.K > 0 && !aligned16(a.A, a.lda);

@@ -120,6 +120,27 @@ __global__ void __launch_bounds__(FIN_THREADS) fused_finish_kernel(const FinishP
         for (int s = 0; s < S; ++s)
           if (s < p.splits) get(p.P + ((int64_t)s * p.M + m) * p.ldp, x[s][i]);
       }
+      // (slices past S, in order: fp32 alone has so many)
+      if constexpr (sizeof(T) == 4 && S > 1) {
+        for (int s0 = S; s0 < p.splits; s0 += S - 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+              for (int s = 1; s < S; ++s) x[0][i].v[j] += x[s][i].v[j];
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int64_t m = (int64_t)lo + r0 + min(i0 + i, rows - 1);
+#pragma unroll
+            for (int s = 1; s < S; ++s) {
+              x[s][i] = Vec4<float>{{0.f, 0.f, 0.f, 0.f}};
+              if (s0 + s - 1 < p.splits) get(p.P + ((int64_t)(s0 + s - 1) * p.M + m) * p.ldp, x[s][i]);
+            }
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         v[i] = x[0][i / 4].v[i % 4];

@@ -334,7 +334,8 @@ cudaError_t launch_mx4(const Mx4Args& a, LaunchCtx& ctx);
 enum { FUSED_DENSE = 0, FUSED_ROWS = 1, FUSED_INNER = 2 };  // one matrix, groups of rows, groups of K
 enum { FUSED_NONE = 0, FUSED_ADD = 1, FUSED_SLOPE = 2 };    // what the epilogue's input is: none, R, U
 enum { FUSED_TILE_PAIR, FUSED_TILE_192, FUSED_TILE_128, FUSED_TILE_64, FUSED_TILES };
-constexpr int FUSED_MAX_SPLITS = 4;
+constexpr int FUSED_MAX_SPLITS = 4;       // slices of K, 16-bit types
+constexpr int FUSED_MAX_SPLITS_F32 = 16;  // and fp32 grouped products
 struct FusedArgs {
   int kind, dtype;     // dtype: 0 fp32, 1 fp16, 2 bf16
   int transA, transB;
@@ -382,8 +383,9 @@ constexpr int FUSED_FEW_ROWS = 16;
 cudaError_t launch_fused_stream(const FusedArgs& a, LaunchCtx& ctx);
 // dbias[g][j] = the sum of group g's slots of `part`
 cudaError_t launch_fused_dbias(const FusedArgs& a, float* dbias, LaunchCtx& ctx);
-// fp32: the raw products of a grouped call into P (FUSED_ROWS, pitch ldp), or C
-// itself (FUSED_INNER)
+// fp32 grouped products: slices of K that fill the GPU; the raw products into P
+// [splits][rows, or groups x M][ldp] -- or, FUSED_INNER and one slice, C itself
+int sgemm_grouped_splits(const FusedArgs& a);
 cudaError_t launch_sgemm_grouped(const FusedArgs& a, float* P, int64_t ldp, LaunchCtx& ctx);
 // the epilogue of the raw products P, `splits` of them to be added up (rows of the
 // groups only); of one in fp32, P may be Y or U

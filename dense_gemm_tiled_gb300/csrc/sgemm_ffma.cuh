@@ -158,6 +158,7 @@ struct Params {
   // of C (stride_c), their rows of A or their ranges of K from `offsets`
   const int* offsets;
   int groups;
+  int64_t stride_z;  // K slices (blockIdx.z): elements between their results
 };
 
 // Kernel kinds: one output tile per block (C), one K slice of a tile per
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(TL::THREADS, TL::MIN_BLOCKS) sgemm_ffma_kernel
     Bg += (int64_t)g * p.stride_b;
     Cg += (int64_t)lo * p.ldc;
   }
+  if constexpr (KIND == KIND_ROWS || KIND == KIND_INNER) Cg += (int64_t)blockIdx.z * p.stride_z;
   const uint32_t sbase = smem_u32(smem);
 
   // work state: non-persistent blocks do one item; persistent blocks walk
@@ -612,7 +614,12 @@ __global__ void __launch_bounds__(TL::THREADS, TL::MIN_BLOCKS) sgemm_ffma_kernel
       if constexpr (KIND == KIND_INNER) {
         int n;
         group_span(p.offsets, blockIdx.y, p.K, w.kbeg, n);
-        w.kend = w.kbeg + n;
+        // this slice of the group's range, in whole K steps (possibly none)
+        const int steps = (n + BK - 1) / BK;
+        const int per = (steps + (int)gridDim.z - 1) / (int)gridDim.z * BK;
+        const int end = w.kbeg + n;
+        w.kbeg = min(w.kbeg + (int)blockIdx.z * per, end);
+        w.kend = min(w.kbeg + per, end);
       }
     } else {
       if (!walk.next<BK>(p, G, w)) break;

@@ -199,6 +199,29 @@ def test_grouped_wgrad(g, sizes, ahead, behind, dtype):
             ref.check(C[e], y, ey, e)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sizes,N,K", [([455], 130, 1332), ([3, 0, 2], 72, 3000), ([40] * 9, 30, 257)])
+def test_long_inner_dimension(g, sizes, N, K, dtype):
+    """Few tiles and a long inner dimension: slices of it (fp32), for weights too."""
+    grouped_call(g, sizes, 1, 4, N, K, dtype, True, "gelu", True, True, True, 7)
+    grouped_call(g, sizes, 0, 0, N, K, dtype, False, "none", False, True, False, 8, 3, 1)
+    at, offs = offsets_of([K, 0, K // 3, 1], 2)
+    A, B = matrix((at[-1], 49), dtype, 1), matrix((at[-1], N), dtype, 2)
+    for pad in (0, 5):
+        C = matrix((4, 49, N), dtype, 3, pad=pad)
+        c0 = f64(C)
+        g.gemm_grouped_wgrad(A, B, C, offs, alpha=0.5, beta=-1.0)
+        for e, (lo, hi) in enumerate(zip(at, at[1:])):
+            _, _, y, ey = ref.forward(f64(A[lo:hi].t()), f64(B[lo:hi]), dtype, 0.5, residual=c0[e],
+                                      beta=-1.0)
+            ref.check(C[e], y, ey, e)
+    C = torch.zeros((8, 49, N), dtype=DT[dtype], device="cuda")[::2]  # (apart from one another)
+    g.gemm_grouped_wgrad(A, B, C, offs)
+    for e, (lo, hi) in enumerate(zip(at, at[1:])):
+        _, _, y, ey = ref.forward(f64(A[lo:hi].t()), f64(B[lo:hi]), dtype)
+        ref.check(C[e], y, ey, e)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("off,pad", [(0, 8), (1, 0), (0, 1), (3, 5)])
 def test_pitches_and_alignment(g, off, pad, dtype):
