@@ -66,6 +66,8 @@ struct FuCfg {
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + FIXED;
 };
 
+enum { U_NONE, U_SECTORS, U_HALVES, U_ROWS };
+
 struct FuParams {
   int kind;
   int M, N, K;         // rows of all groups (FUSED_INNER: of C_g), columns, inner size (of all groups)
@@ -91,7 +93,7 @@ struct FuParams {
   void* Y;
   int64_t ldy, stride_y;
   int tma_in, tma_y;  // 16-byte aligned rows: through the tensor-memory-access unit
-  int vec_u;          // 32-byte aligned rows
+  int u_way;          // U's rows: U_SECTORS 32-byte aligned, U_HALVES 16-byte, U_ROWS neither
   float* part;         // column sums of each 32 rows of a group, [rows / 32 + groups + 1][N]
   unsigned int* status;
   uint64_t timeout_ns;
@@ -199,7 +201,33 @@ __device__ __forceinline__ float warp_column_sum(float (&v)[16], int lane) {
 __device__ __forceinline__ uint32_t fu_at(int r, int c) {
   return (uint32_t)(r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
 }
-// A box's rows from its staging buffer to memory, row by row
+// A box's rows between memory and its staging buffer, row by row: a row's 64 columns at
+// a time, by the whole warp (rows off 16-byte alignment, or that a group's end cuts; rows
+// and columns past the ends excepted).  Off alignment, a row a lane would touch 32 rows
+// at every access (2000 x 4001 x 2048 with R and U: 130 us, this way 48).
+template <typename T>
+__device__ __forceinline__ void fu_rows_in(const T* src, int64_t ld, int rows, int cols,
+                                           uint32_t sbuf, int lane) {
+  const uint16_t* s = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    uint16_t v[8][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[i][h] = (r0 + i < rows && lane + 32 * h < cols) ? s[(int64_t)(r0 + i) * ld + lane + 32 * h]
+                                                          : (uint16_t)0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(sbuf + fu_at(r0 + i, lane + 32 * h)),
+                     "h"(v[i][h])
+                     : "memory");
+  }
+  __syncwarp();
+}
 // (vec: 16-byte aligned rows, eight lanes a row)
 template <typename T>
 __device__ __forceinline__ void fu_rows_out(T* dst, int64_t ld, int rows, int cols, bool vec,
@@ -475,9 +503,8 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
       const int64_t gy = p.kind == FUSED_INNER ? (int64_t)u.g * p.stride_y : 0;
       auto sbuf_of = [&](int b) { return staging_addr + (uint32_t)((4 * b + q) * 4096); };
       // R, U or C: the boxes into their staging buffers, once the last stores have read
-      // those; rows off alignment by their lanes instead, sixteen columns ahead
+      // those
       const bool in_box = p.mode != FUSED_NONE && p.tma_in;
-      const bool in_lanes = p.mode != FUSED_NONE && !p.tma_in;
       if (in_box && lane == 0 && hh < boxes) {
         bulk_wait_read<0>();
         for (int b = hh; b < boxes; b += BOX_WARPS) {
@@ -501,19 +528,6 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
         const uint32_t sbuf = sbuf_of(b);
         const int gn = u.n0 + 64 * b, cols = min(p.N - gn, 64);
         const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + 64 * b);
-        uint32_t ahead[8];
-        const uint16_t* const src = reinterpret_cast<const uint16_t*>(
-            static_cast<const T*>(p.in) + gy + (int64_t)(gm + lane) * p.ld_in + gn);
-        auto read_in = [&](int c) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const int at = 16 * c + e;
-            const uint32_t lo = lane < rows && at < cols ? src[at] : 0u;
-            const uint32_t hi = lane < rows && at + 1 < cols ? src[at + 1] : 0u;
-            ahead[e / 2] = lo | hi << 16;
-          }
-        };
-        if (in_lanes) read_in(0);
         got = true;
         if (lane == 0) {
           if (in_box) {
@@ -528,48 +542,12 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
         }
         got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
         if (!got) break;
-        // Sixteen columns at a time.  (Not unrolled: the code that one call takes of all
-        // that is here then stays in the instruction cache; unrolled over 64 columns,
-        // steps that a call does not take slowed it as well: wgrad of 4000 rows of 8
-        // groups 140 us, 117 without the slope's code in the kernel.)
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int col = gn + 16 * c;
-          uint32_t r[16];
+        // sixteen columns' accumulators, and U in fp32
+        auto sums_of = [&](int c, uint32_t (&r)[16]) {
           tmem_ld_32x32b_x16(t_row + (uint32_t)(16 * c), r);
-          const uint32_t at[2] = {sbuf + (uint32_t)(lane * 128 + (((2 * c) ^ (lane & 7)) * 16)),
-                                  sbuf + (uint32_t)(lane * 128 + (((2 * c + 1) ^ (lane & 7)) * 16))};
-          uint32_t now[8];
-          if (in_box) {
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(now[4 * w]), "=r"(now[4 * w + 1]), "=r"(now[4 * w + 2]),
-                             "=r"(now[4 * w + 3])
-                           : "r"(at[w])
-                           : "memory");
-          } else if (in_lanes) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) now[e] = ahead[e];
-            if (c < 3) read_in(c + 1);
-          }
           tmem_ld_wait();
-          if (c == 3 && b + BOX_WARPS >= boxes) release_acc(buf);
-          if (p.splits > 1) {
-            // raw sums of the slice: 64 bytes of this lane's row of P (whose rows are whole)
-            if (lane < rows && col < p.ldp) {
-              float* const d = p.P + ((int64_t)u.slice * p.M + gm + lane) * p.ldp + col;
-#pragma unroll
-              for (int e = 0; e < 16; e += 8)
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + e),
-                             "r"(r[e]), "r"(r[e + 1]), "r"(r[e + 2]), "r"(r[e + 3]), "r"(r[e + 4]),
-                             "r"(r[e + 5]), "r"(r[e + 6]), "r"(r[e + 7])
-                             : "memory");
-            }
-            __syncwarp();
-            continue;
-          }
-          float v[16];
+        };
+        auto linear = [&](int col, const uint32_t (&r)[16], float (&v)[16]) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
           if (p.alpha != 1.f) {
@@ -598,31 +576,98 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
                 if (col + e < p.N) v[e] += E::to(b[e]);
             }
           }
-          auto pack = [&](uint4 (&o)[2]) {
-            typename E::T2* oh = reinterpret_cast<typename E::T2*>(o);
+        };
+        auto place = [&](int c, int w) {  // the lane's 16-byte chunk 2c + w of its row
+          return sbuf + (uint32_t)(lane * 128 + (((2 * c + w) ^ (lane & 7)) * 16));
+        };
+        auto pack = [&](const float (&v)[16], uint4 (&o)[2]) {
+          typename E::T2* oh = reinterpret_cast<typename E::T2*>(o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) oh[e] = E::pack(v[2 * e], v[2 * e + 1]);
-          };
-          if (p.U && lane < rows) {
+          for (int e = 0; e < 8; ++e) oh[e] = E::pack(v[2 * e], v[2 * e + 1]);
+        };
+        auto put = [&](int c, const uint4 (&o)[2]) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(c, w)), "r"(o[w].x),
+                         "r"(o[w].y), "r"(o[w].z), "r"(o[w].w)
+                         : "memory");
+        };
+        if (p.u_way == U_ROWS) {
+          // U through the staging buffer, ahead of the rest
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[16];
+            float v[16];
             uint4 o[2];
-            pack(o);
+            sums_of(c, r);
+            linear(gn + 16 * c, r, v);
+            pack(v, o);
+            put(c, o);
+            __syncwarp();
+          }
+          fu_rows_out(static_cast<T*>(p.U) + (int64_t)gm * p.ldu + gn, p.ldu, rows, cols, false, sbuf,
+                      lane);
+          __syncwarp();
+        }
+        if (p.mode != FUSED_NONE && !in_box)
+          fu_rows_in(static_cast<const T*>(p.in) + gy + (int64_t)gm * p.ld_in + gn, p.ld_in, rows, cols,
+                     sbuf, lane);
+        // Sixteen columns at a time.  (Not unrolled: the code that one call takes of all
+        // that is here then stays in the instruction cache; unrolled over 64 columns,
+        // steps that a call does not take slowed it as well: wgrad of 4000 rows of 8
+        // groups 140 us, 117 without the slope's code in the kernel.)
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = gn + 16 * c;
+          uint32_t r[16];
+          sums_of(c, r);
+          if (c == 3 && b + BOX_WARPS >= boxes) release_acc(buf);
+          if (p.splits > 1) {
+            // raw sums of the slice: 64 bytes of this lane's row of P (whose rows are whole)
+            if (lane < rows && col < p.ldp) {
+              float* const d = p.P + ((int64_t)u.slice * p.M + gm + lane) * p.ldp + col;
+#pragma unroll
+              for (int e = 0; e < 16; e += 8)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + e),
+                             "r"(r[e]), "r"(r[e + 1]), "r"(r[e + 2]), "r"(r[e + 3]), "r"(r[e + 4]),
+                             "r"(r[e + 5]), "r"(r[e + 6]), "r"(r[e + 7])
+                             : "memory");
+            }
+            __syncwarp();
+            continue;
+          }
+          float v[16];
+          linear(col, r, v);
+          uint4 o[2];
+          if ((p.u_way == U_SECTORS || p.u_way == U_HALVES) && lane < rows) {
+            pack(v, o);
             T* const dst = static_cast<T*>(p.U) + (int64_t)(gm + lane) * p.ldu + col;
-            if (p.vec_u && col + 15 < p.N) {
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
-                           "r"(o[0].x), "r"(o[0].y), "r"(o[0].z), "r"(o[0].w), "r"(o[1].x), "r"(o[1].y),
-                           "r"(o[1].z), "r"(o[1].w)
-                           : "memory");
-            } else {
+            if (col + 15 >= p.N) {
               const uint32_t* w = reinterpret_cast<const uint32_t*>(o);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if (col + e < p.N)
                   reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            } else if (p.u_way == U_SECTORS) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+                           "r"(o[0].x), "r"(o[0].y), "r"(o[0].z), "r"(o[0].w), "r"(o[1].x), "r"(o[1].y),
+                           "r"(o[1].z), "r"(o[1].w)
+                           : "memory");
+            } else {
+              reinterpret_cast<uint4*>(dst)[0] = o[0];
+              reinterpret_cast<uint4*>(dst)[1] = o[1];
             }
           }
           if (p.mode != FUSED_SLOPE) act_of<T>(v, p.act);
           if (p.mode != FUSED_NONE) {
-            const typename E::T2* c2 = reinterpret_cast<const typename E::T2*>(now);
+            uint4 in[2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(in[w].x), "=r"(in[w].y), "=r"(in[w].z), "=r"(in[w].w)
+                           : "r"(place(c, w))
+                           : "memory");
+            const typename E::T2* c2 = reinterpret_cast<const typename E::T2*>(in);
             float f[16];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -637,13 +682,8 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
               for (int e = 0; e < 16; ++e) v[e] = __fmaf_rn(p.beta, f[e], v[e]);
             }
           }
-          uint4 o[2];
-          pack(o);
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at[w]), "r"(o[w].x),
-                         "r"(o[w].y), "r"(o[w].z), "r"(o[w].w)
-                         : "memory");
+          pack(v, o);
+          put(c, o);
           if (p.part) {
             if (lane >= rows) {
 #pragma unroll
@@ -753,8 +793,12 @@ cudaError_t launch_fused_cfg(const FusedArgs& a, LaunchCtx& ctx) {
   p.Y = a.Y; p.ldy = a.ldy; p.stride_y = inner ? a.stride_y : 0;
   auto aligned = [](const void* q, int64_t ld) { return ((uintptr_t)q & 15u) == 0 && ld % 8 == 0; };
   p.tma_y = aligned(a.Y, a.ldy) && (!inner || a.groups == 1 || a.stride_y % 8 == 0);
-  p.tma_in = p.mode != FUSED_NONE && aligned(a.in, a.ld_in) && (!inner || p.tma_y);
-  p.vec_u = ((uintptr_t)a.U & 31u) == 0 && a.ldu % 16 == 0;
+  p.u_way = !a.U || a.splits > 1                                   ? U_NONE
+            : ((uintptr_t)a.U & 31u) == 0 && a.ldu % 16 == 0 ? U_SECTORS
+            : aligned(a.U, a.ldu)                            ? U_HALVES
+                                                             : U_ROWS;
+  // (U on its way through the staging buffer leaves no room for a box asked for ahead)
+  p.tma_in = p.mode != FUSED_NONE && aligned(a.in, a.ld_in) && (!inner || p.tma_y) && p.u_way != U_ROWS;
   p.part = a.part;
   p.status = ctx.status;
   p.timeout_ns = ctx.timeout_ns;
