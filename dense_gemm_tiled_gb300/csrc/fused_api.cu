@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "../../include/gemm.h"
+#include "fused_plan.h"
 #include "internal.h"
 
 using namespace gb300;
@@ -202,7 +203,7 @@ int run_call(Call& c, cudaStream_t stream) {
     const bool few = !inner && !a.transA && a.transB && a.M <= FUSED_FEW_ROWS &&
                      a.mode != FUSED_SLOPE && !c.dbias;
     a.splits = 1;
-    if (!few) fused_plan(a);
+    if (!few && !none) fused_plan(a);
     a.ldp = (a.N + 15) / 16 * 16;
     const int64_t bytes_p = a.splits > 1 ? pad256((int64_t)a.splits * a.M * a.ldp * 4) : 0;
     e = ws.get((size_t)(part_bytes + bytes_a + bytes_b + bytes_p), stream);

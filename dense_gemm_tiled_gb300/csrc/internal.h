@@ -369,7 +369,7 @@ struct FusedArgs {
 inline int64_t fused_part_floats(int64_t rows, int64_t groups, int64_t N) {
   return (rows / 32 + groups + 1) * N;
 }
-void fused_plan(FusedArgs& a);  // its tile and slices
+void fused_plan(FusedArgs& a);  // its tile and slices (fused_plan.h)
 // 16-bit operands with 16-byte aligned rows (A, B) on the tensor cores;
 // cudaErrorNotSupported (nothing launched) where a tensor map does not take them
 cudaError_t launch_fused(const FusedArgs& a, LaunchCtx& ctx);
