@@ -700,6 +700,9 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
         if (!p.tma_y || (p.kind == FUSED_ROWS && rows < 32)) {
           fu_rows_out(static_cast<T*>(p.Y) + gy + (int64_t)gm * p.ldy + gn, p.ldy, rows, cols, p.tma_y,
                       sbuf, lane);
+          // (the next tile's `in` comes into the buffer by TMA: after what was read and
+          // written here)
+          if (in_box) fence_proxy_async_smem();
           __syncwarp();
         } else {
           fence_proxy_async_smem();
