@@ -160,6 +160,14 @@ __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity,
   }
 }
 
+// Whole warp, after lane 0 alone has waited: whether it got what it waited for.  What the
+// wait made visible to lane 0 is so for every lane then (a shuffle orders no memory,
+// __syncwarp does).
+__device__ __forceinline__ bool warp_got(bool got) {
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

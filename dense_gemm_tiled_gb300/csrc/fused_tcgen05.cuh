@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
       }
       bool got = false;
       if (lane == 0) got = mbar_wait(accf_bar(buf), (uint32_t)(it >> 1) & 1u, wc);
-      got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+      got = warp_got(got);
       if (!got) break;
       tc_fence_after();
       if (hh >= boxes) {
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
             bulk_wait_read<0>();  // the last store has read the buffer
           }
         }
-        got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+        got = warp_got(got);
         if (!got) break;
         // sixteen columns' accumulators, and U in fp32
         auto sums_of = [&](int c, uint32_t (&r)[16]) {

@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = mbar_wait(cload_bar(ew * nbw + lb), (cph >> lb) & 1u, wc);
         if (ok) { cph ^= 1u << lb; cpend &= ~(1u << lb); }
       }
-      return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      return warp_got(ok);
     };
     int it = 0;
     bool dead = false;
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // warp-collective, so the whole warp must take the same branch
       bool got = false;
       if (lane == 0) got = mbar_wait(accf_bar(buf), acc_phase, wc);
-      got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+      got = warp_got(got);
       if (!got) break;
       tc_fence_after();
       const int gm = m0 + row;
@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (!ok) mbar_wait_drain(fix_bar(ew), fph, p.timeout_ns);
               fph ^= 1u;
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            ok = warp_got(ok);
             if (!ok) break;
             int sl = 0;
 #pragma unroll 1

@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
       const uint32_t acc_phase = (uint32_t)(it / NACC) & 1u;
       bool got = false;
       if (lane == 0) got = mbar_wait(accf_bar(buf), acc_phase, wc);
-      got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+      got = warp_got(got);
       if (!got) break;
       tc_fence_after();
       const int gn0 = n0 + hh * CW, gm0 = m0 + q * 32;

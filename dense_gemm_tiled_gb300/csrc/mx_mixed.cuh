@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const int q = warp & 3;
     bool got = false;
     if (lane == 0) got = mbar_wait(acc_bar, 0u, wc);
-    got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+    got = warp_got(got);
     if (got) {
       tc_fence_after();
       const uint32_t row = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       bool ok = false;
       if (lane == 0) ok = mbar_wait(free_bar(group), wphase, wc) && mbar_wait(code_bar(st), ph, wc);
       wphase ^= 1u;
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      ok = warp_got(ok);
       if (!ok) break;
       const uint32_t c = c_at(st), s = c + (uint32_t)CODE_BYTES;
       uint32_t codes[4][FMT == MX_INT8 ? 8 : 4];

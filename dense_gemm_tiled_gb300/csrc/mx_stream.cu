@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(ST_THREADS)
     for (int k = k_lo; k < k_hi; ++k) {
       bool ok = false;
       if (lane == 0) ok = mbar_wait(full_bar(stage), phase, wc);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      ok = warp_got(ok);
       if (!ok) break;
       const uint32_t w = base + (uint32_t)(stage * C_::STAGE), x = w + C_::W_BYTES;
       const uint32_t s = x + C_::X_BYTES, xs = s + C_::S_BYTES;

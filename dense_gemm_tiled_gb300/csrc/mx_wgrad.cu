@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(WG_THREADS)
       // (the codes' own barrier too: it is the scales' warp that has seen it)
       if (lane == 0)
         ok = mbar_wait(scale_bar(stage), phase, wc) && mbar_wait(full_bar(stage), phase, wc);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      ok = warp_got(ok);
       if (!ok) break;
       const uint32_t q = base + (uint32_t)(stage * C_::STAGE);
 #pragma unroll
