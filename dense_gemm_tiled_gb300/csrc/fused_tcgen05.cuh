@@ -75,7 +75,7 @@ struct FuParams {
   const int* offsets;  // groups + 1 (grouped kinds)
   int b_mask;          // 0: one matrix of B for all groups, else -1
   int tiles_m, tiles_n;
-  int64_t tiles;       // (not FUSED_ROWS)
+  int64_t tiles;       // (FUSED_ROWS: the most that ascending offsets can have)
   // slices of K (FUSED_DENSE): a unit is a tile's slice of k_slice columns, whose raw sums
   // go to P [splits][M][ldp]; 1: none
   int splits, k_slice;
@@ -125,6 +125,9 @@ struct FuWalk {
     u.slice = 0;
     if (p.kind == FUSED_ROWS) {
       int n;
+      // (offsets that do not ascend may hold the same rows many times over: no more tiles
+      // than ascending ones can have)
+      if (t >= p.tiles) return false;
       if (!rows.find(p.offsets, p.groups, p.M, p.tiles_n, t, lane, u.g, u.g_lo, n, loc)) return false;
       u.row_end = u.g_lo + n;
       rt = (n + BMT - 1) / BMT;
