@@ -145,8 +145,13 @@ int run_call(Call& c, cudaStream_t stream) {
     // 94 into aligned rows).
     float* P = static_cast<float*>(a.U ? a.U : a.Y);
     int64_t ldp = a.U ? a.ldu : a.ldy;
-    // (bias and activation alone: the product's own kernels apply them)
-    const bool plain = a.kind == FUSED_DENSE && !a.U && a.mode == FUSED_NONE && !c.dbias;
+    // (Bias and relu alone: the product's own kernels apply them.  Not gelu: theirs is another
+    // evaluation, and a layer's values would change when U is kept.  Its pass, us: 4096^3
+    // 1999 -> 2009, 1 x 5632 x 2048 73.2 -> 76.5, 1000 x 3001 x 777 116 -> 115.  The pass's form
+    // in the products' own epilogues doubled their code: 4096^3 2197, and gemm() itself at
+    // 1000 x 3001 x 777 110 -> 119.)
+    const bool plain = a.kind == FUSED_DENSE && !a.U && a.mode == FUSED_NONE && !c.dbias &&
+                       a.act != GEMM_ACT_GELU;
     // Slices of K are apart too; those of weights' gradients are finished as one matrix, so
     // only where the groups' follow one another.
     const int64_t p_rows = (int64_t)a.M * (inner ? a.groups : 1);

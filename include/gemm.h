@@ -355,8 +355,7 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
  *
  * dtype: GEMM_F32, GEMM_F16_F32ACC or GEMM_BF16_F32ACC, of every matrix and of bias.
  * bias: N elements, or NULL.  act: a gemm_act_t, applied to the fp32 value of U
- *   before its rounding.  GEMM_ACT_GELU as in gemm_mx_quantize(); in fp32 without U
- *   and R it is gemm_ex()'s.
+ *   before its rounding, as in gemm_mx_quantize() (relu of a NaN is 0).
  * R: M x N with ldr, or NULL; beta == 0 reads no R.  R may be Y itself with the same
  *   pitch.
  * U: M x N with ldu, stored rounded to dtype; or NULL.
