@@ -408,6 +408,7 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
                        p.kind == FUSED_INNER ? kz : u.g & p.b_mask, bar);
               }
             } else {
+              // (the odd block's box may lie wholly past the last column: zeros)
               load(sb, &tmB, u.k_lo + k0, u.n0 + rank * (BN / 2), u.g & p.b_mask, bar);
             }
           }

@@ -375,10 +375,12 @@ void fused_plan(FusedArgs& a);  // its tile and slices (fused_plan.h)
 cudaError_t launch_fused(const FusedArgs& a, LaunchCtx& ctx);
 cudaError_t launch_fused_bf16(const FusedArgs& a, LaunchCtx& ctx);
 // forward products of up to FUSED_FEW_ROWS rows in all (operands as above, B stored by
-// rows of K): every matrix whose group has rows read once.  In a graph, us, against the
-// tensor-core kernel: 5632 x 2048 8 rows 9.3 / 13, 16 rows 11.0 / 12.0; 2048 x 5632 8 rows
-// 8.9 / 13.9; 8192 x 8192 8 rows 27.9 / 30.2, 16 rows 32.1 / 30.2; 1408 x 2048 of 64 groups,
-// 16 rows in 16 of them 19.8 / 27, 32 rows in 24 31.1 / 28.5.
+// rows of K): every matrix whose group has rows read once (where B had to be copied into
+// aligned rows, the copy reads all of them).  In a graph, us, against the tensor-core
+// kernel: 5632 x 2048 8 rows 9.3 / 13, 16 rows 11.0 / 12.0; 2048 x 5632 8 rows 8.9 / 13.9;
+// 8192 x 8192 8 rows 27.9 / 30.2; 1408 x 2048 of 64 groups, 16 rows in 16 of them 19.8 / 27.
+// Sixteen rows are the end of it: a large single matrix is already slower (8192 x 8192
+// 32.1 / 30.2), experts are not; with 32 rows in 24 of 64 groups they are too (31.1 / 28.5).
 constexpr int FUSED_FEW_ROWS = 16;
 cudaError_t launch_fused_stream(const FusedArgs& a, LaunchCtx& ctx);
 // dbias[g][j] = the sum of group g's slots of `part`

@@ -359,9 +359,12 @@ int gemm_mx(int format, int transA, int transB, int64_t M, int64_t N, int64_t K,
  * R: M x N with ldr, or NULL; beta == 0 reads no R.  R may be Y itself with the same
  *   pitch.
  * U: M x N with ldu, stored rounded to dtype; or NULL.
- * M, N and K up to 2^31 - 2^18 (else GEMM_ERR_UNSUPPORTED).  Outputs may overlap no
- * input but as said (GEMM_ERR_ALIAS).  K == 0: the product is zero.  16-bit operands
- * whose rows are not 16-byte aligned are copied to scratch in stream order.
+ * M, N and K up to 2^31 - 2^18 (else GEMM_ERR_UNSUPPORTED).  Outputs may overlap one
+ * another not at all and inputs only as said (GEMM_ERR_ALIAS; checked over whole extents,
+ * so U and Y that interleave within one wider matrix are refused).  K == 0: the product
+ * is zero.  16-bit operands whose rows are not 16-byte aligned are copied to scratch in
+ * stream order, on each call (of grouped products all matrices of B, also those whose
+ * groups have no rows).
  */
 int gemm_fused(int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype, float alpha,
                const void* A, int64_t lda, const void* B, int64_t ldb, const void* bias, int act,
@@ -378,7 +381,9 @@ int gemm_fused(int transA, int transB, int64_t M, int64_t N, int64_t K, int dtyp
  *   be NULL).  act': relu 1 where U > 0, else dX is 0; gelu Phi(U) + U phi(U).
  * dX: M x N with lddx; may be U itself with the same pitch.
  * dbias: N fp32 sums of dX before its rounding (in an order that does not change from
- *   call to call), or NULL.  M == 0 sets them to zero.
+ *   call to call), or NULL.  M == 0 sets them to zero.  With 16-bit operands dX's values
+ *   are the tensor cores' sums over K, whose additions are cut rather than rounded: at K =
+ *   2048 dbias is 2 10^-6 off in norm (fp32: 4 to 8 10^-7).
  */
 int gemm_fused_backward(int transA, int transB, int64_t M, int64_t N, int64_t K, int dtype,
                         float alpha, const void* A, int64_t lda, const void* B, int64_t ldb, int act,
