@@ -455,8 +455,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
-// Tiled store of the shared-memory box at `src` to (x, y, z), clipped to the
-// tensor's extent in each dimension, in this thread's bulk group.
+// Tiled store of the shared-memory box at `src` to (x, y, z), in this thread's bulk
+// group, clipped to the tensor's extent: in y and z exactly, in x to 16 bytes (a row of
+// 257 16-bit elements is stored up to its 264th).  So only where a row's bytes are a
+// multiple of 16, or what follows it up to one is free to be written.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int32_t x, int32_t y,
                                              int32_t z, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),

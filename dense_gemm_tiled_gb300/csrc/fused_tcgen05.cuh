@@ -700,8 +700,9 @@ __global__ void __launch_bounds__(fu_threads(W), 1)
           __syncwarp();  // (the tensor-memory loads are the warp's together)
         }
         if (p.splits > 1) continue;
-        // a box that the group's end cuts is stored row by row, as are rows off alignment
-        if (!p.tma_y || (p.kind == FUSED_ROWS && rows < 32)) {
+        // a box that the group's end cuts is stored row by row, as are rows off alignment and
+        // a last box that ends within 16 bytes (tma_store_3d would fill those)
+        if (!p.tma_y || cols % 8 != 0 || (p.kind == FUSED_ROWS && rows < 32)) {
           fu_rows_out(static_cast<T*>(p.Y) + gy + (int64_t)gm * p.ldy + gn, p.ldy, rows, cols, p.tma_y,
                       sbuf, lane);
           // (the next tile's `in` comes into the buffer by TMA: after what was read and
