@@ -245,7 +245,7 @@ int pair_enabled() {
 int c_tma_enabled() {
   static const int v = [] {
     const char* e = getenv("GEMM_GB300_HG_CTMA");
-    return e ? atoi(e) : 1;
+    return e && atoi(e) == 0 ? 0 : 1;
   }();
   return v;
 }
@@ -487,7 +487,7 @@ int run_gemm(int transA, int transB, int64_t M64, int64_t N64, int64_t K64, int 
     }
     if (e == cudaSuccess) {
       HgemmArgs a{0, 1, M, N, K, Ad, ldad, Bd, ldbd, Cd, ldcd, alpha, beta, sms, bn,
-                  c_tma_enabled(), g_fault_injection.load()};
+                  c_scr ? C_TMA_PADDED : c_tma_enabled(), g_fault_injection.load()};
       a.dtype = GEMM_F32_TF32;
       a.plan = pl;
       a.sk_ws = sk_ws;
@@ -636,7 +636,7 @@ int run_gemm(int transA, int transB, int64_t M64, int64_t N64, int64_t K64, int 
     }
     if (e == cudaSuccess) {
       HgemmArgs a{transA, transB, M, N, K, Ad, ldad, Bd, ldbd, Cd, ldcd, alpha, beta, sms, bn,
-                  c_tma_enabled(), g_fault_injection.load()};
+                  c_scr ? C_TMA_PADDED : c_tma_enabled(), g_fault_injection.load()};
       a.dtype = dtype;
       a.plan = pl;
       a.sk_ws = sk_ws;

@@ -1351,7 +1351,9 @@ cudaError_t launch_hgemm_t(const HgemmArgs& a, LaunchCtx& ctx) {
   constexpr int VEC = 16 / (int)sizeof(T);  // elements per 16 bytes
   p.c_vec_ok = ((reinterpret_cast<uintptr_t>(a.C) & 15u) == 0 && (a.ldc % VEC) == 0 &&
                 (a.batch <= 1 || (a.stride_c % VEC) == 0)) ? 1 : 0;
-  p.c_tma = (p.c_vec_ok && a.c_tma && bn >= (sizeof(T) == 4 ? 32 : 64)) ? 1 : 0;
+  // (a TMA store fills a row's last 16 bytes: see tma_store_3d)
+  const bool whole_rows = a.N % VEC == 0 || a.c_tma == C_TMA_PADDED;
+  p.c_tma = (p.c_vec_ok && a.c_tma && whole_rows && bn >= (sizeof(T) == 4 ? 32 : 64)) ? 1 : 0;
   p.pair = pl.pair;
   p.batch = a.batch > 1 ? a.batch : 1;
   p.stride_c = p.batch > 1 ? a.stride_c : 0;

@@ -73,6 +73,7 @@ struct HPlan {
 };
 
 // One tcgen05 GEMM launch (fp16, bf16, or fp32 on TF32 MMAs).
+constexpr int C_TMA_PADDED = 2;
 struct HgemmArgs {
   int transA, transB;
   int M, N, K;
@@ -85,7 +86,8 @@ struct HgemmArgs {
   float alpha, beta;
   int num_sms;
   int bn;               // tile width: 32, 64, 128, 192 or 256
-  int c_tma;            // allow TMA stores (and, beta != 0, TMA loads) of C when C is aligned
+  int c_tma;            // allow TMA stores (and, beta != 0, TMA loads) of C when C is aligned;
+                        // C_TMA_PADDED: also where they fill a row's last 16 bytes past N
   int fault_injection;  // test hook: 1 = producer skips its first stage
   int dtype = 1;        // 1 fp16, 2 bf16, 3 fp32 on TF32 MMAs (gemm_dtype_t)
   // 3xTF32 (fp32 operands only): A and B are two planes each, hi and lo, a

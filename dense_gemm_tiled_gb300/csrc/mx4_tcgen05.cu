@@ -510,7 +510,7 @@ cudaError_t launch_mx4_cfg(const Mx4Args& a, LaunchCtx& ctx) {
   p.c_vec_ok = ((uintptr_t)a.C & 15u) == 0 && (a.ldc % VEC) == 0;
   p.batch = 1;
   p.ep = a.ep;
-  p.c_tma = p.c_vec_ok;
+  p.c_tma = p.c_vec_ok && a.N % VEC == 0;  // (see tma_store_3d)
   mp.s_tiles = (int)mx_scale_tiles(FMT, a.K);
   mp.stages_k = (a.K + KSTAGE - 1) / KSTAGE;
   const int64_t kbytes = ((int64_t)a.K + 1) / 2;
