@@ -654,7 +654,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // staging buffers of this warp (the block's 4 KiB buffers split over the
     // warps in use)
     const int nbw = (C_::STAGING_BYTES / 4096) / (4 * nh);
-    auto wait_staging = [&]() {  // this warp's oldest store has read its buffer
+    // this warp's oldest store has read its buffer: of the boxes before, which take the
+    // buffers in turn and are a group each, at most the last one's is still read
+    auto wait_staging = [&]() {
       if (lane == 0) {
         if (nbw >= 2) bulk_wait_read<1>();
         else bulk_wait_read<0>();
@@ -942,7 +944,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (c == c_hi - 1) release_acc(buf);
             const int gn0 = n0 + c * 32;
             const uint32_t sbuf = staging_addr + (uint32_t)((ew * nbw + box_buf(c)) * 4096);
-            if (CIN) {
+            const bool here = c_rows && gn0 < p.N;
+            if (CIN && here) {
               if (!c_wait(box_buf(c))) { dead = true; break; }
             } else {
               wait_staging();
@@ -970,9 +973,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && c_rows && gn0 < p.N) {
-              tma_store_3d(&tmC, gn0, m0 + q * 32, bz, sbuf);
-              bulk_commit();
+            if (lane == 0) {
+              if (here) tma_store_3d(&tmC, gn0, m0 + q * 32, bz, sbuf);
+              bulk_commit();  // (also of nothing: wait_staging counts a group a box)
             }
           }
         };
@@ -1007,7 +1010,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (g == g_hi - 1) release_acc(buf);
             const int gn0 = n0 + c * 32;
             const uint32_t sbuf = staging_addr + (uint32_t)((ew * nbw + box_buf(g)) * 4096);
-            if (CIN) {
+            const bool here = c_rows && gn0 < p.N;
+            if (CIN && here) {
               if (!c_wait(box_buf(g))) { dead = true; break; }
             } else {
               wait_staging();
@@ -1056,9 +1060,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             // (a block wholly past M or N -- the second tile of a pair on an odd
             // tile-row count -- is not stored at all)
-            if (lane == 0 && c_rows && gn0 < p.N) {
-              tma_store_3d(&tmC, gn0, m0 + q * 32, bz, sbuf);
-              bulk_commit();
+            if (lane == 0) {
+              if (here) tma_store_3d(&tmC, gn0, m0 + q * 32, bz, sbuf);
+              bulk_commit();  // (also of nothing: wait_staging counts a group a box)
             }
           }
         };

@@ -27,3 +27,18 @@ def test_the_answer():
     body = text[text.index("bool warp_got(bool got) {"):]
     body = body[: body.index("}")]
     assert body.index("__syncwarp();") < body.index("__shfl_sync(")
+
+
+def test_every_box_is_a_group():
+    """The 16-bit kernel's boxes take staging buffers in turn and wait until at most one
+    group is still read: a box that is not stored (past M or N) counts as one too, and
+    waits like the others before it writes its buffer."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "hgemm_tcgen05.cuh")).read())
+    stores = list(re.finditer(r"tma_store_3d\([^;]*;", text))
+    assert len(stores) == 2
+    for m in stores:
+        before, after = text[: m.start()], text[m.end():]
+        assert re.search(r"if \(lane == 0\) \{\s*if \(here\) $", before), before[-120:]
+        assert re.match(r"\s*bulk_commit\(\);\s*\}", after), after[:80]
+        wait = before[before.rindex("const bool here"):]
+        assert re.search(r"if \(CIN && here\) \{[^}]*c_wait[^}]*\}[^}]*\} else \{\s*wait_staging\(\);", wait)
