@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // in flight, the 32 x 64 16-bit block packed into this warp's staging
         // buffer in the 128-byte swizzle (16-byte chunk w of row l at chunk
         // w ^ (l & 7): the 8 lanes of each store phase hit distinct banks),
-        // then one TMA store clipped by the unit at M and N
+        // then one TMA store clipped by the unit at M and at N (whole 16-byte units: c_tma)
         // (two copies of the loop: with C loads (beta != 0) and without)
         auto boxes = [&](auto cin_tag) {
           constexpr bool CIN = decltype(cin_tag)::value;
